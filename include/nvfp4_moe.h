@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define NVFP4_MOE_ABI_VERSION 9
+#define NVFP4_MOE_ABI_VERSION 10
 
 /* Status codes. */
 #define NVFP4_OK 0
@@ -173,6 +173,54 @@ int nvfp4_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld
  * the usual reading.  1 <= topk <= min(E, 32), E <= 1024. */
 int moe_route_topk(const float* logits, int32_t T, int32_t E, int32_t topk, int32_t* ids,
                    float* weights, void* stream);
+
+/* The router's product: logits float32 [T][E] = x wg^T (+ bias), the logits
+ * that moe_route_topk and moe_route choose from.  x bfloat16 [T][ldx] (the
+ * first H of each row used), wg [E][H] in w_dtype (NVFP4_BF16 or NVFP4_F32:
+ * routers stay unquantised), bias float32 [E] or NULL.  Products are exact
+ * (float32 weights enter as three bfloat16 parts, 24 significant bits, parts
+ * below 2^-126 excepted), sums FP32.  1 <= E <= 1024; H and ldx multiples of
+ * 8; x and wg 16-byte aligned. */
+int moe_gate(const uint16_t* x, int64_t ldx, const void* wg, int w_dtype, const float* bias, int32_t T, int32_t E,
+             int32_t H, float* logits, void* stream);
+
+/* Parameters of moe_route (host struct). */
+#define NVFP4_SCORE_SOFTMAX 0 /* p = softmax of a token's logits            */
+#define NVFP4_SCORE_SIGMOID 1 /* p = 1 / (1 + e^-z), expert by expert       */
+#define NVFP4_GROUP_MAX 0     /* value of a group: its largest choice value */
+#define NVFP4_GROUP_TOP2 1    /* the sum of its two largest (its only one)  */
+typedef struct nvfp4_route_params {
+  int32_t score;
+  int32_t groups;       /* 1..64, divides E: groups of E / groups consecutive experts */
+  int32_t topk_groups;  /* 1..groups */
+  int32_t group_score;
+  int32_t renormalize;  /* 1: divide the chosen scores by their sum */
+  float scale;          /* factor of every weight, positive */
+} nvfp4_route_params;
+
+/* Choice of experts from scores, with a selection bias and expert groups.
+ * For every token, with logits z [E] (float32 or bfloat16 in dtype, rows ldl
+ * elements apart):
+ *   p_e = softmax(z)_e or 1 / (1 + e^-z_e)
+ *   c_e = p_e + bias_e  (bias float32 [E], a load-balancing correction that
+ *         moves the choice and not the weights); without a bias the experts
+ *         are in the order of z
+ *   groups > 1: v_g = the largest p or c of group g (or the sum of its two
+ *         largest); only the topk_groups groups of largest v (equal: lower
+ *         index first) are chosen from
+ *   ids [T][topk]: the largest c in decreasing order, equal ones by lower id
+ *   weights float32 [T][topk]: p of the chosen (without the bias), divided by
+ *         their sum with renormalize (0 if that sum is 0), times scale
+ * Scores, choice values and weights are evaluated in FP64 and the weights
+ * rounded once; the softmax weights without a bias or groups are those of
+ * moe_route_topk, bit for bit.  An expert whose logit or bias is NaN or
+ * -infinity is not available: it has score 0 and is never chosen; +infinity
+ * counts as the largest finite float.  Where a token has fewer available
+ * experts than topk, the remaining ids are -1 (dropped by moe_align) with
+ * weight 0.  1 <= topk <= min(E, 32), topk <= E / groups * topk_groups,
+ * E <= 1024. */
+int moe_route(const nvfp4_route_params* params, const void* logits, int dtype, int64_t ldl, const float* bias,
+              int32_t T, int32_t E, int32_t topk, int32_t* ids, float* weights, void* stream);
 
 /* Router and permutation in one call: the same results, bit for bit, as
  * moe_route_topk(logits, T, E, topk, topk_ids, topk_w) followed by

@@ -13,7 +13,7 @@ from ctypes import c_char_p, c_int, c_int32, c_int64, c_size_t, c_void_p
 # variant with different tile settings); the default is the in-tree build.
 LIB_PATH = os.environ.get("NVFP4_MOE_LIB") or os.path.join(
     os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
-ABI_VERSION = 9
+ABI_VERSION = 10
 
 NVFP4_OK = 0
 NVFP4_EINVAL = -1
@@ -32,7 +32,13 @@ class Dims(ctypes.Structure):
         return "Dims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
+class RouteParams(ctypes.Structure):
+    _fields_ = [("score", c_int32), ("groups", c_int32), ("topk_groups", c_int32),
+                ("group_score", c_int32), ("renormalize", c_int32), ("scale", ctypes.c_float)]
+
+
 _P = ctypes.POINTER(Dims)
+_R = ctypes.POINTER(RouteParams)
 
 # name -> (restype, argtypes); every symbol include/nvfp4_moe.h declares.
 SIGNATURES = {
@@ -50,6 +56,10 @@ SIGNATURES = {
                           c_void_p]),
     "moe_scale_and_align": (c_int, [_P, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p,
                                     c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_gate": (c_int, [c_void_p, c_int64, c_void_p, c_int, c_void_p, c_int32, c_int32, c_int32,
+                         c_void_p, c_void_p]),
+    "moe_route": (c_int, [_R, c_void_p, c_int, c_int64, c_void_p, c_int32, c_int32, c_int32, c_void_p,
+                          c_void_p, c_void_p]),
     "moe_route_and_align": (c_int, [_P, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                     c_void_p, c_void_p, c_size_t, c_void_p]),
     "moe_quantize_and_align": (c_int, [_P, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p,

@@ -5,6 +5,7 @@
 // the workspace size for the GEMMs, like the grouped-GEMM initialisation error
 // of vLLM PR #29242, review of nvfp4_blockwise_moe_kernel.cu).
 #include <algorithm>
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -125,6 +126,60 @@ int moe_route_topk(const float* logits, int32_t T, int32_t E, int32_t topk, int3
   if (T == 0) return ok();
   if (!logits || !ids || !weights) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
   return launched(nvfp4::launch_route_topk(logits, T, E, topk, ids, weights, S(stream)), W);
+}
+
+int moe_gate(const uint16_t* x, int64_t ldx, const void* wg, int w_dtype, const float* bias, int32_t T, int32_t E,
+             int32_t H, float* logits, void* stream) {
+  const char* W = "moe_gate";
+  if (w_dtype != NVFP4_BF16 && w_dtype != NVFP4_F32) return fail(NVFP4_EINVAL, "%s: EINVAL w_dtype=%d", W, w_dtype);
+  if (T < 0 || E < 1 || E > 1024 || H < 8 || H % 8 || ldx < H || ldx % 8)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE T=%d num_experts=%d H=%d ldx=%lld (1 <= E <= 1024, H and ldx multiples of 8)",
+                W, T, E, H, (long long)ldx);
+  if (T == 0) return ok();
+  if (!x || !wg || !logits) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
+  if (!aligned(x, 16) || !aligned(wg, 16) || !aligned(bias, 4) || !aligned(logits, 4))
+    return fail(NVFP4_EINVAL, "%s: EINVAL misaligned pointer (x and wg 16 B, bias and logits 4 B)", W);
+  return launched(nvfp4::launch_gate(x, ldx, wg, w_dtype == NVFP4_F32, bias, T, E, H, logits, S(stream)), W);
+}
+
+int moe_route(const nvfp4_route_params* p, const void* logits, int dtype, int64_t ldl, const float* bias, int32_t T,
+              int32_t E, int32_t topk, int32_t* ids, float* weights, void* stream) {
+  const char* W = "moe_route";
+  if (!p) return fail(NVFP4_EINVAL, "%s: EINVAL params is NULL", W);
+  if (dtype != NVFP4_BF16 && dtype != NVFP4_F32) return fail(NVFP4_EINVAL, "%s: EINVAL dtype=%d", W, dtype);
+  if ((p->score != NVFP4_SCORE_SOFTMAX && p->score != NVFP4_SCORE_SIGMOID) ||
+      (p->group_score != NVFP4_GROUP_MAX && p->group_score != NVFP4_GROUP_TOP2) ||
+      (p->renormalize != 0 && p->renormalize != 1))
+    return fail(NVFP4_EINVAL, "%s: EINVAL score=%d group_score=%d renormalize=%d", W, p->score, p->group_score,
+                p->renormalize);
+  if (!(p->scale > 0.0f && p->scale < INFINITY))
+    return fail(NVFP4_EINVAL, "%s: EINVAL scale=%g (positive and finite)", W, (double)p->scale);
+  if (T < 0 || E < 1 || E > 1024 || topk < 1 || topk > E || topk > 32 || ldl < E)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE T=%d num_experts=%d topk=%d ldl=%lld (1 <= topk <= min(E, 32), E <= 1024)",
+                W, T, E, topk, (long long)ldl);
+  if (p->groups < 1 || p->groups > 64 || E % p->groups || p->topk_groups < 1 || p->topk_groups > p->groups ||
+      topk > E / p->groups * p->topk_groups)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE num_experts=%d topk=%d groups=%d topk_groups=%d (groups <= 64 divide the "
+                "experts, topk_groups of them hold topk)", W, E, topk, p->groups, p->topk_groups);
+  if (T == 0) return ok();
+  if (!logits || !ids || !weights) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
+  if (!aligned(logits, dtype == NVFP4_BF16 ? 2 : 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return fail(NVFP4_EINVAL, "%s: EINVAL misaligned pointer", W);
+  nvfp4::RouteArgs a{};
+  a.T = T;
+  a.E = E;
+  a.k = topk;
+  a.ldl = ldl;
+  a.score = p->score;
+  a.groups = p->groups;
+  a.topk_groups = p->topk_groups;
+  a.group_top2 = p->group_score == NVFP4_GROUP_TOP2;
+  a.renormalize = p->renormalize;
+  a.scale = p->scale;
+  a.bias = bias;
+  a.ids = ids;
+  a.weights = weights;
+  return launched(nvfp4::launch_route(logits, dtype == NVFP4_BF16, a, S(stream)), W);
 }
 
 // ------------------------------------------------------------------ align

@@ -39,6 +39,26 @@ hipError_t launch_quantize(const void* x, int dtype, int64_t rows, int64_t K, in
 hipError_t launch_route_topk(const float* logits, int T, int E, int k, int32_t* ids, float* w,
                              hipStream_t s);
 
+// The router's product: x bf16 [T][ldx], wg [E][H] (bf16, or float32 with
+// w_f32), bias [E] or null -> logits f32 [T][E].
+hipError_t launch_gate(const uint16_t* x, int64_t ldx, const void* wg, bool w_f32, const float* bias, int T, int E,
+                       int H, float* logits, hipStream_t s);
+
+// The choice of experts (moe_route; logits f32 or bf16, row stride ldl).
+struct RouteArgs {
+  int T, E, k;
+  int64_t ldl;
+  int score;        // 0 softmax, 1 sigmoid
+  int groups, topk_groups;
+  int group_top2;   // value of a group: 0 its largest choice value, 1 the sum of its two largest
+  int renormalize;
+  float scale;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+};
+hipError_t launch_route(const void* logits, bool bf16, const RouteArgs& a, hipStream_t s);
+
 struct AlignShape {
   int T, topk, E, shared, H;
   int64_t P;        // pairs

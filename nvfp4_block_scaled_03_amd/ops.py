@@ -5,14 +5,16 @@ current stream.  Names follow include/nvfp4_moe.h.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
+import functools
 from typing import Optional
 
 import torch
 
 from . import _lib
-from ._lib import NVFP4_BF16, NVFP4_F32, Dims, call
+from ._lib import NVFP4_BF16, NVFP4_F32, Dims, RouteParams, call
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -35,6 +37,26 @@ def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
             raise ValueError("tensors must live on the GPU")
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _device_of(t: torch.Tensor, *others):
+    """Checks that the tensors (None among them) share one GPU; a context in
+    which that GPU is the current device, so that the call runs on its
+    current stream."""
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"tensors on {t.device} and {o.device}")
+    return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _need(cond: bool, what: str):
+    if not cond:
+        raise ValueError(what)
 
 
 def dims(T: int, topk: int, E: int, H: int, I: int, shared: int = 0) -> Dims:
@@ -84,6 +106,73 @@ def route_topk(logits: torch.Tensor, k: int):
     w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
     call("moe_route_topk", _p(logits), T, E, k, _p(ids), _p(w), _stream())
     return ids, w
+
+
+def gate_logits(x: torch.Tensor, wg: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The router's product: float32 logits [T, E] = x wg^T (+ bias), x bf16
+    [T, H], wg [E, H] bf16 or float32, bias float32 [E]."""
+    with _device_of(x, wg, bias, out):
+        _need(x.dim() == 2 and wg.dim() == 2 and wg.shape[1] == x.shape[1], "x [T, H] and wg [E, H]")
+        _need(x.dtype == torch.bfloat16, "x must be bfloat16")
+        T, H = x.shape
+        E = wg.shape[0]
+        if x.stride(1) != 1 or x.stride(0) % 8 or x.stride(0) < H or x.data_ptr() % 16:
+            x = x.contiguous() if not x.is_contiguous() else x.clone()
+        wg = wg.contiguous()
+        if bias is not None:
+            _need(bias.shape == (E,) and bias.dtype == torch.float32, "bias must be float32 [E]")
+            bias = bias.contiguous()
+        if out is None:
+            out = torch.empty(T, E, dtype=torch.float32, device=x.device)
+        _need(out.shape == (T, E) and out.dtype == torch.float32 and out.is_contiguous(),
+              "out must be contiguous float32 [T, E]")
+        call("moe_gate", _p(x), x.stride(0), _p(wg), _dtype_code(wg), _p(bias), T, E, H, _p(out), _stream())
+    return out
+
+
+@functools.lru_cache(maxsize=64)
+def _route_params(score, groups, topk_groups, group_score, renormalize, scale) -> RouteParams:
+    _need(score in ROUTE_SCORES, f"score must be one of {sorted(ROUTE_SCORES)}")
+    _need(group_score in GROUP_SCORES, f"group_score must be one of {sorted(GROUP_SCORES)}")
+    return RouteParams(ROUTE_SCORES[score], groups, topk_groups, GROUP_SCORES[group_score], int(renormalize), scale)
+
+
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
+
+
+def route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+                 groups: int = 1, topk_groups: int = 1, group_score: str = "max", renormalize: bool = True,
+                 scale: float = 1.0, ids: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None):
+    """Choice of k experts per token from logits [T, E] (float32 or bf16):
+    (ids int32 [T, k], weights float32 [T, k]).  ``score``: "softmax" or
+    "sigmoid"; ``bias`` (float32 [E]) moves the choice and not the weights;
+    the experts are chosen from the ``topk_groups`` best of ``groups`` groups,
+    valued by their largest score ("max") or the sum of their two largest
+    ("top2"); the weights are the scores of the chosen, divided by their sum
+    with ``renormalize``, times ``scale``.  Experts with a logit or bias of
+    -inf or NaN are not available; ids that no expert fills are -1."""
+    params = _route_params(score, groups, topk_groups, group_score, renormalize, scale)
+    with _device_of(logits, bias, ids, weights):
+        _need(logits.dim() == 2, "logits [T, E]")
+        T, E = logits.shape
+        if logits.stride(1) != 1 or logits.stride(0) < E:
+            logits = logits.contiguous()
+        if bias is not None:
+            _need(bias.shape == (E,) and bias.dtype == torch.float32, "bias must be float32 [E]")
+            bias = bias.contiguous()
+        if ids is None:
+            ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+        if weights is None:
+            weights = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+        _need(ids.shape == (T, k) and ids.dtype == torch.int32 and ids.is_contiguous(),
+              "ids must be contiguous int32 [T, k]")
+        _need(weights.shape == (T, k) and weights.dtype == torch.float32 and weights.is_contiguous(),
+              "weights must be contiguous float32 [T, k]")
+        call("moe_route", ctypes.byref(params), _p(logits), _dtype_code(logits), max(logits.stride(0), E), _p(bias),
+             T, E, k, _p(ids), _p(weights), _stream())
+    return ids, weights
 
 
 @dataclasses.dataclass

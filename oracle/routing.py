@@ -63,3 +63,71 @@ def route_two_step(logits, k: int) -> tuple[np.ndarray, np.ndarray]:
     ids = np.argsort(-z, axis=1, kind="stable")[:, :k]
     sel = np.take_along_axis(p, ids, axis=1)
     return ids.astype(np.int32), (sel / sel.sum(axis=1, keepdims=True))
+
+
+def gate_logits(x, wg, bias=None) -> np.ndarray:
+    """FP64 logits [T, E] = x wg^T (+ bias) of x [T, H] and wg [E, H]."""
+    z = np.asarray(x, dtype=np.float64) @ np.asarray(wg, dtype=np.float64).T
+    return z if bias is None else z + np.asarray(bias, dtype=np.float64)
+
+
+def route_scored(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+                 group_score: str = "max", renormalize: bool = True, scale: float = 1.0):
+    """Choice of experts with scores, a selection bias and expert groups:
+    (ids int32 [T, k], FP64 weights [T, k]), token by token in FP64.
+
+    An expert is available unless its logit or bias is NaN or -inf (+inf is
+    the largest finite float).  Scores p are over the available experts; the
+    choice values are p + bias, or the logits themselves without a bias (the
+    same order); of ``groups`` groups of consecutive experts the
+    ``topk_groups`` with the largest value (largest score or sum of the two
+    largest, of p or p + bias) remain; the k largest choice values of those
+    are chosen, equal values by lower index throughout.  Missing experts:
+    id -1, weight 0.
+    """
+    z = np.asarray(logits).astype(np.float64)
+    T, E = z.shape
+    top = float(np.finfo(np.float32).max)
+    z = np.minimum(np.where(np.isnan(z), -np.inf, z), top)
+    b = None if bias is None else np.minimum(np.where(np.isnan(bias), -np.inf, np.asarray(bias, dtype=np.float64)), top)
+    ids = np.full((T, k), -1, dtype=np.int32)
+    weights = np.zeros((T, k))
+    per = E // groups
+    for t in range(T):
+        on = z[t] > -np.inf
+        if b is not None:
+            on &= b > -np.inf
+        p = np.zeros(E)
+        live = z[t] > -np.inf   # a bias keeps an expert from being chosen, not from the softmax
+        if score == "softmax":
+            if live.any():
+                p[live] = np.exp(z[t][live] - z[t][live].max())
+                p /= p.sum()
+        else:
+            with np.errstate(over="ignore"):
+                p[live] = 1.0 / (1.0 + np.exp(-z[t][live]))
+        valued = np.where(on, p if b is None else p + np.where(on, b, 0.0), -np.inf)
+        order_by = valued if b is not None else np.where(on, z[t], -np.inf)
+        if groups > 1:
+            best = -np.sort(-valued.reshape(groups, per), axis=1)
+            v = best[:, 0].copy()
+            if group_score == "top2" and per > 1:
+                two = best[:, 1] > -np.inf
+                v[two] += best[two, 1]
+            keep = np.argsort(-v, kind="stable")[:topk_groups]
+            order_by = np.where(np.isin(np.arange(E) // per, keep), order_by, -np.inf)
+        chosen = [e for e in np.argsort(-order_by, kind="stable")[:k] if order_by[e] > -np.inf]
+        ids[t, :len(chosen)] = chosen
+        if not chosen:
+            continue
+        if renormalize and score == "softmax":   # the full softmax's denominator cancels
+            w = np.exp(z[t][chosen] - z[t][chosen].max())
+        else:
+            w = p[chosen]
+        if renormalize:
+            s = 0.0
+            for v in w:
+                s += v
+            w = w / s if s > 0 else np.zeros_like(w)
+        weights[t, :len(chosen)] = w * scale
+    return ids, weights

@@ -280,3 +280,42 @@ def test_parts_query_and_errors(lib):
     assert "grouped_gemm2_combine_part: EWORKSPACE" in _lib.last_error()
     assert lib.grouped_gemm1_swiglu_part(r, *([None] * 13), 2, None) == _lib.NVFP4_EINVAL
     assert "grouped_gemm1_swiglu_part: EINVAL null" in _lib.last_error()
+
+
+def _route(**kw):
+    return _lib.RouteParams(*[{**dict(score=0, groups=1, topk_groups=1, group_score=0, renormalize=1, scale=1.0),
+                               **kw}[n] for n in ("score", "groups", "topk_groups", "group_score", "renormalize",
+                                                  "scale")])
+
+
+def test_router_errors(lib):
+    """moe_gate and moe_route check everything before a launch: enums, sizes,
+    strides, groups, pointers and their alignment; T == 0 is a no-op."""
+    p = ctypes.c_void_p(256)
+    off = ctypes.c_void_p(256 + 8)
+    assert lib.moe_gate(None, 64, None, 0, None, 0, 8, 64, None, None) == _lib.NVFP4_OK
+    assert lib.moe_gate(p, 64, p, 2, None, 4, 8, 64, p, None) == _lib.NVFP4_EINVAL
+    for T, E, H, ldx in ((-1, 8, 64, 64), (4, 0, 64, 64), (4, 1025, 64, 64), (4, 8, 60, 64), (4, 8, 64, 56),
+                         (4, 8, 64, 68), (4, 8, 0, 64)):
+        assert lib.moe_gate(p, ldx, p, 0, None, T, E, H, p, None) == _lib.NVFP4_ESHAPE, (T, E, H, ldx)
+        assert f"num_experts={E}" in _lib.last_error()
+    for x, w, out in ((None, p, p), (p, None, p), (p, p, None), (off, p, p), (p, off, p)):
+        assert lib.moe_gate(x, 64, w, 1, None, 4, 8, 64, out, None) == _lib.NVFP4_EINVAL
+
+    def route(par, T=4, E=8, k=2, ldl=8, dtype=1, z=p, ids=p, w=p):
+        return lib.moe_route(ctypes.byref(par) if par is not None else None, z, dtype, ldl, None, T, E, k, ids, w, None)
+
+    assert route(_route(), T=0, z=None, ids=None, w=None) == _lib.NVFP4_OK
+    for bad in (None, _route(score=2), _route(group_score=-1), _route(renormalize=2), _route(scale=0.0),
+                _route(scale=-1.0), _route(scale=float("inf")), _route(scale=float("nan"))):
+        assert route(bad) == _lib.NVFP4_EINVAL
+    for kw in (dict(T=-1), dict(E=0), dict(E=1025, ldl=2000), dict(k=0), dict(k=9), dict(E=64, ldl=64, k=33),
+               dict(ldl=7)):
+        assert route(_route(), **kw) == _lib.NVFP4_ESHAPE, kw
+    for bad in (_route(groups=3), _route(groups=0), _route(groups=4, topk_groups=5), _route(groups=4, topk_groups=0),
+                _route(groups=8, topk_groups=1)):
+        assert route(bad) == _lib.NVFP4_ESHAPE
+    assert "topk_groups=1" in _lib.last_error()
+    assert lib.moe_route(ctypes.byref(_route(groups=128)), p, 1, 256, None, 4, 256, 1, p, p, None) == _lib.NVFP4_ESHAPE
+    for kw in (dict(z=None), dict(ids=None), dict(w=None), dict(dtype=3), dict(z=ctypes.c_void_p(257))):
+        assert route(_route(), **kw) == _lib.NVFP4_EINVAL, kw
