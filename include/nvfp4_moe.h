@@ -319,6 +319,54 @@ int nvfp4_linear_w4a16(const uint16_t* x, int64_t M, int64_t N, int64_t K, const
                        void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Dense linear layers with bias, activation and residual in the epilogue.   */
+/* ------------------------------------------------------------------------ */
+/* The dense projections beside the routed experts (attention projections,
+ * dense layers, shared experts) with what follows their product:
+ *   v = the product of nvfp4_linear, nvfp4_linear_w4a16 or mxfp4_linear
+ *       (FP32, [M][N]) + bias[n]
+ *   plain:  y[m][n] = act(v[m][n])                            N columns
+ *   gated:  y[m][i] = act(v[m][i]) * v[m][N/2 + i]            N/2 columns
+ *   out[m][n] = y[m][n] + residual[m][n], rounded once to out_dtype
+ * All of it is FP32.  Activations: NVFP4_ACT_RELU max(v, 0), NVFP4_ACT_SILU
+ * v / (1 + e^-v), NVFP4_ACT_GELU v Phi(v) (the normal distribution function),
+ * NVFP4_ACT_GELU_TANH v / (1 + e^-2u) with u = sqrt(2/pi) (v + 0.044715 v^3).
+ *
+ * Plain weights are prepared as for the calls without an epilogue.  Gated
+ * weights W [N][K], rows [0, N/2) gate and [N/2, N) up, are prepared as one
+ * expert's gate/up weights: nvfp4_prep_weights or mxfp4_prep_expert_weights
+ * with dims {T: any, topk: 1, E: 1, H: K, I: N/2, shared: 0} and which = 13;
+ * N is then a multiple of 256.  bias float32 [N] in W's row order, or NULL.
+ * residual [M][ld_residual] in residual_dtype, or NULL; it may be out itself
+ * (same pointer, stride and type) and must not overlap it otherwise.
+ * out [M][ld_out]; only its N (gated: N/2) columns are written; it must not
+ * overlap x, the weight, the bias or the workspace.  Strides in
+ * elements, multiples of 4; residual and out are aligned to 4 elements.
+ * M, N, K, x, gw, out_dtype and ws (with its size query) as for the call
+ * without an epilogue. */
+#define NVFP4_ACT_NONE 0
+#define NVFP4_ACT_RELU 1
+#define NVFP4_ACT_SILU 2
+#define NVFP4_ACT_GELU 3
+#define NVFP4_ACT_GELU_TANH 4
+typedef struct nvfp4_epilogue {   /* host struct */
+  int32_t act;
+  int32_t gated;
+  const float* bias;
+  const void* residual;
+  int32_t residual_dtype;
+  int64_t ld_residual;
+  int64_t ld_out;
+} nvfp4_epilogue;
+int nvfp4_linear_fused(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep, const float* gw,
+                       const nvfp4_epilogue* epi, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream);
+int nvfp4_linear_w4a16_fused(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,
+                             const float* gw, const nvfp4_epilogue* epi, void* out, int out_dtype, void* ws,
+                             size_t ws_bytes, void* stream);
+int mxfp4_linear_fused(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,
+                       const nvfp4_epilogue* epi, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Dense OCP MXFP4 linear layer on the scaled FP4 matrix instruction.        */
 /* ------------------------------------------------------------------------ */
 /* The emulation backend's other block format, OCP MXFP4 on MI3xx (vLLM PR

@@ -37,8 +37,14 @@ class RouteParams(ctypes.Structure):
                 ("group_score", c_int32), ("renormalize", c_int32), ("scale", ctypes.c_float)]
 
 
+class Epilogue(ctypes.Structure):
+    _fields_ = [("act", c_int32), ("gated", c_int32), ("bias", c_void_p), ("residual", c_void_p),
+                ("residual_dtype", c_int32), ("ld_residual", c_int64), ("ld_out", c_int64)]
+
+
 _P = ctypes.POINTER(Dims)
 _R = ctypes.POINTER(RouteParams)
+_E = ctypes.POINTER(Epilogue)
 
 # name -> (restype, argtypes); every symbol include/nvfp4_moe.h declares.
 SIGNATURES = {
@@ -70,6 +76,12 @@ SIGNATURES = {
                              c_void_p, c_size_t, c_void_p]),
     "nvfp4_linear_w4a16": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
                                    c_int, c_void_p, c_size_t, c_void_p]),
+    "nvfp4_linear_fused": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, _E, c_void_p, c_int,
+                                   c_void_p, c_size_t, c_void_p]),
+    "nvfp4_linear_w4a16_fused": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, _E, c_void_p,
+                                         c_int, c_void_p, c_size_t, c_void_p]),
+    "mxfp4_linear_fused": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, _E, c_void_p, c_int, c_void_p,
+                                   c_size_t, c_void_p]),
     "mxfp4_quantize": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
     "mxfp4_prep_weights_size": (c_size_t, [c_int64, c_int64]),
     "mxfp4_prep_weights": (c_int, [c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p]),

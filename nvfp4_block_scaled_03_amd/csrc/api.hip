@@ -344,8 +344,46 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K, bool w4a4) {
   return w;
 }
 
+// Checks the epilogue of a fused layer (sizes and enums always, pointers where
+// there are rows) and fills the kernels' form of it.
+int check_epilogue(const char* W, const nvfp4_epilogue* e, int64_t M, int64_t N, int64_t K, void* out, int out_dtype,
+                   nvfp4::LinearEpi* k) {
+  if (!e) return fail(NVFP4_EINVAL, "%s: EINVAL epi is NULL", W);
+  if (e->act < NVFP4_ACT_NONE || e->act > NVFP4_ACT_GELU_TANH || (e->gated != 0 && e->gated != 1))
+    return fail(NVFP4_EINVAL, "%s: EINVAL act=%d gated=%d", W, e->act, e->gated);
+  if (out_dtype != NVFP4_BF16 && out_dtype != NVFP4_F32)
+    return fail(NVFP4_EINVAL, "%s: EINVAL out_dtype=%d", W, out_dtype);
+  if (e->residual && e->residual_dtype != NVFP4_BF16 && e->residual_dtype != NVFP4_F32)
+    return fail(NVFP4_EINVAL, "%s: EINVAL residual_dtype=%d", W, e->residual_dtype);
+  if (e->gated && N % 256)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE M=%lld N=%lld K=%lld (gated: N a multiple of 256)", W, (long long)M,
+                (long long)N, (long long)K);
+  const int64_t n_out = e->gated ? N / 2 : N;
+  if (e->ld_out < n_out || e->ld_out % 4 || (e->residual && (e->ld_residual < n_out || e->ld_residual % 4)))
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE N=%lld ld_out=%lld ld_residual=%lld (at least the output columns, multiples "
+                "of 4)", W, (long long)N, (long long)e->ld_out, (long long)e->ld_residual);
+  if (M > 0) {
+    if (!out) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
+    if (!aligned(out, out_dtype == NVFP4_F32 ? 16 : 8) || !aligned(e->bias, 4) ||
+        !aligned(e->residual, e->residual_dtype == NVFP4_F32 ? 16 : 8))
+      return fail(NVFP4_EINVAL, "%s: EINVAL out and residual aligned to 4 elements, bias to 4 bytes", W);
+  }
+  k->bias = e->bias;
+  k->act = e->act;
+  k->gated = e->gated;
+  k->half = N / 2;
+  k->res = e->residual;
+  k->res_f32 = e->residual_dtype == NVFP4_F32;
+  k->ldr = e->ld_residual;
+  k->out = out;
+  k->out_f32 = out_dtype == NVFP4_F32;
+  k->ldo = e->ld_out;
+  return NVFP4_OK;
+}
+
+// epi: the epilogue of a fused layer (already checked), or null.
 int linear_run(const char* W, bool w4a4, const uint16_t* x, int64_t M, int64_t N, int64_t K,
-               const uint8_t* w_prep, const float* gw, void* out, int out_dtype, void* ws,
+               const uint8_t* w_prep, const float* gw, const nvfp4::LinearEpi* epi, void* out, int out_dtype, void* ws,
                size_t ws_bytes, void* stream) {
   if (!linear_shape_ok(M, N, K))
     return fail(NVFP4_ESHAPE, "%s: ESHAPE M=%lld N=%lld K=%lld (N, K multiples of 128)", W, (long long)M,
@@ -357,7 +395,7 @@ int linear_run(const char* W, bool w4a4, const uint16_t* x, int64_t M, int64_t N
                 W, (long long)M, (long long)N, (long long)K, ws_bytes, L.total);
   if (M == 0) return ok();
   if (!x || !w_prep || !gw || !out) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
-  if (!aligned(x, 16) || !aligned(w_prep, 16) || !aligned(ws, 256) || !aligned(out, 16))
+  if (!aligned(x, 16) || !aligned(w_prep, 16) || !aligned(ws, 256) || (!epi && !aligned(out, 16)))
     return fail(NVFP4_EINVAL, "%s: EINVAL x, w_prep and out 16-byte, ws 256-byte aligned", W);
   uint8_t* b = static_cast<uint8_t*>(ws);
   nvfp4::AlignShape a = nvfp4::align_shape((int)M, 1, 1, 0);
@@ -376,6 +414,7 @@ int linear_run(const char* W, bool w4a4, const uint16_t* x, int64_t M, int64_t N
   la.g_w = gw;
   la.out = out;
   la.out_dtype = out_dtype;
+  la.epi = epi;
   hipError_t e;
   if (w4a4) {
     float* g = reinterpret_cast<float*>(b + L.g);
@@ -405,14 +444,40 @@ size_t nvfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4) {
 
 int nvfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,
                  const float* gw, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream) {
-  return linear_run("nvfp4_linear", true, x, M, N, K, w_prep, gw, out, out_dtype, ws, ws_bytes, stream);
+  return linear_run("nvfp4_linear", true, x, M, N, K, w_prep, gw, nullptr, out, out_dtype, ws, ws_bytes, stream);
 }
 
 int nvfp4_linear_w4a16(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,
                        const float* gw, void* out, int out_dtype, void* ws, size_t ws_bytes,
                        void* stream) {
-  return linear_run("nvfp4_linear_w4a16", false, x, M, N, K, w_prep, gw, out, out_dtype, ws, ws_bytes,
+  return linear_run("nvfp4_linear_w4a16", false, x, M, N, K, w_prep, gw, nullptr, out, out_dtype, ws, ws_bytes,
                     stream);
+}
+
+namespace {
+int linear_fused_run(const char* W, bool w4a4, const uint16_t* x, int64_t M, int64_t N, int64_t K,
+                     const uint8_t* w_prep, const float* gw, const nvfp4_epilogue* epi, void* out, int out_dtype,
+                     void* ws, size_t ws_bytes, void* stream) {
+  if (!linear_shape_ok(M, N, K))
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE M=%lld N=%lld K=%lld (N, K multiples of 128)", W, (long long)M,
+                (long long)N, (long long)K);
+  nvfp4::LinearEpi k{};
+  if (int r = check_epilogue(W, epi, M, N, K, out, out_dtype, &k)) return r;
+  return linear_run(W, w4a4, x, M, N, K, w_prep, gw, &k, out, out_dtype, ws, ws_bytes, stream);
+}
+}  // namespace
+
+int nvfp4_linear_fused(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep, const float* gw,
+                       const nvfp4_epilogue* epi, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  return linear_fused_run("nvfp4_linear_fused", true, x, M, N, K, w_prep, gw, epi, out, out_dtype, ws, ws_bytes,
+                          stream);
+}
+
+int nvfp4_linear_w4a16_fused(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,
+                             const float* gw, const nvfp4_epilogue* epi, void* out, int out_dtype, void* ws,
+                             size_t ws_bytes, void* stream) {
+  return linear_fused_run("nvfp4_linear_w4a16_fused", false, x, M, N, K, w_prep, gw, epi, out, out_dtype, ws, ws_bytes,
+                          stream);
 }
 
 // ------------------------------------------------------------------ MXFP4
@@ -458,14 +523,9 @@ size_t mxfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
   return mx_ws_codes(M, K) + up256((size_t)nvfp4::mx_rows_pad(M) * (K / 32));
 }
 
-int mxfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep, void* out,
-                 int out_dtype, void* ws, size_t ws_bytes, void* stream) {
-  const char* W = "mxfp4_linear";
-  if (!linear_shape_ok(M, N, K) || nvfp4::mx_rows_pad(M) * K >= (int64_t(1) << 31) ||
-      (N * K / 32) * 17 >= (int64_t(1) << 32))
-    return fail(NVFP4_ESHAPE, "%s: ESHAPE M=%lld N=%lld K=%lld (N, K multiples of 128; M K < 2^31, prepared "
-                "weight < 4 GiB)", W, (long long)M, (long long)N, (long long)K);
-  if (out_dtype != 0 && out_dtype != 1) return fail(NVFP4_EINVAL, "%s: EINVAL out_dtype=%d", W, out_dtype);
+namespace {
+int mx_linear_run(const char* W, const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,
+                  const nvfp4::LinearEpi* epi, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream) {
   const size_t need = mxfp4_linear_workspace_size(M, N, K);
   if (ws_bytes < need || (M > 0 && !ws))
     return fail(NVFP4_EWORKSPACE, "%s: EWORKSPACE M=%lld N=%lld K=%lld workspace_size=%zu needed=%zu", W,
@@ -478,7 +538,33 @@ int mxfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8
   uint8_t* ae = aq + mx_ws_codes(M, K);
   hipError_t e = nvfp4::launch_mx_quantize_operand(x, M, K, aq, ae, S(stream));
   if (e != hipSuccess) return launched(e, W);
+  if (epi) return launched(nvfp4::launch_mx_gemm_fused(aq, ae, M, N, K, w_prep, *epi, S(stream)), W);
   return launched(nvfp4::launch_mx_gemm(aq, ae, M, N, K, w_prep, out, out_dtype, S(stream)), W);
+}
+int mx_linear_shape(const char* W, int64_t M, int64_t N, int64_t K) {
+  if (!linear_shape_ok(M, N, K) || nvfp4::mx_rows_pad(M) * K >= (int64_t(1) << 31) ||
+      (N * K / 32) * 17 >= (int64_t(1) << 32))
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE M=%lld N=%lld K=%lld (N, K multiples of 128; M K < 2^31, prepared "
+                "weight < 4 GiB)", W, (long long)M, (long long)N, (long long)K);
+  return NVFP4_OK;
+}
+}  // namespace
+
+int mxfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep, void* out,
+                 int out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  const char* W = "mxfp4_linear";
+  if (int r = mx_linear_shape(W, M, N, K)) return r;
+  if (out_dtype != 0 && out_dtype != 1) return fail(NVFP4_EINVAL, "%s: EINVAL out_dtype=%d", W, out_dtype);
+  return mx_linear_run(W, x, M, N, K, w_prep, nullptr, out, out_dtype, ws, ws_bytes, stream);
+}
+
+int mxfp4_linear_fused(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,
+                       const nvfp4_epilogue* epi, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  const char* W = "mxfp4_linear_fused";
+  if (int r = mx_linear_shape(W, M, N, K)) return r;
+  nvfp4::LinearEpi k{};
+  if (int r = check_epilogue(W, epi, M, N, K, out, out_dtype, &k)) return r;
+  return mx_linear_run(W, x, M, N, K, w_prep, &k, out, out_dtype, ws, ws_bytes, stream);
 }
 
 // ------------------------------------------------------------------ weights

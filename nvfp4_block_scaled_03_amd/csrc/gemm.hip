@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "epilogue.h"
 #include "launch.h"
 
 namespace nvfp4 {
@@ -64,8 +65,12 @@ constexpr int kLDA = kBK + 8;  // LDS row stride in 16-bit elements (272 bytes)
 constexpr int kBufferFlags = 0x00020000;
 
 enum Act { kActCodes = 0, kActF16 = 1, kActBf16 = 2 };
-enum Epi { kEpiSwigluFp4 = 0, kEpiSwigluBf16 = 1, kEpiStoreF32 = 2, kEpiStoreBf16 = 3 };
+enum Epi {
+  kEpiSwigluFp4 = 0, kEpiSwigluBf16 = 1, kEpiStoreF32 = 2, kEpiStoreBf16 = 3,
+  kEpiLinear = 4, kEpiLinearGated = 5   // dense layers: bias, activation, residual (epilogue.h)
+};
 constexpr bool swiglu_epi(int e) { return e == kEpiSwigluFp4 || e == kEpiSwigluBf16; }
+constexpr bool linear_epi(int e) { return e == kEpiLinear || e == kEpiLinearGated; }
 
 
 struct KParams {
@@ -87,6 +92,7 @@ struct KParams {
   uint8_t* out_sf;
   uint16_t* out_h;         // GEMM1: bf16 intermediate (W4A16) or optional f16 copy (W4A4)
   float* out_f32;
+  LinearEpi ep;            // kEpiLinear*
 };
 
 // Bijection from the launch order to the work order such that each XCD (the
@@ -112,7 +118,9 @@ __device__ __forceinline__ void epilogue(const KParams& p, f32x4 (&acc)[MT][NTW]
                                          int nrows, int n_wave0, int lane) {
   const float alpha = p.g_a ? ld_uniform(p.g_a) * ld_uniform(p.g_w + e) : ld_uniform(p.g_w + e);
   const int ln = lane & 15, lg = lane >> 4;
-  if constexpr (EPI == kEpiStoreF32 || EPI == kEpiStoreBf16) {
+  if constexpr (linear_epi(EPI)) {
+    epilogue_linear<EPI == kEpiLinearGated, MT, NTW>(p.ep, acc, alpha, row0, nrows, n_wave0, lane);
+  } else if constexpr (EPI == kEpiStoreF32 || EPI == kEpiStoreBf16) {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -857,7 +865,11 @@ void grouped_gemm_wide_kernel(KParams p) {
   constexpr int WAVE_BYTES = 2 * BUF_BYTES / NW;
   uint8_t* const area = (wv < NW / 2 ? As0 : As1) + (wv % (NW / 2)) * WAVE_BYTES;
   float* sh = reinterpret_cast<float*>(area);
-  if constexpr (!swiglu_epi(EPI)) {
+  if constexpr (linear_epi(EPI)) {
+    static_assert(16 * (16 * NTW + 4) * 4 <= WAVE_BYTES, "one m-tile fits the wave's area");
+    const float alpha = p.g_a ? ld_uniform(p.g_a) * ld_uniform(p.g_w + t.e) : ld_uniform(p.g_w + t.e);
+    epilogue_linear_rowmajor<EPI == kEpiLinearGated, MT, NTW>(p.ep, acc, alpha, t.row0, t.nrows, n_wave0, lane, sh);
+  } else if constexpr (!swiglu_epi(EPI)) {
     static_assert(16 * (16 * NTW + 4) * 4 <= WAVE_BYTES, "one m-tile fits the wave's area");
     epilogue_rowmajor<EPI, MT, NTW>(p, acc, t.e, t.row0, t.nrows, n_wave0, lane, sh);
   } else {
@@ -1251,14 +1263,14 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ 
 // of a persistent pass over (tile, 32-column) units, which at N = 34816
 // leaves most of the device idle for a single 16-row tile.
 // ---------------------------------------------------------------------------
-template <int AK, bool F32, int UB>
+template <int AK, int EPI, int UB>
 __global__ __launch_bounds__(4 * kWave) void linear_splitk_kernel(KParams p) {
   constexpr int NTW = 2;
   static_assert(AK != kActF16, "codes or bf16 activations");
   __shared__ f32x4 red[3][NTW][kWave];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int m = lane & 15, g = lane >> 4;
-  const int M = p.T, N = p.N, K = p.K, KC = K / kBK, NT = N / 16;
+  const int M = p.T, N = p.N, K = p.K, KC = K / kBK;
   const int c_lo = KC * wv / 4, c_hi = KC * (wv + 1) / 4;
   const int nt0 = blockIdx.x * NTW;
   const int row = min(m, M - 1);   // rows past M repeat the last one (never stored)
@@ -1327,6 +1339,7 @@ __global__ __launch_bounds__(4 * kWave) void linear_splitk_kernel(KParams p) {
   __syncthreads();
   if (wv > 0) return;
   const float alpha = p.g_a ? ld_uniform(p.g_a) * ld_uniform(p.g_w) : ld_uniform(p.g_w);
+  f32x4 sum[1][NTW];
 #pragma unroll
   for (int j = 0; j < NTW; ++j) {
     f32x4 v = acc[j];
@@ -1338,17 +1351,23 @@ __global__ __launch_bounds__(4 * kWave) void linear_splitk_kernel(KParams p) {
       v[2] += o[2];
       v[3] += o[3];
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int rr = g * 4 + r;
-      if (rr < M) {
-        const int64_t o = (int64_t)rr * N + (nt0 + j) * 16 + m;
-        if constexpr (F32) p.out_f32[o] = alpha * v[r];
-        else p.out_h[o] = (uint16_t)f32_to_bf16_bits(alpha * v[r]);
-      }
-    }
+    sum[0][j] = v;
   }
-  (void)NT;
+  if constexpr (linear_epi(EPI)) {
+    epilogue_linear<EPI == kEpiLinearGated, 1, NTW>(p.ep, sum, alpha, 0, M, nt0 * 16, lane);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NTW; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int rr = g * 4 + r;
+        if (rr < M) {
+          const int64_t o = (int64_t)rr * N + (nt0 + j) * 16 + m;
+          if constexpr (EPI == kEpiStoreF32) p.out_f32[o] = alpha * sum[0][j][r];
+          else p.out_h[o] = (uint16_t)f32_to_bf16_bits(alpha * sum[0][j][r]);
+        }
+      }
+  }
 }
 
 
@@ -1521,6 +1540,27 @@ hipError_t launch_gemm1(const GemmArgs& a, bool w4a4, hipStream_t s) {
   return launch_gemm<kActBf16, kEpiSwigluBf16>(k, al, s, a.part);
 }
 
+// One dense layer with epilogue EPI: few rows on the split-K kernel, else the
+// grouped kernels' rules with one expert.
+template <int EPI>
+static hipError_t launch_linear_epi(const LinearArgs& a, const KParams& k, const AlignShape& al, hipStream_t s) {
+  // Few rows from codes (at most 16) or bf16 (at most 4): K split over the
+  // 4 wavefronts of a workgroup per 32 columns (N is a multiple of 128).
+  // Measured at N = 34816, K = 5120: M = 1 W4A4 33.0 -> 30.3 us, W4A16
+  // 35.7 -> 31.8 us, M = 16 W4A4 41.0 -> 39.7 us; W4A16 at M = 16 is faster
+  // on the streaming kernel (35.7 against 47.1 us: its bf16 rows are 4x the
+  // bytes of codes).
+  if (a.M >= 1 && ((a.w4a4 && !a.a_h && a.M <= 16) || (!a.w4a4 && a.M <= 4))) {
+    const dim3 grid((unsigned)(a.N / 32));
+    if (a.w4a4) linear_splitk_kernel<kActCodes, EPI, 4><<<grid, 4 * kWave, 0, s>>>(k);
+    else linear_splitk_kernel<kActBf16, EPI, 4><<<grid, 4 * kWave, 0, s>>>(k);
+    return hipGetLastError();
+  }
+  if (!a.w4a4) return launch_gemm<kActBf16, EPI>(k, al, s, kPartAll);
+  if (a.a_h) return launch_gemm<kActF16, EPI>(k, al, s, kPartAll);
+  return launch_gemm<kActCodes, EPI>(k, al, s, kPartAll);
+}
+
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   AlignShape al = align_shape((int)a.M, 1, 1, 0);
   KParams k{};
@@ -1538,34 +1578,16 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   k.a_q = a.a_q;
   k.a_sf = a.a_sf;
   k.a_h = a.a_h;
-  const bool f32 = a.out_dtype != 0;
-  if (f32) k.out_f32 = static_cast<float*>(a.out);
-  else k.out_h = static_cast<uint16_t*>(a.out);
-  // Few rows from codes (at most 16) or bf16 (at most 4): K split over the
-  // 4 wavefronts of a workgroup per 32 columns (N is a multiple of 128).
-  // Measured at N = 34816, K = 5120: M = 1 W4A4 33.0 -> 30.3 us, W4A16
-  // 35.7 -> 31.8 us, M = 16 W4A4 41.0 -> 39.7 us; W4A16 at M = 16 is faster
-  // on the streaming kernel (35.7 against 47.1 us: its bf16 rows are 4x the
-  // bytes of codes).
-  if (a.M >= 1 && ((a.w4a4 && !a.a_h && a.M <= 16) || (!a.w4a4 && a.M <= 4))) {
-    const dim3 grid((unsigned)(a.N / 32));
-    if (a.w4a4) {
-      if (f32) linear_splitk_kernel<kActCodes, true, 4><<<grid, 4 * kWave, 0, s>>>(k);
-      else linear_splitk_kernel<kActCodes, false, 4><<<grid, 4 * kWave, 0, s>>>(k);
-    } else {
-      if (f32) linear_splitk_kernel<kActBf16, true, 4><<<grid, 4 * kWave, 0, s>>>(k);
-      else linear_splitk_kernel<kActBf16, false, 4><<<grid, 4 * kWave, 0, s>>>(k);
-    }
-    return hipGetLastError();
+  if (a.epi) {
+    k.ep = *a.epi;
+    return a.epi->gated ? launch_linear_epi<kEpiLinearGated>(a, k, al, s) : launch_linear_epi<kEpiLinear>(a, k, al, s);
   }
-  if (!a.w4a4)
-    return f32 ? launch_gemm<kActBf16, kEpiStoreF32>(k, al, s, kPartAll)
-               : launch_gemm<kActBf16, kEpiStoreBf16>(k, al, s, kPartAll);
-  if (a.a_h)
-    return f32 ? launch_gemm<kActF16, kEpiStoreF32>(k, al, s, kPartAll)
-               : launch_gemm<kActF16, kEpiStoreBf16>(k, al, s, kPartAll);
-  return f32 ? launch_gemm<kActCodes, kEpiStoreF32>(k, al, s, kPartAll)
-             : launch_gemm<kActCodes, kEpiStoreBf16>(k, al, s, kPartAll);
+  if (a.out_dtype) {
+    k.out_f32 = static_cast<float*>(a.out);
+    return launch_linear_epi<kEpiStoreF32>(a, k, al, s);
+  }
+  k.out_h = static_cast<uint16_t*>(a.out);
+  return launch_linear_epi<kEpiStoreBf16>(a, k, al, s);
 }
 
 hipError_t launch_combine(const float* d, const int32_t* inv_pos, const float* topk_w, int T, int topk,

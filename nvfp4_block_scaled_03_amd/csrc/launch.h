@@ -164,6 +164,23 @@ int pick_list(int64_t P, int slots);
 // every token).
 bool split_experts(const AlignShape& al);
 
+// Epilogue of a dense linear layer (epilogue.h): activations, and what it
+// reads and writes.  ``half``: N / 2 of a gated layer (output columns; the
+// offset of the up projection's bias).
+enum LinearAct { kFnNone = 0, kFnRelu = 1, kFnSilu = 2, kFnGelu = 3, kFnGeluTanh = 4 };
+struct LinearEpi {
+  const float* bias;   // [N] or null
+  int act;
+  int gated;
+  int64_t half;
+  const void* res;     // [M][ldr] or null
+  int res_f32;
+  int64_t ldr;
+  void* out;           // [M][ldo]
+  int out_f32;
+  int64_t ldo;
+};
+
 // Dense linear y [M][N] = x [M][K] W^T on the grouped-GEMM kernels with one
 // expert (plan from an alignment of M pairs to expert 0).
 struct LinearArgs {
@@ -178,6 +195,7 @@ struct LinearArgs {
   const uint16_t* a_h;     // the exact f16 copy (W4A4) / bf16 x (W4A16)
   void* out;
   int out_dtype;           // 0 bf16, 1 f32
+  const LinearEpi* epi;    // host pointer, or null: y alone (out, out_dtype)
 };
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 

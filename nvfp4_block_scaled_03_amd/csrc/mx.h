@@ -22,6 +22,11 @@ hipError_t launch_mx_prep(int64_t N, int64_t K, const uint8_t* q, const uint8_t*
 // a_q / a_e: the activation operand from launch_mx_quantize_operand.
 hipError_t launch_mx_gemm(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
                           const uint8_t* w_prep, void* out, int out_dtype, hipStream_t s);
+// The same with the epilogue of a fused layer (output, bias, activation,
+// residual in ep; a gated layer's w_prep alternates gate and up tiles).
+struct LinearEpi;
+hipError_t launch_mx_gemm_fused(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
+                                const uint8_t* w_prep, const LinearEpi& ep, hipStream_t s);
 
 // Mixture-of-experts layer in MXFP4: expert weights prepared per slot
 // (interleave_I = I for the gate/up weights: column tiles alternate gate and

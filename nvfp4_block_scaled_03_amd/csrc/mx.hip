@@ -10,6 +10,7 @@
 #include <algorithm>
 
 #include "common.h"
+#include "epilogue.h"
 #include "launch.h"
 #include "mx.h"
 #include "quant.h"
@@ -139,10 +140,14 @@ struct MxRing {
 // are outstanding (the LDS and export counters left at their maxima).
 constexpr int mx_vmcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 
-template <int WM, int D, bool F32>
+// Epilogue of the dense kernels: the product alone (kMxOutBf16, kMxOutF32) or
+// that of the fused layers (epilogue.h).
+enum MxOut { kMxOutBf16 = 0, kMxOutF32 = 1, kMxOutLinear = 2, kMxOutGated = 3 };
+
+template <int WM, int D, int OUT>
 __global__ __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(WM, WM))) void mx_gemm_kernel(
     const uint8_t* __restrict__ a_q, const uint8_t* __restrict__ a_e, int64_t M, int64_t N, int64_t K,
-    const uint8_t* __restrict__ w_prep, void* __restrict__ out) {
+    const uint8_t* __restrict__ w_prep, void* __restrict__ out, LinearEpi ep) {
   using R = MxRing<WM>;
   static_assert(D >= 2 && (D - 2) * R::Loads <= 63, "ring depth");
   constexpr int ROWS = 128 * WM, MT = 8, NTW = 4, NBW = 4 / WM;
@@ -266,6 +271,10 @@ __global__ __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(WM, WM
   __builtin_amdgcn_s_waitcnt(mx_vmcnt(0));
   if (!wave_on) return;
   const int64_t mw0 = m0 + wm * 128;
+  if constexpr (OUT == kMxOutLinear || OUT == kMxOutGated) {
+    epilogue_linear<OUT == kMxOutGated, MT, NTW>(ep, acc, 1.0f, mw0, M - mw0, n_wave0, lane);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -275,7 +284,7 @@ __global__ __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(WM, WM
         const int64_t row = mw0 + i * 16 + fg * 4 + r;
         if (row < M) {
           const int64_t o = row * N + n_wave0 + 16 * j + fr;
-          if constexpr (F32) static_cast<float*>(out)[o] = acc[i][j][r];
+          if constexpr (OUT == kMxOutF32) static_cast<float*>(out)[o] = acc[i][j][r];
           else static_cast<uint16_t*>(out)[o] = (uint16_t)f32_to_bf16_bits(acc[i][j][r]);
         }
       }
@@ -287,12 +296,12 @@ __global__ __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(WM, WM
 // loading UB chunks of weights and activations (straight from global memory:
 // the activations are small and stay in L2) before multiplying them, then
 // the quarters are summed through LDS.
-template <int MT, int NTW, int UB, bool F32>
+template <int MT, int NTW, int UB, int OUT>
 __global__ __launch_bounds__(256) void mx_gemm_splitk_kernel(const uint8_t* __restrict__ a_q,
                                                              const uint8_t* __restrict__ a_e, int64_t M,
                                                              int64_t N, int64_t K,
                                                              const uint8_t* __restrict__ w_prep,
-                                                             void* __restrict__ out) {
+                                                             void* __restrict__ out, LinearEpi ep) {
   __shared__ f32x4 red[3][MT][NTW][64];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int fr = lane & 15, fg = lane >> 4;
@@ -363,35 +372,54 @@ __global__ __launch_bounds__(256) void mx_gemm_splitk_kernel(const uint8_t* __re
         v[2] += o[2];
         v[3] += o[3];
       }
+      acc[i][j] = v;
+    }
+  if constexpr (OUT == kMxOutLinear || OUT == kMxOutGated) {
+    epilogue_linear<OUT == kMxOutGated, MT, NTW>(ep, acc, 1.0f, 0, M, nt0 * 16, lane);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NTW; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int64_t row = i * 16 + fg * 4 + r;
         if (row < M) {
           const int64_t o = row * N + (nt0 + j) * 16 + fr;
-          if constexpr (F32) static_cast<float*>(out)[o] = v[r];
-          else static_cast<uint16_t*>(out)[o] = (uint16_t)f32_to_bf16_bits(v[r]);
+          if constexpr (OUT == kMxOutF32) static_cast<float*>(out)[o] = acc[i][j][r];
+          else static_cast<uint16_t*>(out)[o] = (uint16_t)f32_to_bf16_bits(acc[i][j][r]);
         }
       }
-    }
 }
 
-template <int MT, int NTW, int UB>
+template <int MT, int NTW, int UB, int OUT>
 hipError_t launch_mx_splitk(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
-                            const uint8_t* w_prep, void* out, int out_dtype, hipStream_t s) {
+                            const uint8_t* w_prep, void* out, const LinearEpi& ep, hipStream_t s) {
   const dim3 grid((unsigned)(N / (16 * NTW)));
-  if (out_dtype) mx_gemm_splitk_kernel<MT, NTW, UB, true><<<grid, 256, 0, s>>>(a_q, a_e, M, N, K, w_prep, out);
-  else mx_gemm_splitk_kernel<MT, NTW, UB, false><<<grid, 256, 0, s>>>(a_q, a_e, M, N, K, w_prep, out);
+  mx_gemm_splitk_kernel<MT, NTW, UB, OUT><<<grid, 256, 0, s>>>(a_q, a_e, M, N, K, w_prep, out, ep);
   return hipGetLastError();
 }
 
-template <int WM>
+template <int WM, int OUT>
 hipError_t launch_mx_gemm_ring(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
-                               const uint8_t* w_prep, void* out, int out_dtype, hipStream_t s) {
+                               const uint8_t* w_prep, void* out, const LinearEpi& ep, hipStream_t s) {
   const int64_t tiles = ((M + 128 * WM - 1) / (128 * WM)) * ((N + 255) / 256);
   const unsigned grid = (unsigned)(8 * ((tiles + 7) / 8));
-  if (out_dtype) mx_gemm_kernel<WM, NVFP4_MX_DEPTH, true><<<grid, 256 * WM, 0, s>>>(a_q, a_e, M, N, K, w_prep, out);
-  else mx_gemm_kernel<WM, NVFP4_MX_DEPTH, false><<<grid, 256 * WM, 0, s>>>(a_q, a_e, M, N, K, w_prep, out);
+  mx_gemm_kernel<WM, NVFP4_MX_DEPTH, OUT><<<grid, 256 * WM, 0, s>>>(a_q, a_e, M, N, K, w_prep, out, ep);
   return hipGetLastError();
+}
+
+template <int OUT>
+hipError_t launch_mx_gemm_out(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
+                              const uint8_t* w_prep, void* out, const LinearEpi& ep, hipStream_t s) {
+  // N is a multiple of 128, so NTW <= 8 column tiles divide it.
+  if (M <= 16) return launch_mx_splitk<1, NVFP4_MX_NTW1, NVFP4_MX_UB1, OUT>(a_q, a_e, M, N, K, w_prep, out, ep, s);
+  if (M <= 32) return launch_mx_splitk<2, NVFP4_MX_NTW2, NVFP4_MX_UB2, OUT>(a_q, a_e, M, N, K, w_prep, out, ep, s);
+  if (M <= 64) return launch_mx_splitk<4, NVFP4_MX_NTW4, NVFP4_MX_UB4, OUT>(a_q, a_e, M, N, K, w_prep, out, ep, s);
+  // up to 128 rows: one 128-row tile (4 wavefronts); more: 256-row tiles
+  if (M <= 128) return launch_mx_gemm_ring<1, OUT>(a_q, a_e, M, N, K, w_prep, out, ep, s);
+  return launch_mx_gemm_ring<2, OUT>(a_q, a_e, M, N, K, w_prep, out, ep, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -1077,13 +1105,14 @@ hipError_t launch_mx_prep(int64_t N, int64_t K, const uint8_t* q, const uint8_t*
 
 hipError_t launch_mx_gemm(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
                           const uint8_t* w_prep, void* out, int out_dtype, hipStream_t s) {
-  // N is a multiple of 128, so NTW <= 8 column tiles divide it.
-  if (M <= 16) return launch_mx_splitk<1, NVFP4_MX_NTW1, NVFP4_MX_UB1>(a_q, a_e, M, N, K, w_prep, out, out_dtype, s);
-  if (M <= 32) return launch_mx_splitk<2, NVFP4_MX_NTW2, NVFP4_MX_UB2>(a_q, a_e, M, N, K, w_prep, out, out_dtype, s);
-  if (M <= 64) return launch_mx_splitk<4, NVFP4_MX_NTW4, NVFP4_MX_UB4>(a_q, a_e, M, N, K, w_prep, out, out_dtype, s);
-  // up to 128 rows: one 128-row tile (4 wavefronts); more: 256-row tiles
-  if (M <= 128) return launch_mx_gemm_ring<1>(a_q, a_e, M, N, K, w_prep, out, out_dtype, s);
-  return launch_mx_gemm_ring<2>(a_q, a_e, M, N, K, w_prep, out, out_dtype, s);
+  return out_dtype ? launch_mx_gemm_out<kMxOutF32>(a_q, a_e, M, N, K, w_prep, out, LinearEpi{}, s)
+                   : launch_mx_gemm_out<kMxOutBf16>(a_q, a_e, M, N, K, w_prep, out, LinearEpi{}, s);
+}
+
+hipError_t launch_mx_gemm_fused(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
+                                const uint8_t* w_prep, const LinearEpi& ep, hipStream_t s) {
+  return ep.gated ? launch_mx_gemm_out<kMxOutGated>(a_q, a_e, M, N, K, w_prep, nullptr, ep, s)
+                  : launch_mx_gemm_out<kMxOutLinear>(a_q, a_e, M, N, K, w_prep, nullptr, ep, s);
 }
 
 }  // namespace nvfp4

@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import NVFP4_BF16, NVFP4_F32, Dims, RouteParams, call
+from ._lib import NVFP4_BF16, NVFP4_F32, Dims, Epilogue, RouteParams, call
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -372,25 +372,32 @@ def gemm2_w4a16(d: Dims, a2, al: Alignment, topk_w, w: ExpertWeights, out_dtype=
 
 # ---------------------------------------------------------------- dense linear
 class LinearWeight:
-    """An NVFP4 weight W [N, K] prepared for nvfp4_linear*."""
+    """An NVFP4 weight W [N, K] prepared for nvfp4_linear*; ``gated``: rows
+    [0, N/2) are a gate projection and [N/2, N) the matching up projection."""
 
-    def __init__(self, prep: torch.Tensor, g: torch.Tensor, N: int, K: int):
-        self.prep, self.g, self.N, self.K = prep, g, N, K
+    def __init__(self, prep: torch.Tensor, g: torch.Tensor, N: int, K: int, gated: bool = False):
+        self.prep, self.g, self.N, self.K, self.gated = prep, g, N, K, gated
 
 
-def prepare_linear_weight(w_q: torch.Tensor, w_sf: torch.Tensor, g: torch.Tensor) -> LinearWeight:
+def _gated_dims(N: int, K: int) -> Dims:
+    """One expert whose gate/up weights are the gated layer's W [N, K]."""
+    _need(N % 256 == 0, f"a gated layer's N={N} must be a multiple of 256")
+    return dims(1, 1, 1, K, N // 2, 0)
+
+
+def prepare_linear_weight(w_q: torch.Tensor, w_sf: torch.Tensor, g: torch.Tensor, gated: bool = False) -> LinearWeight:
     """From canonical NVFP4 (codes [N, K/2], scales [N, K/16], global scale)."""
     N, K = w_q.shape[0], w_q.shape[1] * 2
-    d = dims(1, 1, 1, N, K, 0)
-    prep = prep_weights(d, 2, w_q.reshape(1, N, K // 2), w_sf.reshape(1, N, K // 16))
-    return LinearWeight(prep, g.reshape(1).float(), N, K)
+    d = _gated_dims(N, K) if gated else dims(1, 1, 1, N, K, 0)
+    prep = prep_weights(d, 13 if gated else 2, w_q.reshape(1, N, K // 2), w_sf.reshape(1, N, K // 16))
+    return LinearWeight(prep, g.reshape(1).float(), N, K, gated)
 
 
-def quantize_linear_weight(w: torch.Tensor) -> LinearWeight:
+def quantize_linear_weight(w: torch.Tensor, gated: bool = False) -> LinearWeight:
     """FP32 W [N, K] -> global scale, NVFP4 quantisation on the GPU, prep."""
     g = global_scale(w)
     q, sf = quantize(w.contiguous().float(), g)
-    return prepare_linear_weight(q, sf, g)
+    return prepare_linear_weight(q, sf, g, gated)
 
 
 def linear_workspace(M: int, N: int, K: int, w4a4: bool, device) -> torch.Tensor:
@@ -398,12 +405,67 @@ def linear_workspace(M: int, N: int, K: int, w4a4: bool, device) -> torch.Tensor
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
 
 
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _rows4(t: torch.Tensor) -> bool:
+    """Whether the rows of t [M, n] lie apart and can be read and written
+    four elements at a time."""
+    return (t.stride(1) == 1 and t.data_ptr() % (4 * t.element_size()) == 0
+            and (t.shape[0] <= 1 or (t.stride(0) >= t.shape[1] and t.stride(0) % 4 == 0)))
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _linear_fused(name: str, x, w, scale, bias, act, residual, out_dtype, out, ws):
+    """The fused call ``name`` after its checks; ``scale``: the weight's
+    global scale (NVFP4), or None (MXFP4)."""
+    with _device_of(x, w.prep, bias, residual, out, ws):
+        _need(x.dim() == 2 and x.shape[1] == w.K and x.dtype == torch.bfloat16, f"x must be bfloat16 [M, {w.K}]")
+        _need(act in ACTIVATIONS, f"act must be one of {sorted(ACTIVATIONS)}")
+        M, n_out = x.shape[0], w.N // 2 if w.gated else w.N
+        if out is None:
+            out = torch.empty(M, n_out, dtype=out_dtype, device=x.device)
+        _need(out.shape == (M, n_out) and _rows4(out),
+              f"out must be [{M}, {n_out}] with rows of consecutive elements, starts and strides multiples of 4")
+        epi = Epilogue(ACTIVATIONS[act], int(w.gated), ld_out=_row_stride(out))
+        if bias is not None:
+            _need(bias.shape == (w.N,) and bias.dtype == torch.float32, f"bias must be float32 [{w.N}]")
+            bias = bias.contiguous()
+            epi.bias = bias.data_ptr()
+        if residual is not None:
+            _need(residual.shape == (M, n_out), f"residual must be [{M}, {n_out}]")
+            if not _rows4(residual):
+                residual = residual.clone(memory_format=torch.contiguous_format)
+            epi.residual, epi.residual_dtype = residual.data_ptr(), _dtype_code(residual)
+            epi.ld_residual = _row_stride(residual)
+        x = x.contiguous()
+        operands = (_p(x), M, w.N, w.K, _p(w.prep)) if scale is None else (_p(x), M, w.N, w.K, _p(w.prep), _p(scale))
+        call(name, *operands, ctypes.byref(epi), _p(out), _dtype_code(out), _p(ws),
+             ws.numel() * ws.element_size(), _stream())
+    return out
+
+
 def linear(x: torch.Tensor, w: LinearWeight, variant: str = "w4a4", out_dtype=torch.bfloat16,
-           out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """y [M, N] = x [M, K] W^T (bf16 x; W4A4 quantises x, W4A16 uses it as is)."""
+           out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+           bias: Optional[torch.Tensor] = None, act: str = "none",
+           residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [M, N] = x [M, K] W^T (bf16 x; W4A4 quantises x, W4A16 uses it as is).
+
+    With ``bias`` (float32 [N]), ``act`` (a key of ACTIVATIONS), ``residual``
+    (bf16 or float32 [M, N]; it may be ``out``) or a gated weight, the rest of
+    the layer runs in the product's epilogue: act(y + bias) + residual, or
+    act(gate) * up + residual [M, N/2] with gate, up the halves of y + bias."""
     _need_cuda(x)
     M = x.shape[0]
     w4a4 = variant == "w4a4"
+    if bias is not None or act != "none" or residual is not None or w.gated:
+        _need(variant in ("w4a4", "w4a16"), f"variant {variant!r}: w4a4 or w4a16")
+        ws = ws if ws is not None else linear_workspace(M, w.N, w.K, w4a4, x.device)
+        return _linear_fused("nvfp4_linear_fused" if w4a4 else "nvfp4_linear_w4a16_fused", x, w, w.g, bias, act,
+                             residual, out_dtype, out, ws)
     out = out if out is not None else torch.empty(M, w.N, dtype=out_dtype, device=x.device)
     ws = ws if ws is not None else linear_workspace(M, w.N, w.K, w4a4, x.device)
     call("nvfp4_linear" if w4a4 else "nvfp4_linear_w4a16", _p(x.contiguous()), M, w.N, w.K, _p(w.prep),
@@ -427,26 +489,28 @@ def mx_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None, ex: Optional[
 
 
 class MxLinearWeight:
-    """An MXFP4 weight W [N, K] prepared for mxfp4_linear."""
+    """An MXFP4 weight W [N, K] prepared for mxfp4_linear; ``gated`` as for LinearWeight."""
 
-    def __init__(self, prep: torch.Tensor, N: int, K: int):
-        self.prep, self.N, self.K = prep, N, K
+    def __init__(self, prep: torch.Tensor, N: int, K: int, gated: bool = False):
+        self.prep, self.N, self.K, self.gated = prep, N, K, gated
 
 
-def prepare_mx_weight(w_q: torch.Tensor, w_ex: torch.Tensor) -> MxLinearWeight:
+def prepare_mx_weight(w_q: torch.Tensor, w_ex: torch.Tensor, gated: bool = False) -> MxLinearWeight:
     """From canonical MXFP4 (codes [N, K/2], exponent bytes [N, K/32])."""
     _need_cuda(w_q, w_ex)
     N, K = w_q.shape[0], w_q.shape[1] * 2
+    if gated:
+        return MxLinearWeight(prep_mx_expert_weights(_gated_dims(N, K), 13, w_q, w_ex), N, K, True)
     n = _lib.load().mxfp4_prep_weights_size(N, K)
     prep = torch.empty(max(n, 16), dtype=torch.uint8, device=w_q.device)
     call("mxfp4_prep_weights", N, K, _p(w_q.contiguous()), _p(w_ex.contiguous()), _p(prep), _stream())
     return MxLinearWeight(prep, N, K)
 
 
-def quantize_mx_weight(w: torch.Tensor) -> MxLinearWeight:
+def quantize_mx_weight(w: torch.Tensor, gated: bool = False) -> MxLinearWeight:
     """FP32 or bf16 W [N, K] -> MXFP4 quantisation on the GPU, prep."""
     q, ex = mx_quantize(w.contiguous())
-    return prepare_mx_weight(q, ex)
+    return prepare_mx_weight(q, ex, gated)
 
 
 def mx_linear_workspace(M: int, N: int, K: int, device) -> torch.Tensor:
@@ -455,10 +519,15 @@ def mx_linear_workspace(M: int, N: int, K: int, device) -> torch.Tensor:
 
 
 def mx_linear(x: torch.Tensor, w: MxLinearWeight, out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
-              ws: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """y [M, N] = Q(x) W^T, x bf16 [M, K] quantised to MXFP4 in the call."""
+              ws: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, act: str = "none",
+              residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [M, N] = Q(x) W^T, x bf16 [M, K] quantised to MXFP4 in the call;
+    ``bias``, ``act``, ``residual`` and gated weights as for ``linear``."""
     _need_cuda(x)
     M = x.shape[0]
+    if bias is not None or act != "none" or residual is not None or w.gated:
+        ws = ws if ws is not None else mx_linear_workspace(M, w.N, w.K, x.device)
+        return _linear_fused("mxfp4_linear_fused", x, w, None, bias, act, residual, out_dtype, out, ws)
     out = out if out is not None else torch.empty(M, w.N, dtype=out_dtype, device=x.device)
     ws = ws if ws is not None else mx_linear_workspace(M, w.N, w.K, x.device)
     call("mxfp4_linear", _p(x.contiguous()), M, w.N, w.K, _p(w.prep), _p(out), _dtype_code(out), _p(ws),

@@ -17,6 +17,8 @@ What is computed follows the expert path's conventions (see oracle/moe.py):
 """
 from __future__ import annotations
 
+import math
+
 import numpy as np
 
 from . import nvfp4
@@ -45,3 +47,35 @@ def linear_w4a16(x, w_codes, w_scales, gw) -> np.ndarray:
     x = np.asarray(x, dtype=np.float64)
     w_hat = nvfp4.dequantize(w_codes, w_scales, gw)
     return x @ w_hat.T
+
+
+def activation(v, act: str) -> np.ndarray:
+    """FP64 activation: none, relu, silu z / (1 + e^-z), gelu z Phi(z),
+    gelu_tanh z / (1 + e^-2u) with u = sqrt(2/pi) (z + 0.044715 z^3)."""
+    v = np.asarray(v, dtype=np.float64)
+    with np.errstate(over="ignore"):
+        if act == "none":
+            return v
+        if act == "relu":
+            return np.maximum(v, 0.0)
+        if act == "silu":
+            return v / (1.0 + np.exp(-v))
+        if act == "gelu":
+            return 0.5 * v * np.vectorize(math.erfc, otypes=[np.float64])(-v / math.sqrt(2.0))
+        if act == "gelu_tanh":
+            return v / (1.0 + np.exp(-2.0 * math.sqrt(2.0 / math.pi) * (v + 0.044715 * v ** 3)))
+    raise ValueError(act)
+
+
+def epilogue(v, bias=None, act: str = "none", gated: bool = False, residual=None) -> np.ndarray:
+    """FP64 epilogue of a dense layer on its product v [M, N]: bias, then the
+    activation, or act(first half) * second half, then the residual."""
+    v = np.asarray(v, dtype=np.float64)
+    if bias is not None:
+        v = v + np.asarray(bias, dtype=np.float64)
+    if gated:
+        h = v.shape[1] // 2
+        y = activation(v[:, :h], act) * v[:, h:]
+    else:
+        y = activation(v, act)
+    return y if residual is None else y + np.asarray(residual, dtype=np.float64)

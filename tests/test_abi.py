@@ -319,3 +319,44 @@ def test_router_errors(lib):
     assert lib.moe_route(ctypes.byref(_route(groups=128)), p, 1, 256, None, 4, 256, 1, p, p, None) == _lib.NVFP4_ESHAPE
     for kw in (dict(z=None), dict(ids=None), dict(w=None), dict(dtype=3), dict(z=ctypes.c_void_p(257))):
         assert route(_route(), **kw) == _lib.NVFP4_EINVAL, kw
+
+
+def test_fused_linear_errors(lib):
+    """The fused dense layers check the epilogue, then what the plain calls
+    check, before a launch; M == 0 is a no-op."""
+    p = ctypes.c_void_p(4096)
+
+    def epi(**kw):
+        return _lib.Epilogue(**{**dict(act=0, gated=0, ld_out=512), **kw})
+
+    def nv(e, M=8, N=512, K=256, out=p, dt=0, ws=p, wsb=1 << 30, x=p, w=p, g=p, name="nvfp4_linear_fused"):
+        return getattr(lib, name)(x, M, N, K, w, g, None if e is None else ctypes.byref(e), out, dt, ws, wsb, None)
+
+    def mx(e, M=8, N=512, K=256, out=p, dt=0, ws=p, wsb=1 << 30, x=p, w=p):
+        return lib.mxfp4_linear_fused(x, M, N, K, w, None if e is None else ctypes.byref(e), out, dt, ws, wsb, None)
+
+    def w16(e, **kw):
+        return nv(e, name="nvfp4_linear_w4a16_fused", **kw)
+
+    for f, name in ((nv, "nvfp4_linear_fused"), (w16, "nvfp4_linear_w4a16_fused"), (mx, "mxfp4_linear_fused")):
+        assert f(epi(), M=0, x=None, w=None, out=None) == _lib.NVFP4_OK
+        for bad in (None, epi(act=5), epi(act=-1), epi(gated=2), epi(residual=4096, residual_dtype=2, ld_residual=512)):
+            assert f(bad) == _lib.NVFP4_EINVAL
+            assert _lib.last_error().startswith(name + ":")
+        assert f(epi(), dt=2) == _lib.NVFP4_EINVAL
+        for bad in (epi(ld_out=508), epi(ld_out=514), epi(residual=4096, ld_residual=256),
+                    epi(residual=4096, ld_residual=513), epi(gated=1, ld_out=252)):
+            assert f(bad) == _lib.NVFP4_ESHAPE
+        assert f(epi(gated=1, ld_out=384), N=384) == _lib.NVFP4_ESHAPE and "multiple of 256" in _lib.last_error()
+        assert f(epi(), N=500) == _lib.NVFP4_ESHAPE
+        assert f(epi(), K=100) == _lib.NVFP4_ESHAPE
+        assert f(epi(), M=-1) == _lib.NVFP4_ESHAPE
+        for kw in (dict(out=ctypes.c_void_p(4100)), dict(out=None), dict(x=None), dict(w=None),
+                   dict(x=ctypes.c_void_p(4104)), dict(ws=ctypes.c_void_p(4096 + 128))):
+            assert f(epi(), **kw) == _lib.NVFP4_EINVAL, kw
+        assert f(epi(bias=4098)) == _lib.NVFP4_EINVAL
+        assert f(epi(residual=4100, ld_residual=512)) == _lib.NVFP4_EINVAL
+        assert f(epi(residual=4096 + 8, residual_dtype=1, ld_residual=512)) == _lib.NVFP4_EINVAL
+        assert f(epi(), wsb=0) == _lib.NVFP4_EWORKSPACE and "needed=" in _lib.last_error()
+    assert nv(epi(), g=None) == _lib.NVFP4_EINVAL
+    assert mx(epi(ld_out=1 << 20), M=8, N=1 << 20, K=1 << 14) == _lib.NVFP4_ESHAPE and "4 GiB" in _lib.last_error()

@@ -1,0 +1,321 @@
+"""GPU parity of the dense layers with an epilogue (nvfp4_linear_fused,
+nvfp4_linear_w4a16_fused, mxfp4_linear_fused) against oracle/linear.py and
+oracle/mxfp4.py in FP64.
+
+The operands are exact, so the product v carries FP32 accumulation alone:
+dv = K 2^-23 (|x_hat| |W_hat|^T), as for the layers without an epilogue; the
+scale and the bias round it by 2 half steps more.  The activation passes an
+error on with its largest slope (1.13) and adds its own: the exponential of an
+FP32 argument a is off by |a| half steps, the reciprocal, the products and the
+sum by a few; GELU's erfc by twice the square of its argument.  A gated value
+is a product of two such values.  The residual adds half a step of the sum,
+and a bfloat16 output half a step of its own (2^-8).
+"""
+import functools
+
+import numpy as np
+import pytest
+import torch
+
+from nvfp4_block_scaled_03_amd import _lib, ops
+from oracle import linear as olin
+from oracle import mxfp4 as omx
+from oracle import nvfp4 as onv
+
+from parity import device, to_np
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = ("w4a4", "w4a16", "mxfp4")
+HALF = 2.0 ** -24    # half a step of FP32, relative
+
+
+@pytest.fixture(scope="module")
+def dev():
+    return device()
+
+
+def _gen(dev, seed):
+    return torch.Generator(device=dev).manual_seed(seed)
+
+
+@functools.lru_cache(maxsize=8)
+def _weight(fmt, N, K, gated, seed=3):
+    """(prepared weight, FP64 dequantised weight)"""
+    dev = torch.device("cuda")
+    w = 0.05 * torch.randn(N, K, generator=_gen(dev, seed), device=dev)
+    if fmt == "mxfp4":
+        q, ex = omx.quantize(to_np(w).astype(np.float64))
+        return ops.quantize_mx_weight(w, gated), omx.dequantize(q, ex)
+    c, s, g = olin.quantize_weight(to_np(w))
+    return ops.quantize_linear_weight(w, gated), onv.dequantize(c, s, g)
+
+
+def _x(dev, M, K, seed):
+    x = torch.randn(M, K, generator=_gen(dev, seed), device=dev)
+    x[:, ::97] *= 20.0
+    return x.to(torch.bfloat16)
+
+
+def _operand(fmt, x):
+    xf = to_np(x.float()).astype(np.float64)
+    if fmt == "w4a16":
+        return xf
+    if fmt == "mxfp4":
+        return omx.dequantize(*omx.quantize(xf))
+    g = onv.global_scale(xf)
+    return onv.dequantize(*onv.quantize(xf, g), g)
+
+
+def _act_error(z, dz, act):
+    """Bound of the activation's error for an argument off by dz."""
+    a = np.abs(olin.activation(z, act))
+    if act in ("none", "relu"):
+        return dz
+    if act == "silu":
+        own = 8 + 4 * np.abs(z)
+    elif act == "gelu":
+        own = 16 + 4 * z * z
+    else:
+        own = 16 + 16 * np.abs(1.6 * z * (1 + 0.044715 * z * z))
+    return 1.13 * dz + own * HALF * a + 2.0 ** -120
+
+
+def _reference(fmt, x, w_hat, bias, act, gated, residual, out_dtype):
+    """(FP64 result, bound of the error)"""
+    x_hat = _operand(fmt, x)
+    v = x_hat @ w_hat.T
+    dv = x.shape[1] * 2 * HALF * (np.abs(x_hat) @ np.abs(w_hat).T) + 2 * HALF * np.abs(v)
+    b = None if bias is None else to_np(bias).astype(np.float64)
+    r = None if residual is None else to_np(residual.float()).astype(np.float64)
+    ref = olin.epilogue(v, b, act, gated, r)
+    if b is not None:
+        v = v + b
+        dv = dv + HALF * np.abs(v)
+    if gated:
+        h = v.shape[1] // 2
+        a, u = np.abs(olin.activation(v[:, :h], act)), np.abs(v[:, h:])
+        da, du = _act_error(v[:, :h], dv[:, :h], act), dv[:, h:]
+        err = da * u + a * du + da * du + HALF * a * u
+    else:
+        err = _act_error(v, dv, act)
+    if r is not None:
+        err = err + HALF * (np.abs(ref) + err)
+    if out_dtype == torch.bfloat16:
+        err = err + 2.0 ** -8 * (np.abs(ref) + err)
+    return ref, err + 2.0 ** -125
+
+
+def _call(fmt, x, w, **kw):
+    return ops.mx_linear(x, w, **kw) if fmt == "mxfp4" else ops.linear(x, w, fmt, **kw)
+
+
+def _check(fmt, x, wt, bias, act, gated, residual, got):
+    ref, bound = _reference(fmt, x, wt[1], bias, act, gated, residual, got.dtype)
+    err = np.abs(to_np(got.float()).astype(np.float64) - ref)
+    assert err.shape == bound.shape
+    assert (err <= bound).all(), f"{float((err / bound).max())} times the bound"
+
+
+# (act, gated, bias, residual type, output type)
+CONFIGS = [
+    ("none", False, True, None, torch.bfloat16),
+    ("none", False, False, torch.bfloat16, torch.bfloat16),
+    ("relu", False, True, torch.float32, torch.float32),
+    ("silu", True, False, None, torch.bfloat16),
+    ("gelu", False, True, torch.bfloat16, torch.float32),
+    ("gelu_tanh", True, True, torch.float32, torch.float32),
+]
+
+
+def _case(dev, fmt, M, N, K, cfg, seed=0):
+    act, gated, with_bias, rdt, odt = cfg
+    wt = _weight(fmt, N, K, gated)
+    x = _x(dev, M, K, 100 + M + seed)
+    g = _gen(dev, 200 + M + seed)
+    bias = 0.5 * torch.randn(N, generator=g, device=dev) if with_bias else None
+    n_out = N // 2 if gated else N
+    res = torch.randn(M, n_out, generator=g, device=dev).to(rdt) if rdt else None
+    got = _call(fmt, x, wt[0], bias=bias, act=act, residual=res, out_dtype=odt)
+    assert got.shape == (M, n_out) and got.dtype == odt
+    _check(fmt, x, wt, bias, act, gated, res, got)
+
+
+@pytest.mark.parametrize("cfg", range(len(CONFIGS)))
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 16, 17, 32, 33, 40, 41, 64, 65, 100, 128, 129, 203, 300])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_fused(dev, fmt, M, cfg):
+    _case(dev, fmt, M, 512, 384, CONFIGS[cfg])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(1, 256, 128), (3, 128, 256), (7, 768, 1408), (19, 384, 640), (50, 1280, 128),
+                                   (70, 128, 512), (260, 896, 2048), (1000, 256, 896), (515, 640, 128)])
+def test_fused_sizes(dev, fmt, M, N, K):
+    for cfg in (CONFIGS[3], CONFIGS[4]):
+        if not (cfg[1] and N % 256):
+            _case(dev, fmt, M, N, K, cfg, 7)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_activations_far_out(dev, act, gated):
+    """Arguments from deep in the left tail to far right: the bias carries
+    the argument from -200 to 200."""
+    N, K, M = 512, 128, 9
+    wt = _weight("w4a16", N, K, gated)
+    x = _x(dev, M, K, 5)
+    bias = torch.linspace(-200, 200, N, device=dev)
+    if gated:
+        bias = torch.cat([bias[::2], bias[:N // 2]])
+    got = ops.linear(x, wt[0], "w4a16", bias=bias, act=act, out_dtype=torch.float32)
+    assert torch.isfinite(got).all()
+    _check("w4a16", x, wt, bias, act, gated, None, got)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [1, 3, 30, 70, 200])
+def test_nothing_added_is_the_plain_layer(dev, fmt, M):
+    """A zero bias and residual give the values of the layer without an epilogue."""
+    wt = _weight(fmt, 512, 384, False)
+    x = _x(dev, M, 384, 9)
+    for dt in (torch.float32, torch.bfloat16):
+        plain = _call(fmt, x, wt[0], out_dtype=dt)
+        fused = _call(fmt, x, wt[0], out_dtype=dt, bias=torch.zeros(512, device=dev),
+                      residual=torch.zeros(M, 512, device=dev))
+        if fmt == "mxfp4" or M > 40:
+            assert torch.equal(plain, fused)
+        else:   # few rows: each layer sums K in its own order
+            ref, bound = _reference(fmt, x, wt[1], None, "none", False, None, dt)
+            assert (np.abs(to_np(fused.float()) - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M", [1, 13, 37, 90, 150])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_strides_and_neighbours(dev, fmt, gated, M, dt):
+    """Output and residual inside wider buffers: nothing beside the output's
+    rows and columns is written; then the residual in place."""
+    N, K = 512, 256
+    n_out = N // 2 if gated else N
+    wt = _weight(fmt, N, K, gated)
+    x = _x(dev, M, K, 31)
+    buf = torch.full((M + 2, n_out + 24), 7.0, dtype=dt, device=dev)
+    res = torch.randn(M, n_out + 8, generator=_gen(dev, 8), device=dev).to(dt)[:, 4:4 + n_out]
+    out = buf[1:M + 1, 8:8 + n_out]
+    got = _call(fmt, x, wt[0], act="silu", residual=res, out=out)
+    assert got.data_ptr() == out.data_ptr()
+    _check(fmt, x, wt, None, "silu", gated, res, got)
+    edge = buf.clone()
+    edge[1:M + 1, 8:8 + n_out] = 7
+    assert (edge == 7).all()
+    first = got.clone()
+    out.copy_(res)
+    again = _call(fmt, x, wt[0], act="silu", residual=out, out=out)
+    assert torch.equal(again, first)
+    # a residual of odd stride is taken by copying
+    odd = torch.randn(M, n_out + 1, generator=_gen(dev, 8), device=dev).to(dt)[:, 1:]
+    _check(fmt, x, wt, None, "silu", gated, odd, _call(fmt, x, wt[0], act="silu", residual=odd, out_dtype=dt))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [1, 20, 64, 140])
+def test_rows_and_zeros(dev, fmt, M):
+    """All-zero activations leave act(bias) + residual, exactly for ReLU."""
+    N, K = 256, 256
+    wt = _weight(fmt, N, K, False)
+    bias = torch.randn(N, generator=_gen(dev, 1), device=dev)
+    res = torch.randn(M, N, generator=_gen(dev, 2), device=dev)
+    got = _call(fmt, torch.zeros(M, K, dtype=torch.bfloat16, device=dev), wt[0], bias=bias, act="relu",
+                residual=res, out_dtype=torch.float32)
+    assert torch.equal(got, bias.clamp(min=0) + res)
+
+
+def test_no_rows(dev):
+    for fmt in FORMATS:
+        w = _weight(fmt, 512, 256, True)[0]
+        assert _call(fmt, torch.empty(0, 256, dtype=torch.bfloat16, device=dev), w, act="silu").shape == (0, 256)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [2, 24, 48, 160])
+def test_captured_and_replayed(dev, fmt, M):
+    """Two layers in a row (gated, then with the input as residual) captured
+    once: every replay on new inputs equals the eager run, with eager work of
+    the same buffers in between."""
+    H, I = 256, 384
+    g = _gen(dev, M)
+    up = _weight(fmt, 2 * I, H, True)[0]
+    down = _weight(fmt, H, I, False)[0]
+    x = torch.empty(M, H, dtype=torch.bfloat16, device=dev)
+    h = torch.empty(M, I, dtype=torch.bfloat16, device=dev)
+    y = torch.empty(M, H, dtype=torch.bfloat16, device=dev)
+    if fmt == "mxfp4":
+        ws = [ops.mx_linear_workspace(M, 2 * I, H, dev), ops.mx_linear_workspace(M, H, I, dev)]
+    else:
+        ws = [ops.linear_workspace(M, 2 * I, H, fmt == "w4a4", dev), ops.linear_workspace(M, H, I, fmt == "w4a4", dev)]
+
+    def step():
+        _call(fmt, x, up, act="silu", out=h, ws=ws[0])
+        _call(fmt, h, down, residual=x, out=y, ws=ws[1])
+
+    x.normal_(generator=g)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        x.normal_(generator=g)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(got, y)
+
+
+def test_guard_bands(dev):
+    """Output, residual and workspace between known bytes that stay."""
+    band = 4096
+    for fmt in FORMATS:
+        for M in (1, 9, 37, 100, 257):
+            for gated in (False, True):
+                N, K = 512, 384
+                w = _weight(fmt, N, K, gated)[0]
+                n_out = N // 2 if gated else N
+                wsn = (ops.mx_linear_workspace(M, N, K, dev) if fmt == "mxfp4"
+                       else ops.linear_workspace(M, N, K, fmt == "w4a4", dev)).numel()
+                full = torch.full((2 * band + wsn,), 0xA5, dtype=torch.uint8, device=dev)
+                full[band:band + wsn] = 0
+                o = torch.full((2 * band + M * n_out * 2,), 0xA5, dtype=torch.uint8, device=dev)
+                out = o[band:band + M * n_out * 2].view(torch.bfloat16).view(M, n_out)
+                _call(fmt, _x(dev, M, K, 1), w, act="gelu", bias=torch.zeros(N, device=dev), out=out,
+                      ws=full[band:band + wsn])
+                for t, n in ((full, wsn), (o, M * n_out * 2)):
+                    assert (t[:band] == 0xA5).all() and (t[band + n:] == 0xA5).all(), (fmt, M, gated)
+
+
+def test_refusals(dev):
+    w = _weight("w4a16", 512, 256, True)[0]
+    x = _x(dev, 4, 256, 1)
+    for bad in (dict(act="tanh"), dict(bias=torch.zeros(256, device=dev)),
+                dict(bias=torch.zeros(512, dtype=torch.bfloat16, device=dev)),
+                dict(residual=torch.zeros(4, 512, device=dev)), dict(residual=torch.zeros(4, 256)),
+                dict(out=torch.zeros(4, 512, dtype=torch.bfloat16, device=dev)),
+                dict(out=torch.zeros(4, 257, dtype=torch.bfloat16, device=dev)[:, 1:])):
+        with pytest.raises(ValueError):
+            ops.linear(x, w, "w4a16", **bad)
+    with pytest.raises(ValueError):
+        ops.linear(x, w, "w8a8", act="silu")
+    with pytest.raises(ValueError):
+        ops.linear(x[:, :128], w, "w4a16", act="silu")
+    with pytest.raises(ValueError):
+        ops.linear(x.float(), w, "w4a16", act="silu")
+    with pytest.raises(TypeError):
+        ops.linear(x, w, "w4a16", residual=torch.zeros(4, 256, dtype=torch.float16, device=dev))
+    with pytest.raises(ValueError):
+        ops.quantize_linear_weight(torch.zeros(384, 256, device=dev), gated=True)
+    with pytest.raises(_lib.Nvfp4Error):
+        ops.linear(x, w, "w4a16", act="silu", ws=torch.zeros(256, dtype=torch.uint8, device=dev)[:0])

@@ -85,3 +85,22 @@ def test_matches_single_expert_down_projection():
     off, sp, _ = omoe.align(ids, 1)
     y = omoe.down_and_combine(xh, np.arange(T), sp, off, np.ones((T, 1)), weights, T, 1)
     np.testing.assert_allclose(olin.linear_w4a4(x, wc, ws, gw), y, rtol=1e-13, atol=1e-13)
+
+
+def test_epilogue_by_hand():
+    """Bias, activation, gate and residual on values worked by hand, and each
+    activation against its textbook form."""
+    import math
+
+    v = np.array([[1.0, -2.0, 3.0, 0.5]])
+    b = np.array([0.0, 1.0, -1.0, 0.5])
+    assert olin.epilogue(v).tolist() == v.tolist()
+    assert olin.epilogue(v, b, "relu").tolist() == [[1.0, 0.0, 2.0, 1.0]]
+    # gate (1, -1), up (2, 1): relu(1) * 2, relu(-1) * 1
+    assert olin.epilogue(v, b, "relu", True, np.array([[10.0, 20.0]])).tolist() == [[12.0, 20.0]]
+    for z in (-30.0, -3.0, -0.1, 0.0, 0.7, 5.0, 40.0):
+        u = math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+        want = {"none": z, "relu": max(z, 0.0), "silu": z * 0.5 * (1 + math.tanh(z / 2)),
+                "gelu": z * 0.5 * (1 + math.erf(z / math.sqrt(2))), "gelu_tanh": 0.5 * z * (1 + math.tanh(u))}
+        for act, y in want.items():
+            assert abs(olin.activation(z, act) - y) <= 1e-14 * max(1.0, abs(z))
