@@ -179,8 +179,8 @@ int moe_route_topk(const float* logits, int32_t T, int32_t E, int32_t topk, int3
  * first H of each row used), wg [E][H] in w_dtype (NVFP4_BF16 or NVFP4_F32:
  * routers stay unquantised), bias float32 [E] or NULL.  Products are exact
  * (float32 weights enter as three bfloat16 parts, 24 significant bits, parts
- * below 2^-126 excepted), sums FP32.  1 <= E <= 1024; H and ldx multiples of
- * 8; x and wg 16-byte aligned. */
+ * below 2^-126 excepted), sums FP32.  T <= 2^24, 1 <= E <= 1024; H and ldx
+ * multiples of 8; x and wg 16-byte aligned. */
 int moe_gate(const uint16_t* x, int64_t ldx, const void* wg, int w_dtype, const float* bias, int32_t T, int32_t E,
              int32_t H, float* logits, void* stream);
 
@@ -218,7 +218,7 @@ typedef struct nvfp4_route_params {
  * counts as the largest finite float.  Where a token has fewer available
  * experts than topk, the remaining ids are -1 (dropped by moe_align) with
  * weight 0.  1 <= topk <= min(E, 32), topk <= E / groups * topk_groups,
- * E <= 1024. */
+ * E <= 1024, T <= 2^24. */
 int moe_route(const nvfp4_route_params* params, const void* logits, int dtype, int64_t ldl, const float* bias,
               int32_t T, int32_t E, int32_t topk, int32_t* ids, float* weights, void* stream);
 

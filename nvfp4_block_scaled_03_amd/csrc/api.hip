@@ -132,8 +132,9 @@ int moe_gate(const uint16_t* x, int64_t ldx, const void* wg, int w_dtype, const 
              int32_t H, float* logits, void* stream) {
   const char* W = "moe_gate";
   if (w_dtype != NVFP4_BF16 && w_dtype != NVFP4_F32) return fail(NVFP4_EINVAL, "%s: EINVAL w_dtype=%d", W, w_dtype);
-  if (T < 0 || E < 1 || E > 1024 || H < 8 || H % 8 || ldx < H || ldx % 8)
-    return fail(NVFP4_ESHAPE, "%s: ESHAPE T=%d num_experts=%d H=%d ldx=%lld (1 <= E <= 1024, H and ldx multiples of 8)",
+  if (T < 0 || T > (1 << 24) || E < 1 || E > 1024 || H < 8 || H % 8 || ldx < H || ldx % 8)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE T=%d num_experts=%d H=%d ldx=%lld (T <= 2^24, 1 <= E <= 1024, H and ldx multiples "
+                "of 8)",
                 W, T, E, H, (long long)ldx);
   if (T == 0) return ok();
   if (!x || !wg || !logits) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
@@ -154,8 +155,9 @@ int moe_route(const nvfp4_route_params* p, const void* logits, int dtype, int64_
                 p->renormalize);
   if (!(p->scale > 0.0f && p->scale < INFINITY))
     return fail(NVFP4_EINVAL, "%s: EINVAL scale=%g (positive and finite)", W, (double)p->scale);
-  if (T < 0 || E < 1 || E > 1024 || topk < 1 || topk > E || topk > 32 || ldl < E)
-    return fail(NVFP4_ESHAPE, "%s: ESHAPE T=%d num_experts=%d topk=%d ldl=%lld (1 <= topk <= min(E, 32), E <= 1024)",
+  if (T < 0 || T > (1 << 24) || E < 1 || E > 1024 || topk < 1 || topk > E || topk > 32 || ldl < E)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE T=%d num_experts=%d topk=%d ldl=%lld (T <= 2^24, 1 <= topk <= min(E, 32), "
+                "E <= 1024)",
                 W, T, E, topk, (long long)ldl);
   if (p->groups < 1 || p->groups > 64 || E % p->groups || p->topk_groups < 1 || p->topk_groups > p->groups ||
       topk > E / p->groups * p->topk_groups)
