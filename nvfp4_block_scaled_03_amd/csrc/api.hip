@@ -320,7 +320,7 @@ int moe_mxfp4_quantize_and_align(const nvfp4_moe_dims* d, const uint16_t* x, uin
 namespace {
 // Workspace of nvfp4_linear*: 256-byte aligned sub-buffers in this order.
 struct LinearWs {
-  size_t g, gs, offsets, sorted_pair, inv_pos, plan, align, a_q, a_sf, a_deq, total;
+  size_t g, gs, tiles, offsets, sorted_pair, inv_pos, plan, align, a_q, a_sf, a_deq, total;
 };
 size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 bool linear_shape_ok(int64_t M, int64_t N, int64_t K) {
@@ -334,6 +334,9 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K, bool w4a4) {
   auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
   w.g = take(w4a4 ? 4 : 0);
   w.gs = take(w4a4 ? nvfp4_global_scale_workspace_size(1, std::max<int64_t>(M * K, 8)) : 0);
+  // The fused layers' own kernels use what follows the counter words, which
+  // stay zero between calls of either kind.
+  w.tiles = o;
   w.offsets = take(2 * sizeof(int32_t));
   w.sorted_pair = take((size_t)std::max<int64_t>(M, 1) * 4);
   w.inv_pos = take((size_t)std::max<int64_t>(M, 1) * 4);
@@ -342,7 +345,7 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K, bool w4a4) {
   w.a_q = take(w4a4 ? (size_t)M * (K / 2) : 0);
   w.a_sf = take(w4a4 ? (size_t)M * (K / 16) : 0);
   w.a_deq = take(w4a4 && nvfp4::prefers_decoded((int)M, 1, 1, 0) ? (size_t)M * K * 2 : 0);
-  w.total = o;
+  w.total = std::max(o, w.tiles + up256(nvfp4::linear_tile_ws_bytes(M, N, K)));
   return w;
 }
 
@@ -400,6 +403,8 @@ int linear_run(const char* W, bool w4a4, const uint16_t* x, int64_t M, int64_t N
   if (!aligned(x, 16) || !aligned(w_prep, 16) || !aligned(ws, 256) || (!epi && !aligned(out, 16)))
     return fail(NVFP4_EINVAL, "%s: EINVAL x, w_prep and out 16-byte, ws 256-byte aligned", W);
   uint8_t* b = static_cast<uint8_t*>(ws);
+  if (epi && nvfp4::linear_uses_tiles(M, N, K))
+    return launched(nvfp4::launch_linear_tiles(x, M, N, K, w4a4, w_prep, gw, *epi, b + L.tiles, S(stream)), W);
   nvfp4::AlignShape a = nvfp4::align_shape((int)M, 1, 1, 0);
   a.H = (int)K;
   int32_t* offsets = reinterpret_cast<int32_t*>(b + L.offsets);

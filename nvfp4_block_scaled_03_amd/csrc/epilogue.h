@@ -12,20 +12,42 @@
 
 namespace nvfp4 {
 
-// z / (1 + e^-z): the hardware exponential and reciprocal (1 ulp each).
-__device__ __forceinline__ float act_apply(int act, float z) {
-  switch (act) {   // the same for the whole launch
-    case kFnRelu: return z > 0.0f ? z : 0.0f;
-    case kFnSilu: return silu_fast(z);
-    // x P(X <= x): the complementary error function keeps the relative
-    // accuracy of the left tail, where 1 + erf cancels.
-    case kFnGelu: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+// The activation of N values.  The choice is the same for the whole launch and
+// stands outside the values, so that the code of the others is stepped over
+// once: instruction fetches of code that is run once are a good part of a
+// short kernel's time.
+template <int N>
+__device__ __forceinline__ void act_apply(int act, float (&z)[N]) {
+  switch (act) {
+    case kFnRelu:
+#pragma unroll
+      for (int r = 0; r < N; ++r) z[r] = z[r] > 0.0f ? z[r] : 0.0f;
+      break;
+    // z / (1 + e^-z): the hardware exponential and reciprocal (1 ulp each).
+    case kFnSilu:
+#pragma unroll
+      for (int r = 0; r < N; ++r) z[r] = silu_fast(z[r]);
+      break;
+    // z Phi(z): the complementary error function keeps the relative accuracy
+    // of the left tail, where 1 + erf cancels.
+    case kFnGelu:
+#pragma unroll 1
+      for (int k = 0; k < N; ++k) {   // (rolled: the values turn through one register)
+        const float v = z[0];
+#pragma unroll
+        for (int r = 0; r + 1 < N; ++r) z[r] = z[r + 1];
+        z[N - 1] = 0.5f * v * erfcf(-0.70710678118654752f * v);
+      }
+      break;
     // 0.5 z (1 + tanh u) = z / (1 + e^-2u)
-    case kFnGeluTanh: {
-      const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
-      return z * __builtin_amdgcn_rcpf(1.0f + __expf(-u2));
-    }
-    default: return z;
+    case kFnGeluTanh:
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float u2 = 1.5957691216057308f * (z[r] + 0.044715f * z[r] * z[r] * z[r]);
+        z[r] = z[r] * __builtin_amdgcn_rcpf(1.0f + __expf(-u2));
+      }
+      break;
+    default: break;
   }
 }
 
@@ -82,19 +104,18 @@ __device__ __forceinline__ void epilogue_linear(const LinearEpi& ep, const f32x4
     const float b0 = ep.bias ? ep.bias[col] : 0.0f;
     const float b1 = GATED && ep.bias ? ep.bias[ep.half + col] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i) {
+      float y[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[r] = alpha * acc[i][GATED ? 2 * q : q][r] + b0;
+      act_apply(ep.act, y);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
+        if constexpr (GATED) y[r] *= alpha * acc[i][2 * q + 1][r] + b1;
         const int64_t row = i * 16 + lg * 4 + r;
-        if (row < nrows) {
-          float y;
-          if constexpr (GATED)
-            y = act_apply(ep.act, alpha * acc[i][2 * q][r] + b0) * (alpha * acc[i][2 * q + 1][r] + b1);
-          else
-            y = act_apply(ep.act, alpha * acc[i][q][r] + b0);
-          epi_store(ep, row0 + row, col, y + epi_residual(ep, row0 + row, col));
-        }
+        if (row < nrows) epi_store(ep, row0 + row, col, y[r] + epi_residual(ep, row0 + row, col));
       }
+    }
   }
 }
 
@@ -132,17 +153,13 @@ __device__ __forceinline__ void epilogue_linear_rowmajor(const LinearEpi& ep, co
     for (int ps = 0; ps < 16 / RPP; ++ps) {
       const int64_t row = i * 16 + ps * RPP + rr;
       const float* src = sh + (ps * RPP + rr) * SW;
-      f32x4 y;
-      if constexpr (GATED) {
-        const int cg = (c4 >> 4) * 32 + (c4 & 15);   // gate columns of the pair; the up columns 16 further
-        const f32x4 a = *reinterpret_cast<const f32x4*>(src + cg), u = *reinterpret_cast<const f32x4*>(src + cg + 16);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = act_apply(ep.act, a[j] + b0[j]) * (u[j] + b1[j]);
-      } else {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(src + c4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = act_apply(ep.act, a[j] + b0[j]);
-      }
+      // (gated: gate columns of the pair; the up columns 16 further)
+      const int cg = GATED ? (c4 >> 4) * 32 + (c4 & 15) : c4;
+      const f32x4 a = *reinterpret_cast<const f32x4*>(src + cg) + b0;
+      float z[4] = {a[0], a[1], a[2], a[3]};
+      act_apply(ep.act, z);
+      f32x4 y = {z[0], z[1], z[2], z[3]};
+      if constexpr (GATED) y *= *reinterpret_cast<const f32x4*>(src + cg + 16) + b1;
       if (row < nrows) epi_finish4(ep, row0 + row, col, y);
     }
     // (the next tile rewrites sh only after every lane has read it)

@@ -81,9 +81,9 @@ def _act_error(z, dz, act):
     return 1.13 * dz + own * HALF * a + 2.0 ** -120
 
 
-def _reference(fmt, x, w_hat, bias, act, gated, residual, out_dtype):
+def _reference(fmt, x, w_hat, bias, act, gated, residual, out_dtype, x_hat=None):
     """(FP64 result, bound of the error)"""
-    x_hat = _operand(fmt, x)
+    x_hat = _operand(fmt, x) if x_hat is None else x_hat
     v = x_hat @ w_hat.T
     dv = x.shape[1] * 2 * HALF * (np.abs(x_hat) @ np.abs(w_hat).T) + 2 * HALF * np.abs(v)
     b = None if bias is None else to_np(bias).astype(np.float64)
@@ -150,11 +150,66 @@ def test_fused(dev, fmt, M, cfg):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,N,K", [(1, 256, 128), (3, 128, 256), (7, 768, 1408), (19, 384, 640), (50, 1280, 128),
-                                   (70, 128, 512), (260, 896, 2048), (1000, 256, 896), (515, 640, 128)])
+                                   (70, 128, 512), (260, 896, 2048), (1000, 256, 896), (515, 640, 128),
+                                   # few tiles and a long contraction: split along K and joined
+                                   (1, 128, 16384), (16, 256, 17408), (33, 768, 5120), (64, 640, 8192),
+                                   (100, 1280, 4096), (48, 2560, 6144)])
 def test_fused_sizes(dev, fmt, M, N, K):
     for cfg in (CONFIGS[3], CONFIGS[4]):
         if not (cfg[1] and N % 256):
             _case(dev, fmt, M, N, K, cfg, 7)
+
+
+def _coded_weight(fmt, N, K, gated):
+    """A weight of random codes and scales: (prepared, FP64 dequantised)."""
+    rng = np.random.default_rng(N + K)
+    codes = rng.integers(0, 16, (N, K), dtype=np.uint8)
+    q = torch.from_numpy(codes[:, 0::2] | (codes[:, 1::2] << 4)).cuda()
+    if fmt == "mxfp4":
+        ex = rng.integers(117, 123, (N, K // 32), dtype=np.uint8)
+        return ops.prepare_mx_weight(q, torch.from_numpy(ex).cuda(), gated), omx.dequantize(codes, ex)
+    sf, g = rng.integers(0, 127, (N, K // 16), dtype=np.uint8), np.float32(2.0 ** -14)
+    return (ops.prepare_linear_weight(q, torch.from_numpy(sf).cuda(), torch.tensor([float(g)]).cuda(), gated),
+            onv.dequantize(codes, sf, g))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [
+    # many columns: 64-column workgroups for few rows
+    (1, 32768, 128), (3, 33280, 256), (8, 32768, 256), (16, 32768, 384), (29, 33024, 256),
+    # row blocks of 48 and 64 rows, 128 and 256 columns a tile, N not a multiple of 256
+    (40, 8448, 256), (100, 8192, 384), (37, 8448, 2304), (70, 8320, 2304),
+    # long contractions: chunks dealt out and joined, also with whole rounds before
+    (100, 8320, 4224), (45, 8448, 6144), (333, 8320, 2560),
+    # tiles that fill the device
+    (1024, 8192, 128), (4100, 2048, 256), (515, 13312, 128)])
+def test_fused_large(dev, fmt, M, N, K):
+    gated = N % 256 == 0 and M % 2 == 0
+    wt = _coded_weight(fmt, N, K, gated)
+    x = _x(dev, M, K, M)
+    g = _gen(dev, N)
+    bias = torch.randn(N, generator=g, device=dev)
+    res = torch.randn(M, N // 2 if gated else N, generator=g, device=dev).to(torch.bfloat16)
+    got = _call(fmt, x, wt[0], bias=bias, act="silu", residual=res, out_dtype=torch.float32)
+    rows = np.unique(np.r_[0:min(M, 40), M // 2, max(0, M - 40):M])
+    _check_rows(fmt, x, wt, bias, "silu", gated, res, got, rows)
+    again = _call(fmt, x, wt[0], bias=bias, act="silu", residual=res, out_dtype=torch.float32)
+    assert torch.equal(got, again)
+
+
+def _check_rows(fmt, x, wt, bias, act, gated, residual, got, rows):
+    """_check on some rows (the activations' global scale is that of all)."""
+    at = torch.from_numpy(rows).to(x.device)
+    xs = x[at]
+    if fmt == "w4a4":
+        xf = to_np(x.float()).astype(np.float64)
+        gs = onv.global_scale(xf)
+        x_hat = onv.dequantize(*onv.quantize(xf[rows], gs), gs)
+    else:
+        x_hat = _operand(fmt, xs)
+    ref, bound = _reference(fmt, xs, wt[1], bias, act, gated, residual[at], got.dtype, x_hat)
+    err = np.abs(to_np(got[at].float()).astype(np.float64) - ref)
+    assert (err <= bound).all(), f"{float((err / bound).max())} times the bound"
 
 
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
@@ -176,18 +231,16 @@ def test_activations_far_out(dev, act, gated):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M", [1, 3, 30, 70, 200])
 def test_nothing_added_is_the_plain_layer(dev, fmt, M):
-    """A zero bias and residual give the values of the layer without an epilogue."""
+    """A zero bias and residual give the layer without an epilogue, within
+    its bound (the two may sum K in different orders)."""
     wt = _weight(fmt, 512, 384, False)
     x = _x(dev, M, 384, 9)
     for dt in (torch.float32, torch.bfloat16):
-        plain = _call(fmt, x, wt[0], out_dtype=dt)
-        fused = _call(fmt, x, wt[0], out_dtype=dt, bias=torch.zeros(512, device=dev),
-                      residual=torch.zeros(M, 512, device=dev))
-        if fmt == "mxfp4" or M > 40:
-            assert torch.equal(plain, fused)
-        else:   # few rows: each layer sums K in its own order
-            ref, bound = _reference(fmt, x, wt[1], None, "none", False, None, dt)
-            assert (np.abs(to_np(fused.float()) - ref) <= bound).all()
+        ref, bound = _reference(fmt, x, wt[1], None, "none", False, None, dt)
+        zero = dict(bias=torch.zeros(512, device=dev), residual=torch.zeros(M, 512, device=dev))
+        for kw in ({}, zero):
+            got = _call(fmt, x, wt[0], out_dtype=dt, **kw)
+            assert (np.abs(to_np(got.float()) - ref) <= bound).all()
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
