@@ -5,7 +5,6 @@ current stream.  Names follow include/nvfp4_moe.h.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 import functools
@@ -39,19 +38,23 @@ def _need_cuda(*ts):
             raise ValueError("tensors must live on the GPU")
 
 
-_HERE = contextlib.nullcontext()
+def _raw_stream(device: int) -> int:
+    """Handle of the device's current stream (torch.cuda.current_stream, whose
+    Python object alone takes 2.8 us, most of a short call)."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _device_of(t: torch.Tensor, *others):
-    """Checks that the tensors (None among them) share one GPU; a context in
-    which that GPU is the current device, so that the call runs on its
-    current stream."""
-    if not t.is_cuda:
+def _same_device(device: int, **tensors):
+    """Checks that the tensors (None among them) live on the GPU ``device``."""
+    if device < 0:
         raise ValueError("tensors must live on the GPU")
-    for o in others:
-        if o is not None and o.device != t.device:
-            raise ValueError(f"tensors on {t.device} and {o.device}")
-    return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name} lives on {t.device}, not on GPU {device}")
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _need(cond: bool, what: str):
@@ -112,30 +115,40 @@ def gate_logits(x: torch.Tensor, wg: torch.Tensor, bias: Optional[torch.Tensor] 
                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The router's product: float32 logits [T, E] = x wg^T (+ bias), x bf16
     [T, H], wg [E, H] bf16 or float32, bias float32 [E]."""
-    with _device_of(x, wg, bias, out):
-        _need(x.dim() == 2 and wg.dim() == 2 and wg.shape[1] == x.shape[1], "x [T, H] and wg [E, H]")
-        _need(x.dtype == torch.bfloat16, "x must be bfloat16")
-        T, H = x.shape
-        E = wg.shape[0]
-        if x.stride(1) != 1 or x.stride(0) % 8 or x.stride(0) < H or x.data_ptr() % 16:
-            x = x.contiguous() if not x.is_contiguous() else x.clone()
-        wg = wg.contiguous()
-        if bias is not None:
-            _need(bias.shape == (E,) and bias.dtype == torch.float32, "bias must be float32 [E]")
-            bias = bias.contiguous()
-        if out is None:
-            out = torch.empty(T, E, dtype=torch.float32, device=x.device)
-        _need(out.shape == (T, E) and out.dtype == torch.float32 and out.is_contiguous(),
-              "out must be contiguous float32 [T, E]")
-        call("moe_gate", _p(x), x.stride(0), _p(wg), _dtype_code(wg), _p(bias), T, E, H, _p(out), _stream())
+    dev = x.get_device()
+    _same_device(dev, wg=wg, bias=bias, out=out)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return gate_logits(x, wg, bias, out)
+    if x.dim() != 2 or wg.dim() != 2 or wg.shape[1] != x.shape[1] or x.dtype != torch.bfloat16:
+        raise ValueError("x must be bfloat16 [T, H] and wg [E, H]")
+    T, H = x.shape
+    E = wg.shape[0]
+    ld, one = x.stride()
+    if one != 1 or ld % 8 or ld < H or x.data_ptr() % 16:
+        x = x.clone(memory_format=torch.contiguous_format)
+        ld = H
+    if bias is not None:
+        if bias.shape != (E,) or bias.dtype != torch.float32:
+            raise ValueError("bias must be float32 [E]")
+        bias = bias.contiguous()
+    if out is None:
+        out = torch.empty(T, E, dtype=torch.float32, device=x.device)
+    elif out.shape != (T, E) or out.dtype != torch.float32 or not out.is_contiguous():
+        raise ValueError("out must be contiguous float32 [T, E]")
+    wg = wg.contiguous()
+    call("moe_gate", x.data_ptr(), ld, wg.data_ptr(), _dtype_code(wg), _ptr(bias), T, E, H, out.data_ptr(),
+         _raw_stream(dev))
     return out
 
 
 @functools.lru_cache(maxsize=64)
-def _route_params(score, groups, topk_groups, group_score, renormalize, scale) -> RouteParams:
+def _route_params(score, groups, topk_groups, group_score, renormalize, scale):
+    """The host struct moe_route reads (a function of these values alone)."""
     _need(score in ROUTE_SCORES, f"score must be one of {sorted(ROUTE_SCORES)}")
     _need(group_score in GROUP_SCORES, f"group_score must be one of {sorted(GROUP_SCORES)}")
-    return RouteParams(ROUTE_SCORES[score], groups, topk_groups, GROUP_SCORES[group_score], int(renormalize), scale)
+    return ctypes.pointer(
+        RouteParams(ROUTE_SCORES[score], groups, topk_groups, GROUP_SCORES[group_score], int(renormalize), scale))
 
 
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
@@ -154,24 +167,33 @@ def route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias: Opt
     with ``renormalize``, times ``scale``.  Experts with a logit or bias of
     -inf or NaN are not available; ids that no expert fills are -1."""
     params = _route_params(score, groups, topk_groups, group_score, renormalize, scale)
-    with _device_of(logits, bias, ids, weights):
-        _need(logits.dim() == 2, "logits [T, E]")
-        T, E = logits.shape
-        if logits.stride(1) != 1 or logits.stride(0) < E:
-            logits = logits.contiguous()
-        if bias is not None:
-            _need(bias.shape == (E,) and bias.dtype == torch.float32, "bias must be float32 [E]")
-            bias = bias.contiguous()
-        if ids is None:
-            ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
-        if weights is None:
-            weights = torch.empty(T, k, dtype=torch.float32, device=logits.device)
-        _need(ids.shape == (T, k) and ids.dtype == torch.int32 and ids.is_contiguous(),
-              "ids must be contiguous int32 [T, k]")
-        _need(weights.shape == (T, k) and weights.dtype == torch.float32 and weights.is_contiguous(),
-              "weights must be contiguous float32 [T, k]")
-        call("moe_route", ctypes.byref(params), _p(logits), _dtype_code(logits), max(logits.stride(0), E), _p(bias),
-             T, E, k, _p(ids), _p(weights), _stream())
+    dev = logits.get_device()
+    _same_device(dev, bias=bias, ids=ids, weights=weights)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return route_scored(logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale, ids,
+                                weights)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    ld, one = logits.stride()
+    if one != 1 or ld < E:
+        logits = logits.contiguous()
+        ld = E
+    if bias is not None:
+        if bias.shape != (E,) or bias.dtype != torch.float32:
+            raise ValueError("bias must be float32 [E]")
+        bias = bias.contiguous()
+    if ids is None:
+        ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+    elif ids.shape != (T, k) or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids must be contiguous int32 [T, k]")
+    if weights is None:
+        weights = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+    elif weights.shape != (T, k) or weights.dtype != torch.float32 or not weights.is_contiguous():
+        raise ValueError("weights must be contiguous float32 [T, k]")
+    call("moe_route", params, logits.data_ptr(), _dtype_code(logits), ld, _ptr(bias), T, E, k, ids.data_ptr(),
+         weights.data_ptr(), _raw_stream(dev))
     return ids, weights
 
 
@@ -422,29 +444,39 @@ def _row_stride(t: torch.Tensor) -> int:
 def _linear_fused(name: str, x, w, scale, bias, act, residual, out_dtype, out, ws):
     """The fused call ``name`` after its checks; ``scale``: the weight's
     global scale (NVFP4), or None (MXFP4)."""
-    with _device_of(x, w.prep, bias, residual, out, ws):
-        _need(x.dim() == 2 and x.shape[1] == w.K and x.dtype == torch.bfloat16, f"x must be bfloat16 [M, {w.K}]")
-        _need(act in ACTIVATIONS, f"act must be one of {sorted(ACTIVATIONS)}")
-        M, n_out = x.shape[0], w.N // 2 if w.gated else w.N
-        if out is None:
-            out = torch.empty(M, n_out, dtype=out_dtype, device=x.device)
-        _need(out.shape == (M, n_out) and _rows4(out),
-              f"out must be [{M}, {n_out}] with rows of consecutive elements, starts and strides multiples of 4")
-        epi = Epilogue(ACTIVATIONS[act], int(w.gated), ld_out=_row_stride(out))
-        if bias is not None:
-            _need(bias.shape == (w.N,) and bias.dtype == torch.float32, f"bias must be float32 [{w.N}]")
-            bias = bias.contiguous()
-            epi.bias = bias.data_ptr()
-        if residual is not None:
-            _need(residual.shape == (M, n_out), f"residual must be [{M}, {n_out}]")
-            if not _rows4(residual):
-                residual = residual.clone(memory_format=torch.contiguous_format)
-            epi.residual, epi.residual_dtype = residual.data_ptr(), _dtype_code(residual)
-            epi.ld_residual = _row_stride(residual)
-        x = x.contiguous()
-        operands = (_p(x), M, w.N, w.K, _p(w.prep)) if scale is None else (_p(x), M, w.N, w.K, _p(w.prep), _p(scale))
-        call(name, *operands, ctypes.byref(epi), _p(out), _dtype_code(out), _p(ws),
-             ws.numel() * ws.element_size(), _stream())
+    dev = x.get_device()
+    _same_device(dev, weight=w.prep, bias=bias, residual=residual, out=out, ws=ws)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _linear_fused(name, x, w, scale, bias, act, residual, out_dtype, out, ws)
+    N, K = w.N, w.K
+    if x.dim() != 2 or x.shape[1] != K or x.dtype != torch.bfloat16:
+        raise ValueError(f"x must be bfloat16 [M, {K}]")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    M, n_out = x.shape[0], N // 2 if w.gated else N
+    if out is None:
+        out = torch.empty(M, n_out, dtype=out_dtype, device=x.device)
+    elif out.shape != (M, n_out) or not _rows4(out):
+        raise ValueError(f"out must be [{M}, {n_out}] with rows of consecutive elements, starts and strides "
+                         "multiples of 4")
+    epi = Epilogue(ACTIVATIONS[act], int(w.gated), ld_out=_row_stride(out))
+    if bias is not None:
+        if bias.shape != (N,) or bias.dtype != torch.float32:
+            raise ValueError(f"bias must be float32 [{N}]")
+        bias = bias.contiguous()
+        epi.bias = bias.data_ptr()
+    if residual is not None:
+        if residual.shape != (M, n_out):
+            raise ValueError(f"residual must be [{M}, {n_out}]")
+        if not _rows4(residual):
+            residual = residual.clone(memory_format=torch.contiguous_format)
+        epi.residual, epi.residual_dtype = residual.data_ptr(), _dtype_code(residual)
+        epi.ld_residual = _row_stride(residual)
+    x = x.contiguous()
+    weight = (w.prep.data_ptr(),) if scale is None else (w.prep.data_ptr(), scale.data_ptr())
+    call(name, x.data_ptr(), M, N, K, *weight, epi, out.data_ptr(), _dtype_code(out), ws.data_ptr(),
+         ws.numel() * ws.element_size(), _raw_stream(dev))
     return out
 
 
@@ -462,7 +494,8 @@ def linear(x: torch.Tensor, w: LinearWeight, variant: str = "w4a4", out_dtype=to
     M = x.shape[0]
     w4a4 = variant == "w4a4"
     if bias is not None or act != "none" or residual is not None or w.gated:
-        _need(variant in ("w4a4", "w4a16"), f"variant {variant!r}: w4a4 or w4a16")
+        if variant not in ("w4a4", "w4a16"):
+            raise ValueError(f"variant {variant!r}: w4a4 or w4a16")
         ws = ws if ws is not None else linear_workspace(M, w.N, w.K, w4a4, x.device)
         return _linear_fused("nvfp4_linear_fused" if w4a4 else "nvfp4_linear_w4a16_fused", x, w, w.g, bias, act,
                              residual, out_dtype, out, ws)
