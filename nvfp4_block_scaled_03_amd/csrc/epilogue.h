@@ -168,4 +168,132 @@ __device__ __forceinline__ void epilogue_linear_rowmajor(const LinearEpi& ep, co
   }
 }
 
+// What the epilogue reads for four consecutive output columns of a row,
+// requested ahead of their use (the residual as stored).
+template <int N>
+struct EpiIn {
+  float b0[4], b1[4];
+  u32x4 res[N];
+};
+template <bool GATED, int N>
+__device__ __forceinline__ void epi_request_bias(const LinearEpi& ep, int64_t col, EpiIn<N>& d) {
+  if (!ep.bias) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    d.b0[j] = ep.bias[col + j];
+    if constexpr (GATED) d.b1[j] = ep.bias[ep.half + col + j];
+  }
+}
+__device__ __forceinline__ void epi_request_res(const LinearEpi& ep, int64_t row, int64_t col, u32x4& d) {
+  if (!ep.res) return;
+  const int64_t i = row * ep.ldr + col;
+  if (ep.res_f32) {
+    d = *reinterpret_cast<const u32x4*>(static_cast<const float*>(ep.res) + i);
+  } else {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(ep.res) + i);
+    d[0] = w[0];
+    d[1] = w[1];
+  }
+}
+template <bool GATED>
+__device__ __forceinline__ void epi_request(const LinearEpi& ep, int64_t row, int64_t col, EpiIn<1>& d) {
+  epi_request_bias<GATED>(ep, col, d);
+  epi_request_res(ep, row, col, d.res[0]);
+}
+// Finishes four output columns from col of N rows: z the products (gated: the
+// gates; u the up projections), row[n] < 0: none.
+template <bool GATED, int N>
+__device__ __forceinline__ void epi_finish(const LinearEpi& ep, float (&z)[4 * N], const f32x4 (&u)[N],
+                                           const EpiIn<N>& in, const int64_t (&row)[N], int64_t col) {
+  if (ep.bias) {
+#pragma unroll
+    for (int k = 0; k < 4 * N; ++k) z[k] += in.b0[k % 4];
+  }
+  act_apply(ep.act, z);
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    f32x4 y = {z[4 * n], z[4 * n + 1], z[4 * n + 2], z[4 * n + 3]};
+    if constexpr (GATED) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] *= ep.bias ? u[n][j] + in.b1[j] : u[n][j];
+    }
+    if (ep.res) {
+      if (ep.res_f32) {
+        y += __builtin_bit_cast(f32x4, in.res[n]);
+      } else {
+        y[0] += bf16_bits_to_f32(in.res[n][0] & 0xFFFFu);
+        y[1] += bf16_bits_to_f32(in.res[n][0] >> 16);
+        y[2] += bf16_bits_to_f32(in.res[n][1] & 0xFFFFu);
+        y[3] += bf16_bits_to_f32(in.res[n][1] >> 16);
+      }
+    }
+    if (row[n] < 0) continue;
+    const int64_t o = row[n] * ep.ldo + col;
+    if (ep.out_f32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(ep.out) + o) = y;
+    } else {
+      const uint32_t lo = f32_to_bf16_bits(y[0]) | (f32_to_bf16_bits(y[1]) << 16);
+      const uint32_t hi = f32_to_bf16_bits(y[2]) | (f32_to_bf16_bits(y[3]) << 16);
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(ep.out) + o) = u32x2{lo, hi};
+    }
+  }
+}
+
+// First streaming column, within a tile, of the thread's four output columns
+// (gated: of the gate; its up columns lie 16 further).
+template <bool GATED>
+__device__ __forceinline__ int tile_col(int c4) {
+  return GATED ? (c4 >> 4) * 32 + (c4 & 15) : c4;
+}
+
+// Finishes ROWS rows of column block nb (BN streaming columns) of a workgroup's
+// tile out of LDS: row_of(r) is row r's row of the output, sum(at) the four
+// products at float `at` of LDS, in rows of BN + 4.  A thread keeps its four
+// columns and walks down the rows, N at a time; the residuals of the next N are
+// requested before the present ones are finished.
+template <bool GATED, int ROWS, int BN, int THREADS, class RowOf, class Sum>
+__device__ __forceinline__ void emit_tile(const LinearEpi& ep, int64_t M, int64_t n_all, int64_t nb,
+                                          const RowOf& row_of, const Sum& sum) {
+  constexpr int SW = BN + 4, OUTC = GATED ? BN / 2 : BN, STEP = THREADS / (OUTC / 4),
+                N = ROWS >= 4 * STEP ? 4 : ROWS >= 2 * STEP ? 2 : 1;
+  static_assert(THREADS % (OUTC / 4) == 0, "a thread's columns stay");
+  const int r0 = threadIdx.x / (OUTC / 4), c4 = threadIdx.x % (OUTC / 4) * 4, src = tile_col<GATED>(c4);
+  const int64_t col = nb * OUTC + c4;
+  if (col >= (GATED ? n_all / 2 : n_all)) return;
+  EpiIn<N> in;
+  u32x4 ahead[N];
+  auto row_at = [&](int r) {
+    const int64_t row = r < ROWS ? (int64_t)row_of(r) : M;
+    return row < M ? row : -1;
+  };
+  auto request = [&](int r) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int64_t row = row_at(r + n * STEP);
+      if (row >= 0) epi_request_res(ep, row, col, ahead[n]);
+    }
+  };
+  epi_request_bias<GATED>(ep, col, in);
+  request(r0);
+#pragma unroll 1
+  for (int r = r0; r < ROWS; r += N * STEP) {
+    int64_t row[N];
+    f32x4 u[N];
+    float z[4 * N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) in.res[n] = ahead[n];
+    request(r + N * STEP);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      row[n] = row_at(r + n * STEP);
+      const int at = row[n] < 0 ? src : (r + n * STEP) * SW + src;
+      const f32x4 v = sum(at);
+      if constexpr (GATED) u[n] = sum(at + 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[4 * n + j] = v[j];
+    }
+    epi_finish<GATED, N>(ep, z, u, in, row, col);
+  }
+}
+
 }  // namespace nvfp4

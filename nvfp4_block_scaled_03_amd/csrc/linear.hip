@@ -191,78 +191,6 @@ struct TileParams {
 // First chunk (over the streamed tiles, in order) of workgroup b's run.
 __device__ __forceinline__ int stream_start(const TileSplit& t, int b) { return b * t.run + min(b, t.extra); }
 
-// What the epilogue reads for four consecutive output columns of a row,
-// requested ahead of their use (the residual as stored).
-struct EpiIn {
-  float b0[4], b1[4];
-  u32x4 res;
-};
-template <bool GATED>
-__device__ __forceinline__ void epi_request(const LinearEpi& ep, int64_t row, int64_t col, EpiIn& d) {
-  if (ep.bias) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      d.b0[j] = ep.bias[col + j];
-      if constexpr (GATED) d.b1[j] = ep.bias[ep.half + col + j];
-    }
-  }
-  if (ep.res) {
-    const int64_t i = row * ep.ldr + col;
-    if (ep.res_f32) {
-      d.res = *reinterpret_cast<const u32x4*>(static_cast<const float*>(ep.res) + i);
-    } else {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(ep.res) + i);
-      d.res[0] = w[0];
-      d.res[1] = w[1];
-    }
-  }
-}
-// Finishes N times four output columns: z the products (gated: the gates; u
-// the up projections), row[n] < 0: none.
-template <bool GATED, int N>
-__device__ __forceinline__ void epi_finish(const LinearEpi& ep, float (&z)[4 * N], const f32x4 (&u)[N],
-                                           const EpiIn (&in)[N], const int64_t (&row)[N], const int64_t (&col)[N]) {
-  if (ep.bias) {
-#pragma unroll
-    for (int k = 0; k < 4 * N; ++k) z[k] += in[k / 4].b0[k % 4];
-  }
-  act_apply(ep.act, z);
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    f32x4 y = {z[4 * n], z[4 * n + 1], z[4 * n + 2], z[4 * n + 3]};
-    if constexpr (GATED) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] *= ep.bias ? u[n][j] + in[n].b1[j] : u[n][j];
-    }
-    if (ep.res) {
-      if (ep.res_f32) {
-        y += __builtin_bit_cast(f32x4, in[n].res);
-      } else {
-        y[0] += bf16_bits_to_f32(in[n].res[0] & 0xFFFFu);
-        y[1] += bf16_bits_to_f32(in[n].res[0] >> 16);
-        y[2] += bf16_bits_to_f32(in[n].res[1] & 0xFFFFu);
-        y[3] += bf16_bits_to_f32(in[n].res[1] >> 16);
-      }
-    }
-    if (row[n] < 0) continue;
-    const int64_t o = row[n] * ep.ldo + col[n];
-    if (ep.out_f32) {
-      *reinterpret_cast<f32x4*>(static_cast<float*>(ep.out) + o) = y;
-    } else {
-      const uint32_t lo = f32_to_bf16_bits(y[0]) | (f32_to_bf16_bits(y[1]) << 16);
-      const uint32_t hi = f32_to_bf16_bits(y[2]) | (f32_to_bf16_bits(y[3]) << 16);
-      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(ep.out) + o) = u32x2{lo, hi};
-    }
-  }
-}
-
-// First streaming column, within a tile, of the thread's four output columns
-// (gated: of the gate; its up columns lie 16 further).
-template <bool GATED>
-__device__ __forceinline__ int tile_col(int c4) {
-  return GATED ? (c4 >> 4) * 32 + (c4 & 15) : c4;
-}
-
 // Sends rows [i0, i0 + 16 PM) of every wavefront row of a finished tile out of
 // LDS: sh holds SUMS copies of [WR 16 PM][SW], added in order.  Whole tiles are
 // finished, parts of one go to the workspace.
@@ -286,39 +214,7 @@ __device__ __forceinline__ void emit_rows(const TileParams& p, const float* sh, 
     }
     return;
   }
-  // Four fours of columns a thread at a time: their biases and residuals are
-  // requested together.
-  constexpr int OUTC = GATED ? BN / 2 : BN, TOTAL = ROWS * (OUTC / 4), N = TOTAL >= 4 * THREADS ? 4 : 2;
-  const int64_t cols = GATED ? p.N / 2 : p.N;
-#pragma unroll 1
-  for (int at0 = threadIdx.x; at0 < TOTAL; at0 += N * THREADS) {
-    EpiIn in[N];
-    int64_t row[N], col[N];
-    int src[N];
-    f32x4 u[N];
-    float z[4 * N];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int at = at0 + n * THREADS, r = at / (OUTC / 4), c4 = at % (OUTC / 4) * 4;
-      row[n] = row0 + tile_row(r);
-      col[n] = (int64_t)nb * OUTC + c4;
-      src[n] = r * SW + tile_col<GATED>(c4);
-      if (at >= TOTAL || row[n] >= p.M || col[n] >= cols) {
-        row[n] = -1;
-        src[n] = 0;
-      } else {
-        epi_request<GATED>(p.ep, row[n], col[n], in[n]);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const f32x4 v = sum(src[n]);
-      if constexpr (GATED) u[n] = sum(src[n] + 16);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) z[4 * n + j] = v[j];
-    }
-    epi_finish<GATED, N>(p.ep, z, u, in, row, col);
-  }
+  emit_tile<GATED, ROWS, BN, THREADS>(p.ep, p.M, p.N, nb, [&](int r) { return row0 + tile_row(r); }, sum);
 }
 
 // A workgroup's work: whole tiles, then its run over the streamed tiles.
@@ -581,8 +477,8 @@ __global__ __launch_bounds__(256) void linear_join_kernel(TileParams p) {
     const int r = r0 + at / (outc / 4), c4 = at % (outc / 4) * 4;
     const int64_t row = (int64_t)mb * BM + r, col = (int64_t)nb * outc + c4;
     if (row >= p.M || col >= cols) continue;
-    EpiIn in[1];
-    epi_request<GATED>(p.ep, row, col, in[0]);
+    EpiIn<1> in;
+    epi_request<GATED>(p.ep, row, col, in);
     const float* src = p.part + (int64_t)r * BN + tile_col<GATED>(c4);
     f32x4 v = {0.f, 0.f, 0.f, 0.f}, up[1] = {v};
     auto slot = [&](int b) {
@@ -596,7 +492,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(TileParams p) {
       if constexpr (GATED) up[0] += *reinterpret_cast<const f32x4*>(s + 16);
     }
     float z[4] = {v[0], v[1], v[2], v[3]};
-    epi_finish<GATED, 1>(p.ep, z, up, in, {row}, {col});
+    epi_finish<GATED, 1>(p.ep, z, up, in, {row}, col);
   }
 }
 
@@ -764,14 +660,14 @@ __global__ __launch_bounds__(KW * kWave) void linear_few_kernel(FewParams p) {
   // The thread's first four output columns: what the epilogue reads for them
   // is requested behind the first chunk.
   constexpr int OUTC = GATED ? BN / 2 : BN, TOTAL = BM * (OUTC / 4);
-  EpiIn in[1];
+  EpiIn<1> in;
   int64_t row_out[1] = {(int64_t)mb * BM + threadIdx.x / (OUTC / 4)};
-  int64_t col_out[1] = {(int64_t)nb * OUTC + threadIdx.x % (OUTC / 4) * 4};
+  int64_t col_out = (int64_t)nb * OUTC + threadIdx.x % (OUTC / 4) * 4;
   const bool on = (int)threadIdx.x < TOTAL && row_out[0] < p.M;
   if (c_lo < c_hi) {
     Chunk d0, d1;   // (past the end: the last chunk, not used)
     load(c_lo, d0);
-    if (on) epi_request<GATED>(p.ep, row_out[0], col_out[0], in[0]);
+    if (on) epi_request<GATED>(p.ep, row_out[0], col_out, in);
     load(min(c_lo + 1, c_hi - 1), d1);
     for (int c = c_lo; c < c_hi; c += 2) {
       __builtin_amdgcn_sched_barrier(0);
@@ -784,7 +680,7 @@ __global__ __launch_bounds__(KW * kWave) void linear_few_kernel(FewParams p) {
       }
     }
   } else if (on) {
-    epi_request<GATED>(p.ep, row_out[0], col_out[0], in[0]);
+    epi_request<GATED>(p.ep, row_out[0], col_out, in);
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -797,9 +693,9 @@ __global__ __launch_bounds__(KW * kWave) void linear_few_kernel(FewParams p) {
   for (int at = threadIdx.x; at < TOTAL; at += KW * kWave) {
     const int r = at / (OUTC / 4), c4 = at % (OUTC / 4) * 4;
     row_out[0] = (int64_t)mb * BM + r;
-    col_out[0] = (int64_t)nb * OUTC + c4;
+    col_out = (int64_t)nb * OUTC + c4;
     if (row_out[0] >= p.M) break;   // (rows ascend)
-    if (at != (int)threadIdx.x) epi_request<GATED>(p.ep, row_out[0], col_out[0], in[0]);
+    if (at != (int)threadIdx.x) epi_request<GATED>(p.ep, row_out[0], col_out, in);
     auto sum = [&](int col) {
       f32x4 v = *reinterpret_cast<const f32x4*>(sh + r * SW + col);
 #pragma unroll

@@ -140,14 +140,14 @@ struct MxRing {
 // are outstanding (the LDS and export counters left at their maxima).
 constexpr int mx_vmcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 
-// Epilogue of the dense kernels: the product alone (kMxOutBf16, kMxOutF32) or
-// that of the fused layers (epilogue.h).
+// Output of the dense kernels: the product alone (kMxOutBf16, kMxOutF32) or
+// the fused layers' epilogue (epilogue.h; the ring kernel).
 enum MxOut { kMxOutBf16 = 0, kMxOutF32 = 1, kMxOutLinear = 2, kMxOutGated = 3 };
 
 template <int WM, int D, int OUT>
 __global__ __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(WM, WM))) void mx_gemm_kernel(
     const uint8_t* __restrict__ a_q, const uint8_t* __restrict__ a_e, int64_t M, int64_t N, int64_t K,
-    const uint8_t* __restrict__ w_prep, void* __restrict__ out, LinearEpi ep) {
+    const uint8_t* __restrict__ w_prep, void* __restrict__ out, LinearEpi ep, int64_t tn0, int64_t TN) {
   using R = MxRing<WM>;
   static_assert(D >= 2 && (D - 2) * R::Loads <= 63, "ring depth");
   constexpr int ROWS = 128 * WM, MT = 8, NTW = 4, NBW = 4 / WM;
@@ -155,14 +155,14 @@ __global__ __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(WM, WM
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wv >> 2, wn = wv & 3;
-  const int64_t TM = (M + ROWS - 1) / ROWS, TN = (N + 255) / 256, tiles = TM * TN;
+  const int64_t TM = (M + ROWS - 1) / ROWS, tiles = TM * TN;   // column tiles tn0 .. tn0 + TN - 1
   const int64_t per_xcd = (tiles + 7) / 8;
   const int64_t L = (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
   if (L >= tiles) return;
   const int64_t grp = L / (NVFP4_MX_GM * TN);
   const int64_t gh = min((int64_t)NVFP4_MX_GM, TM - grp * NVFP4_MX_GM);
   const int64_t Lg = L - grp * NVFP4_MX_GM * TN;
-  const int64_t tm = grp * NVFP4_MX_GM + Lg % gh, tn = Lg / gh;
+  const int64_t tm = grp * NVFP4_MX_GM + Lg % gh, tn = tn0 + Lg / gh;
   const int64_t m0 = tm * ROWS;
   const int64_t n_wave0 = tn * 256 + wn * 64;
   const bool wave_on = n_wave0 < N;
@@ -269,12 +269,31 @@ __global__ __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(WM, WM
   // Drain the direct loads still in flight (chunks past the end) before the
   // workgroup's LDS can be handed to another workgroup.
   __builtin_amdgcn_s_waitcnt(mx_vmcnt(0));
-  if (!wave_on) return;
   const int64_t mw0 = m0 + wm * 128;
   if constexpr (OUT == kMxOutLinear || OUT == kMxOutGated) {
-    epilogue_linear<OUT == kMxOutGated, MT, NTW>(ep, acc, 1.0f, mw0, M - mw0, n_wave0, lane);
+    // Half of the rows at a time through LDS, so that they leave, and residuals
+    // come, in whole rows.
+    constexpr int PM = MT / 2, SW = 260;
+    static_assert(WM * 16 * PM * SW * 4 <= D * R::Slot, "staging space");
+    float* const sh = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < PM; ++i)
+#pragma unroll
+        for (int j = 0; j < NTW; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            sh[((wm * PM + i) * 16 + fg * 4 + r) * SW + wn * 64 + 16 * j + fr] = acc[h * PM + i][j][r];
+      __syncthreads();
+      emit_tile<OUT == kMxOutGated, WM * 16 * PM, 256, 256 * WM>(
+          ep, M, N, tn, [&](int r) { return m0 + (r / (16 * PM)) * 128 + h * 16 * PM + r % (16 * PM); },
+          [&](int at) { return *reinterpret_cast<const f32x4*>(sh + at); });
+    }
     return;
   }
+  if (!wave_on) return;
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -301,7 +320,7 @@ __global__ __launch_bounds__(256) void mx_gemm_splitk_kernel(const uint8_t* __re
                                                              const uint8_t* __restrict__ a_e, int64_t M,
                                                              int64_t N, int64_t K,
                                                              const uint8_t* __restrict__ w_prep,
-                                                             void* __restrict__ out, LinearEpi ep) {
+                                                             void* __restrict__ out) {
   __shared__ f32x4 red[3][MT][NTW][64];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int fr = lane & 15, fg = lane >> 4;
@@ -374,10 +393,6 @@ __global__ __launch_bounds__(256) void mx_gemm_splitk_kernel(const uint8_t* __re
       }
       acc[i][j] = v;
     }
-  if constexpr (OUT == kMxOutLinear || OUT == kMxOutGated) {
-    epilogue_linear<OUT == kMxOutGated, MT, NTW>(ep, acc, 1.0f, 0, M, nt0 * 16, lane);
-    return;
-  }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -393,33 +408,217 @@ __global__ __launch_bounds__(256) void mx_gemm_splitk_kernel(const uint8_t* __re
       }
 }
 
+// The fused layers with few rows, or few enough tiles for one workgroup per CU:
+// 16 MT rows x 16 NT columns a workgroup, whose KW wavefronts split K.  The
+// next chunk's operands are in flight while the present one is multiplied (the
+// codes are the instruction's operands as stored, so a chunk is a few
+// instructions and the time is the weight stream); the partial sums meet in LDS
+// and leave in whole rows.
+struct MxFewParams {
+  int M, N, K;
+  int n0;                // first column
+  const uint8_t* a_q;    // operand layout
+  const uint8_t* a_e;
+  const uint8_t* w;      // streaming layout
+  LinearEpi ep;
+};
+template <bool GATED, int MT, int NT, int KW>
+__global__ __launch_bounds__(KW * 64) void mx_few_kernel(MxFewParams p) {
+  constexpr int BM = 16 * MT, BN = 16 * NT, SW = BN + 4;
+  // One row block and many columns: the weights, read once, pass the caches by
+  // (34816 x 5120, M = 1 / 16: 22.5 / 23.0 us against 24.2 / 24.5).
+  constexpr bool ONCE = MT < 4 && NT == 4;
+  static_assert(NT == 2 || NT == 4, "column tiles of one scale word");
+  __shared__ __attribute__((aligned(16))) float sh[KW * BM * SW];
+  const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+  const int kw = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  // Row blocks are the faster index, eight workgroups apart in launch order,
+  // so that those of one column block share an XCD's L2.
+  const int rb = (p.M + BM - 1) / BM;
+  const int grp = blockIdx.x / (8 * rb), rem = blockIdx.x - grp * 8 * rb, nb = p.n0 / BN + grp * 8 + (rem & 7), mb = rem >> 3;
+  if (nb * BN >= p.N) return;
+  const int KC = p.K / 128, nt0 = nb * NT;
+  const int c_lo = KC * kw / KW, c_hi = KC * (kw + 1) / KW;
+  const uint8_t* wq = p.w + ((int64_t)nt0 * KC * 64 + lane) * 16;
+  const uint8_t* we = p.w + (int64_t)p.N * (p.K / 2) + ((int64_t)(nt0 >> 2) * KC * 64 + lane) * 4;
+  const int w_shift = (nt0 & 3) * 8;   // this workgroup's bytes of the scale word
+  // (with several row blocks MT is 4, so that a block's tiles share scale
+  // words; the operand's rows are padded with zeros to 64)
+  const uint8_t* aq = p.a_q + ((int64_t)mb * MT * KC * 64 + lane) * 16;
+  const uint8_t* ae = p.a_e + ((int64_t)mb * KC * 64 + lane) * 4;
+  struct Chunk {
+    u32x4 w[NT], a[MT];
+    uint32_t ws, as;
+  };
+  auto load = [&](int c, Chunk& d) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const u32x4* at = reinterpret_cast<const u32x4*>(wq + ((int64_t)j * KC + c) * 1024);
+      if constexpr (ONCE) d.w[j] = __builtin_nontemporal_load(at);
+      else d.w[j] = *at;
+    }
+    d.ws = *reinterpret_cast<const uint32_t*>(we + (int64_t)c * 256);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) d.a[i] = *reinterpret_cast<const u32x4*>(aq + ((int64_t)i * KC + c) * 1024);
+    d.as = *reinterpret_cast<const uint32_t*>(ae + (int64_t)c * 256);
+  };
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const Chunk& d) {
+    const int ws = (int)(d.ws >> w_shift);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const v8i av = {(int)d.a[i][0], (int)d.a[i][1], (int)d.a[i][2], (int)d.a[i][3], 0, 0, 0, 0};
+      const int as = (int)((d.as >> (8 * i)) & 0xFFu);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const v8i bv = {(int)d.w[j][0], (int)d.w[j][1], (int)d.w[j][2], (int)d.w[j][3], 0, 0, 0, 0};
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[i][j], 4, 4, 0, as, 0,
+                                                                    (ws >> (8 * j)) & 0xFF);
+      }
+    }
+  };
+  constexpr int OUTC = GATED ? BN / 2 : BN, TOTAL = BM * (OUTC / 4);
+  EpiIn<1> in;
+  int64_t row[1] = {(int64_t)mb * BM + threadIdx.x / (OUTC / 4)};
+  int64_t col = (int64_t)nb * OUTC + threadIdx.x % (OUTC / 4) * 4;
+  const bool on = (int)threadIdx.x < TOTAL && row[0] < p.M;
+  if (c_lo < c_hi) {
+    Chunk d0, d1;   // (past the end: the last chunk, not used)
+    load(c_lo, d0);
+    if (on) epi_request<GATED>(p.ep, row[0], col, in);
+    load(min(c_lo + 1, c_hi - 1), d1);
+    for (int c = c_lo; c < c_hi; c += 2) {
+      __builtin_amdgcn_sched_barrier(0);
+      compute(d0);
+      load(min(c + 2, c_hi - 1), d0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (c + 1 < c_hi) {
+        compute(d1);
+        load(min(c + 3, c_hi - 1), d1);
+      }
+    }
+  } else if (on) {
+    epi_request<GATED>(p.ep, row[0], col, in);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sh[(kw * BM + i * 16 + lg * 4 + r) * SW + 16 * j + ln] = acc[i][j][r];
+  __syncthreads();
+#pragma unroll 1
+  for (int at = threadIdx.x; at < TOTAL; at += KW * 64) {
+    const int r = at / (OUTC / 4), c4 = at % (OUTC / 4) * 4;
+    row[0] = (int64_t)mb * BM + r;
+    col = (int64_t)nb * OUTC + c4;
+    if (row[0] >= p.M) break;   // (rows ascend)
+    if (at != (int)threadIdx.x) epi_request<GATED>(p.ep, row[0], col, in);
+    auto sum = [&](int cc) {
+      f32x4 v = *reinterpret_cast<const f32x4*>(sh + r * SW + cc);
+#pragma unroll
+      for (int k = 1; k < KW; ++k) v += *reinterpret_cast<const f32x4*>(sh + (k * BM + r) * SW + cc);
+      return v;
+    };
+    const int src = tile_col<GATED>(c4);
+    const f32x4 v = sum(src), up[1] = {GATED ? sum(src + 16) : v};
+    float z[4] = {v[0], v[1], v[2], v[3]};
+    epi_finish<GATED, 1>(p.ep, z, up, in, row, col);
+  }
+}
+
+template <bool GATED, int MT, int NT, int KW>
+hipError_t launch_mx_few_t(const MxFewParams& p, hipStream_t s) {
+  const unsigned rb = (unsigned)((p.M + 16 * MT - 1) / (16 * MT)), groups = (unsigned)(((p.N - p.n0) / (16 * NT) + 7) / 8);
+  mx_few_kernel<GATED, MT, NT, KW><<<groups * 8 * rb, KW * 64, 0, s>>>(p);
+  return hipGetLastError();
+}
+template <bool GATED, int MT>
+hipError_t launch_mx_few(const MxFewParams& p, hipStream_t s) {
+  // Columns and wavefronts by the number of 64 x 64 pieces (us, the whole
+  // layer): 32 columns and 8 wavefronts while CUs would be left without work
+  // (5120 x 17408, 80 pieces: 23.1 against 28.8 with 64 columns), then 64
+  // columns, which read the activations half as often, with fewer wavefronts
+  // as there are more workgroups: 160 pieces 29.0 with 8, 32.2 with 4; 320:
+  // 45.7 with 4, 49.2 with 8; 640: 62.4 with 2, 68.6 with 4.
+  const int64_t pieces = (p.M + 63) / 64 * ((p.N - p.n0) / 64);
+  if (pieces < 160 || (MT < 4 && pieces < 512)) return launch_mx_few_t<GATED, MT, 2, 8>(p, s);
+  if constexpr (MT == 4) {
+    if (pieces < 320) return launch_mx_few_t<GATED, MT, 4, 8>(p, s);
+    if (pieces < 640) return launch_mx_few_t<GATED, MT, 4, 4>(p, s);
+  }
+  return launch_mx_few_t<GATED, MT, 4, 2>(p, s);
+}
+template <bool GATED>
+hipError_t launch_mx_few(const MxFewParams& p, hipStream_t s) {
+  if (p.M <= 16) return launch_mx_few<GATED, 1>(p, s);
+  if (p.M <= 32) return launch_mx_few<GATED, 2>(p, s);
+  return launch_mx_few<GATED, 4>(p, s);
+}
+
 template <int MT, int NTW, int UB, int OUT>
 hipError_t launch_mx_splitk(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
-                            const uint8_t* w_prep, void* out, const LinearEpi& ep, hipStream_t s) {
+                            const uint8_t* w_prep, void* out, hipStream_t s) {
   const dim3 grid((unsigned)(N / (16 * NTW)));
-  mx_gemm_splitk_kernel<MT, NTW, UB, OUT><<<grid, 256, 0, s>>>(a_q, a_e, M, N, K, w_prep, out, ep);
+  mx_gemm_splitk_kernel<MT, NTW, UB, OUT><<<grid, 256, 0, s>>>(a_q, a_e, M, N, K, w_prep, out);
   return hipGetLastError();
 }
 
 template <int WM, int OUT>
 hipError_t launch_mx_gemm_ring(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
-                               const uint8_t* w_prep, void* out, const LinearEpi& ep, hipStream_t s) {
-  const int64_t tiles = ((M + 128 * WM - 1) / (128 * WM)) * ((N + 255) / 256);
+                               const uint8_t* w_prep, void* out, const LinearEpi& ep, int64_t tn0, int64_t TN,
+                               hipStream_t s) {
+  const int64_t tiles = ((M + 128 * WM - 1) / (128 * WM)) * TN;
   const unsigned grid = (unsigned)(8 * ((tiles + 7) / 8));
-  mx_gemm_kernel<WM, NVFP4_MX_DEPTH, OUT><<<grid, 256 * WM, 0, s>>>(a_q, a_e, M, N, K, w_prep, out, ep);
+  mx_gemm_kernel<WM, NVFP4_MX_DEPTH, OUT><<<grid, 256 * WM, 0, s>>>(a_q, a_e, M, N, K, w_prep, out, ep, tn0, TN);
   return hipGetLastError();
 }
 
 template <int OUT>
 hipError_t launch_mx_gemm_out(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
-                              const uint8_t* w_prep, void* out, const LinearEpi& ep, hipStream_t s) {
+                              const uint8_t* w_prep, void* out, hipStream_t s) {
   // N is a multiple of 128, so NTW <= 8 column tiles divide it.
-  if (M <= 16) return launch_mx_splitk<1, NVFP4_MX_NTW1, NVFP4_MX_UB1, OUT>(a_q, a_e, M, N, K, w_prep, out, ep, s);
-  if (M <= 32) return launch_mx_splitk<2, NVFP4_MX_NTW2, NVFP4_MX_UB2, OUT>(a_q, a_e, M, N, K, w_prep, out, ep, s);
-  if (M <= 64) return launch_mx_splitk<4, NVFP4_MX_NTW4, NVFP4_MX_UB4, OUT>(a_q, a_e, M, N, K, w_prep, out, ep, s);
+  if (M <= 16) return launch_mx_splitk<1, NVFP4_MX_NTW1, NVFP4_MX_UB1, OUT>(a_q, a_e, M, N, K, w_prep, out, s);
+  if (M <= 32) return launch_mx_splitk<2, NVFP4_MX_NTW2, NVFP4_MX_UB2, OUT>(a_q, a_e, M, N, K, w_prep, out, s);
+  if (M <= 64) return launch_mx_splitk<4, NVFP4_MX_NTW4, NVFP4_MX_UB4, OUT>(a_q, a_e, M, N, K, w_prep, out, s);
   // up to 128 rows: one 128-row tile (4 wavefronts); more: 256-row tiles
-  if (M <= 128) return launch_mx_gemm_ring<1, OUT>(a_q, a_e, M, N, K, w_prep, out, ep, s);
-  return launch_mx_gemm_ring<2, OUT>(a_q, a_e, M, N, K, w_prep, out, ep, s);
+  const int64_t TN = (N + 255) / 256;
+  const LinearEpi none{};
+  if (M <= 128) return launch_mx_gemm_ring<1, OUT>(a_q, a_e, M, N, K, w_prep, out, none, 0, TN, s);
+  return launch_mx_gemm_ring<2, OUT>(a_q, a_e, M, N, K, w_prep, out, none, 0, TN, s);
+}
+
+// The fused layers: 256 x 256 tiles in whole rounds of one a CU (256 of them),
+// and the columns left over by whichever of three is fastest.  Counted in
+// 64 x 64 pieces of the kernel for few rows, whose time follows their number,
+// a round of f <= 256 tiles costs 1200 + 5.8 f in 256 x 256 tiles (16 f
+// pieces) and 850 + 3.1 f in 128 x 256 tiles (8 f); fitted to sweeps of 7
+// weights from 8192 x 512 to 34816 x 5120 with M = 128 .. 4096, e.g. (us, few
+// rows / 128 / 256 rows): 8192 x 8192 M = 512 45 / 69 / 80, M = 1000 88 / 72 /
+// 84, M = 1300 102 / 131 / 88, M = 2048 154 / 140 / 101.
+template <bool GATED>
+hipError_t launch_mx_fused(const MxFewParams& p, hipStream_t s) {
+  constexpr int OUT = GATED ? kMxOutGated : kMxOutLinear;
+  const int64_t M = p.M, TN = ((int64_t)p.N + 255) / 256, TM = (M + 255) / 256, TM1 = (M + 127) / 128;
+  int64_t whole = M <= 128 ? 0 : TM * TN / 256 * 256 / TM;   // column tiles in whole rounds
+  if (M > 128) {
+    const int64_t rest = TN - whole, f1 = TM1 * rest;
+    if (f1 > 256) whole = TN;
+    if (whole) {
+      const hipError_t e = launch_mx_gemm_ring<2, OUT>(p.a_q, p.a_e, M, p.N, p.K, p.w, nullptr, p.ep, 0, whole, s);
+      if (e != hipSuccess || whole == TN) return e;
+    }
+    const int64_t pieces = (M + 63) / 64 * ((p.N - whole * 256) / 64);
+    if (10 * pieces > 8500 + 31 * f1)
+      return launch_mx_gemm_ring<1, OUT>(p.a_q, p.a_e, M, p.N, p.K, p.w, nullptr, p.ep, whole, rest, s);
+  }
+  MxFewParams few = p;
+  few.n0 = (int)(whole * 256);
+  return launch_mx_few<GATED>(few, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -1105,14 +1304,21 @@ hipError_t launch_mx_prep(int64_t N, int64_t K, const uint8_t* q, const uint8_t*
 
 hipError_t launch_mx_gemm(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
                           const uint8_t* w_prep, void* out, int out_dtype, hipStream_t s) {
-  return out_dtype ? launch_mx_gemm_out<kMxOutF32>(a_q, a_e, M, N, K, w_prep, out, LinearEpi{}, s)
-                   : launch_mx_gemm_out<kMxOutBf16>(a_q, a_e, M, N, K, w_prep, out, LinearEpi{}, s);
+  return out_dtype ? launch_mx_gemm_out<kMxOutF32>(a_q, a_e, M, N, K, w_prep, out, s)
+                   : launch_mx_gemm_out<kMxOutBf16>(a_q, a_e, M, N, K, w_prep, out, s);
 }
 
 hipError_t launch_mx_gemm_fused(const uint8_t* a_q, const uint8_t* a_e, int64_t M, int64_t N, int64_t K,
                                 const uint8_t* w_prep, const LinearEpi& ep, hipStream_t s) {
-  return ep.gated ? launch_mx_gemm_out<kMxOutGated>(a_q, a_e, M, N, K, w_prep, nullptr, ep, s)
-                  : launch_mx_gemm_out<kMxOutLinear>(a_q, a_e, M, N, K, w_prep, nullptr, ep, s);
+  MxFewParams p{};
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.a_q = a_q;
+  p.a_e = a_e;
+  p.w = w_prep;
+  p.ep = ep;
+  return ep.gated ? launch_mx_fused<true>(p, s) : launch_mx_fused<false>(p, s);
 }
 
 }  // namespace nvfp4

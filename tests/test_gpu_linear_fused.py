@@ -197,6 +197,26 @@ def test_fused_large(dev, fmt, M, N, K):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("M,N,K,gated", [
+    # 160 .. 639 pieces of 64 x 64: each width and count of wavefronts
+    (130, 4096, 128, False), (250, 5120, 384, True), (330, 5120, 128, False), (333, 8192, 256, True),
+    # a whole round of 256 x 256 tiles, the columns left over in 64-row blocks ...
+    (300, 33024, 128, False), (300, 33024, 256, True), (512, 34816, 128, False),
+    # ... in 128-row tiles, N not a multiple of 256 in the last column tile
+    (260, 60032, 128, False), (500, 60160, 128, True),
+    # 128-row and 256-row tiles alone
+    (1000, 8192, 256, True), (1900, 8320, 128, False), (2100, 8448, 256, True)])
+def test_mx_rounds(dev, M, N, K, gated):
+    wt = _coded_weight("mxfp4", N, K, gated)
+    x = _x(dev, M, K, M)
+    g = _gen(dev, N)
+    bias = torch.randn(N, generator=g, device=dev)
+    res = torch.randn(M, N // 2 if gated else N, generator=g, device=dev).to(torch.bfloat16)
+    got = _call("mxfp4", x, wt[0], bias=bias, act="silu", residual=res, out_dtype=torch.float32)
+    rows = np.unique(np.r_[0:20, 60:70, 120:135, 250:262, M // 2, M - 40:M])
+    _check_rows("mxfp4", x, wt, bias, "silu", gated, res, got, rows[rows < M])
+
+
 def _check_rows(fmt, x, wt, bias, act, gated, residual, got, rows):
     """_check on some rows (the activations' global scale is that of all)."""
     at = torch.from_numpy(rows).to(x.device)
