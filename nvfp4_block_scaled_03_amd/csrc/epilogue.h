@@ -91,8 +91,8 @@ __device__ __forceinline__ void epi_finish4(const LinearEpi& e, int64_t row, int
 // instruction's layout (lane 16 g + n: rows 4 g .. 4 g + 3 of column n), rows
 // row0 + [0, nrows), streaming columns n0 + [0, 16 NTW).  GATED: the column
 // tiles alternate gate and up, and column n of pair q is output column
-// n0 / 2 + 16 q + n.  One store per value: few rows, or no LDS to turn the
-// tile in.
+// n0 / 2 + 16 q + n.  One store per value: the LDS-staged kernel for operands
+// past 2 GiB, whose product takes long.
 template <bool GATED, int MT, int NTW>
 __device__ __forceinline__ void epilogue_linear(const LinearEpi& ep, const f32x4 (&acc)[MT][NTW], float alpha,
                                                 int64_t row0, int64_t nrows, int64_t n0, int lane) {

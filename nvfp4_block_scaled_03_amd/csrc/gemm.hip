@@ -1353,21 +1353,17 @@ __global__ __launch_bounds__(4 * kWave) void linear_splitk_kernel(KParams p) {
     }
     sum[0][j] = v;
   }
-  if constexpr (linear_epi(EPI)) {
-    epilogue_linear<EPI == kEpiLinearGated, 1, NTW>(p.ep, sum, alpha, 0, M, nt0 * 16, lane);
-  } else {
 #pragma unroll
-    for (int j = 0; j < NTW; ++j)
+  for (int j = 0; j < NTW; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int rr = g * 4 + r;
-        if (rr < M) {
-          const int64_t o = (int64_t)rr * N + (nt0 + j) * 16 + m;
-          if constexpr (EPI == kEpiStoreF32) p.out_f32[o] = alpha * sum[0][j][r];
-          else p.out_h[o] = (uint16_t)f32_to_bf16_bits(alpha * sum[0][j][r]);
-        }
+    for (int r = 0; r < 4; ++r) {
+      const int rr = g * 4 + r;
+      if (rr < M) {
+        const int64_t o = (int64_t)rr * N + (nt0 + j) * 16 + m;
+        if constexpr (EPI == kEpiStoreF32) p.out_f32[o] = alpha * sum[0][j][r];
+        else p.out_h[o] = (uint16_t)f32_to_bf16_bits(alpha * sum[0][j][r]);
       }
-  }
+    }
 }
 
 
@@ -1540,10 +1536,10 @@ hipError_t launch_gemm1(const GemmArgs& a, bool w4a4, hipStream_t s) {
   return launch_gemm<kActBf16, kEpiSwigluBf16>(k, al, s, a.part);
 }
 
-// One dense layer with epilogue EPI: few rows on the split-K kernel, else the
-// grouped kernels' rules with one expert.
+// One plain dense layer: few rows on the split-K kernel, else the grouped
+// kernels' rules with one expert.
 template <int EPI>
-static hipError_t launch_linear_epi(const LinearArgs& a, const KParams& k, const AlignShape& al, hipStream_t s) {
+static hipError_t launch_linear_plain(const LinearArgs& a, const KParams& k, const AlignShape& al, hipStream_t s) {
   // Few rows from codes (at most 16) or bf16 (at most 4): K split over the
   // 4 wavefronts of a workgroup per 32 columns (N is a multiple of 128).
   // Measured at N = 34816, K = 5120: M = 1 W4A4 33.0 -> 30.3 us, W4A16
@@ -1559,6 +1555,24 @@ static hipError_t launch_linear_epi(const LinearArgs& a, const KParams& k, const
   if (!a.w4a4) return launch_gemm<kActBf16, EPI>(k, al, s, kPartAll);
   if (a.a_h) return launch_gemm<kActF16, EPI>(k, al, s, kPartAll);
   return launch_gemm<kActCodes, EPI>(k, al, s, kPartAll);
+}
+
+// A fused dense layer whose tiles fill the device (linear_uses_tiles says
+// no): the wide kernel, or the LDS-staged one where a 32-bit buffer offset
+// would not reach the end of an operand.
+template <int AK, int EPI>
+static hipError_t launch_linear_fused(KParams k, const AlignShape& al, hipStream_t s) {
+  k.list_idx = 3;   // 128-row tiles
+  const int len = (int)al.list_len[3];
+  const bool offsets_fit = k.a_rows * 2 * k.K < (int64_t(1) << 31) && (int64_t)k.N * k.K / 2 < (int64_t(1) << 31);
+  if (!offsets_fit) return launch_lds<AK, EPI, 128, NVFP4_BIG_WN>(k, len, s);
+  if constexpr (AK == kActF16)
+    if (al.list_len[3] * ((k.N + 255) / 256) <= NVFP4_SMALL_WIDE_GRID) return launch_wide<AK, EPI, 32>(k, len, s);
+  return launch_wide<AK, EPI>(k, len, s);
+}
+template <int AK>
+static hipError_t launch_linear_fused(const KParams& k, const AlignShape& al, hipStream_t s) {
+  return k.ep.gated ? launch_linear_fused<AK, kEpiLinearGated>(k, al, s) : launch_linear_fused<AK, kEpiLinear>(k, al, s);
 }
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
@@ -1580,14 +1594,15 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   k.a_h = a.a_h;
   if (a.epi) {
     k.ep = *a.epi;
-    return a.epi->gated ? launch_linear_epi<kEpiLinearGated>(a, k, al, s) : launch_linear_epi<kEpiLinear>(a, k, al, s);
+    if (!a.a_h || linear_uses_tiles(a.M, a.N, a.K)) return hipErrorInvalidValue;
+    return a.w4a4 ? launch_linear_fused<kActF16>(k, al, s) : launch_linear_fused<kActBf16>(k, al, s);
   }
   if (a.out_dtype) {
     k.out_f32 = static_cast<float*>(a.out);
-    return launch_linear_epi<kEpiStoreF32>(a, k, al, s);
+    return launch_linear_plain<kEpiStoreF32>(a, k, al, s);
   }
   k.out_h = static_cast<uint16_t*>(a.out);
-  return launch_linear_epi<kEpiStoreBf16>(a, k, al, s);
+  return launch_linear_plain<kEpiStoreBf16>(a, k, al, s);
 }
 
 hipError_t launch_combine(const float* d, const int32_t* inv_pos, const float* topk_w, int T, int topk,

@@ -195,7 +195,8 @@ struct LinearArgs {
   const uint16_t* a_h;     // the exact f16 copy (W4A4) / bf16 x (W4A16)
   void* out;
   int out_dtype;           // 0 bf16, 1 f32
-  const LinearEpi* epi;    // host pointer, or null: y alone (out, out_dtype)
+  const LinearEpi* epi;    // host pointer (only if !linear_uses_tiles, with a_h), or null: y alone
+                           // (out, out_dtype)
 };
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 

@@ -136,7 +136,7 @@ __global__ __launch_bounds__(256) void linear_operand_kernel(const uint16_t* __r
 }
 
 // ---------------------------------------------------------------------------
-// Product and epilogue.  The output is cut into tiles of BM = 16 MT WR rows x
+// Product and epilogue.  The output is cut into tiles of BM = 16 MT rows x
 // BN = 64 CW columns.  A resident workgroup takes whole tiles as long as there
 // is one for every workgroup; the remaining tiles' chunks of K are dealt to
 // all workgroups in equal runs (stream), so that no CU waits for another at
@@ -145,20 +145,24 @@ __global__ __launch_bounds__(256) void linear_operand_kernel(const uint16_t* __r
 // finishes it.  The split depends on the sizes alone: results repeat bit for
 // bit.
 //
-// A workgroup's WR x CW x KW wavefronts: each owns 16 MT rows x 64 columns,
-// and the KW groups split the chunks of a run.  The activations of a chunk go
-// from memory straight into LDS, once for the group's wavefronts, double
-// buffered.  What bounds the kernel where weights do not is the traffic from
-// L2 to the CUs, about 12 TB/s over the device: with each wavefront loading
-// its own activation fragments, 64 rows x 64 columns each, M = 64, N = 34816,
-// K = 5120 moved 435 MB and took 34 us.  The weights of the chunk after next
-// are requested as soon as the registers of the present one are read.
+// A workgroup's CW x KW wavefronts: each owns 16 MT rows x 64 columns, and the
+// KW groups split the chunks of a run.  The activations of a chunk go into LDS
+// once for the group's wavefronts, double buffered.  What bounds the kernel
+// where weights do not is the traffic from L2 to the CUs, about 12 TB/s over
+// the device: with each wavefront loading its own activation fragments, 64 rows
+// x 64 columns each, M = 64, N = 34816, K = 5120 moved 435 MB and took 34 us.
+// The weights of the chunk after next are requested as soon as the registers
+// of the present one are read.  Measured, whole layers: W4A4 34816 x 5120
+// M = 64 47.6 us, of which the activations take 9.6 (maximum, quantisation),
+// the product 33 and the join 5; M = 128 67 us (678 TFLOP/s); W4A16
+// 5120 x 17408 M = 512 123 us (742 TFLOP/s).
 // ---------------------------------------------------------------------------
 constexpr int kNT = 4;        // column tiles of a wavefront: 64 columns
 constexpr int kCUs = 256;
-// Dealing out chunks pays where it takes more than this many chunks off the
-// longest path (the join is a launch and a round trip of the partial sums);
-// a run is at least kMinRun chunks.
+// Dealing out chunks pays where it takes more than kJoinChunks chunks (of 0.3
+// to 0.5 us) off the longest path: the join is a launch and a round trip of the
+// partial sums, about 5 us.  A run is at least kMinRun chunks, so that its
+// start (the first loads' way from memory) stays the smaller part.
 constexpr int kJoinChunks = 16, kMinRun = 8;
 
 // s_waitcnt immediate: at most n vector memory operations outstanding (the
@@ -191,30 +195,28 @@ struct TileParams {
 // First chunk (over the streamed tiles, in order) of workgroup b's run.
 __device__ __forceinline__ int stream_start(const TileSplit& t, int b) { return b * t.run + min(b, t.extra); }
 
-// Sends rows [i0, i0 + 16 PM) of every wavefront row of a finished tile out of
-// LDS: sh holds SUMS copies of [WR 16 PM][SW], added in order.  Whole tiles are
-// finished, parts of one go to the workspace.
-template <bool GATED, int MT, int WR, int PM, int BN, int SUMS, int THREADS>
+// Sends a tile out of LDS: sh holds SUMS copies of [BM][BN + 4], added in
+// order.  Whole tiles are finished, parts of one go to the workspace.
+template <bool GATED, int BM, int BN, int SUMS, int THREADS>
 __device__ __forceinline__ void emit_rows(const TileParams& p, const float* sh, float alpha, float* part, int mb,
-                                          int nb, int i0) {
-  constexpr int SW = BN + 4, ROWS = 16 * PM * WR, BM = 16 * MT * WR;
+                                          int nb) {
+  constexpr int SW = BN + 4;
   auto sum = [&](int at) {
     f32x4 v = *reinterpret_cast<const f32x4*>(sh + at);
 #pragma unroll
-    for (int k = 1; k < SUMS; ++k) v += *reinterpret_cast<const f32x4*>(sh + k * ROWS * SW + at);
+    for (int k = 1; k < SUMS; ++k) v += *reinterpret_cast<const f32x4*>(sh + k * BM * SW + at);
     return alpha * v;
   };
   const int64_t row0 = (int64_t)mb * BM;
-  auto tile_row = [&](int r) { return (r / (16 * PM)) * 16 * MT + i0 * 16 + r % (16 * PM); };
   if (part) {
 #pragma unroll 4
-    for (int at = threadIdx.x; at < ROWS * (BN / 4); at += THREADS) {
-      const int r = at / (BN / 4), c4 = at % (BN / 4) * 4, tr = tile_row(r);
-      if (row0 + tr < p.M) *reinterpret_cast<f32x4*>(part + (int64_t)tr * BN + c4) = sum(r * SW + c4);
+    for (int at = threadIdx.x; at < BM * (BN / 4); at += THREADS) {
+      const int r = at / (BN / 4), c4 = at % (BN / 4) * 4;
+      if (row0 + r < p.M) *reinterpret_cast<f32x4*>(part + (int64_t)r * BN + c4) = sum(r * SW + c4);
     }
     return;
   }
-  emit_tile<GATED, ROWS, BN, THREADS>(p.ep, p.M, p.N, nb, [&](int r) { return row0 + tile_row(r); }, sum);
+  emit_tile<GATED, BM, BN, THREADS>(p.ep, p.M, p.N, nb, [&](int r) { return row0 + r; }, sum);
 }
 
 // A workgroup's work: whole tiles, then its run over the streamed tiles.
@@ -265,19 +267,20 @@ struct TileWork {
 // multiply chunk t from LDS buffer t & 1, request chunk t + D's weights into
 // the registers just read, put chunk t + 1's activations into the other
 // buffer.  The next piece's first requests precede the end of the present one.
-template <bool BF16, bool GATED, int MT, int WR, int CW, int KW, int D, int WPE>
-__global__ __launch_bounds__(WR * CW * KW * kWave) __attribute__((amdgpu_waves_per_eu(WPE, WPE)))
+template <bool BF16, bool GATED, int MT, int CW, int KW>
+__global__ __launch_bounds__(CW * KW * kWave) __attribute__((amdgpu_waves_per_eu(CW * KW / 4, CW * KW / 4)))
 void linear_tile_kernel(TileParams p) {
-  constexpr int G = WR * CW, THREADS = G * KW * kWave;
-  constexpr int BM = 16 * MT * WR, BN = 64 * CW, SW = BN + 4;
-  constexpr int STAGE = MT * WR * 4096;                 // activations of a chunk
+  constexpr int THREADS = CW * KW * kWave;
+  constexpr int D = 2;   // (3: 1 to 2 us slower, for the registers)
+  constexpr int BM = 16 * MT, BN = 64 * CW, SW = BN + 4;
+  constexpr int STAGE = MT * 4096;                 // activations of a chunk
   constexpr int LPW = MT * 4 / CW;                      // of which each wavefront moves LPW KiB
   static_assert(MT * 4 % CW == 0, "whole loads per wavefront");
   constexpr int RING = KW * 2 * STAGE, EPI = KW * BM * SW * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[RING > EPI ? RING : EPI];
   const int tid = threadIdx.x, lane = tid & 63, ln = lane & 15, lg = lane >> 4, l16 = lane * 16;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int kw = wv / G, wg = wv % G, wr = wg / CW, wc = wg % CW;
+  const int kw = wv / CW, wc = wv % CW;
   const int KC = p.K / kBK, row_tiles = (p.M + 15) >> 4, col_tiles = p.N / 16, GS = scale_group(KC);
   const float alpha = p.g_a ? ld_uniform(p.g_a) * ld_uniform(p.g_w) : ld_uniform(p.g_w);
   uint8_t* const ring = lds + kw * 2 * STAGE;
@@ -317,12 +320,12 @@ void linear_tile_kernel(TileParams p) {
                                             kBufferFlags);
     P.s = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w_sf + (int64_t)(nt0 >> 1) * KC * 256), (short)0, 0x7FFFFFFF,
                                             kBufferFlags);
-    P.a = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + (int64_t)k.mb * MT * WR * KC * 2048), (short)0, 0x7FFFFFFF,
+    P.a = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + (int64_t)k.mb * MT * KC * 2048), (short)0, 0x7FFFFFFF,
                                             kBufferFlags);
 #pragma unroll
     for (int q = 0; q < LPW; ++q) {
-      const int at = wg * LPW + q;
-      P.va[q] = l16 + min(at / 4, row_tiles - 1 - k.mb * MT * WR) * KC * 4096 + at % 4 * 1024;
+      const int at = wc * LPW + q;
+      P.va[q] = l16 + min(at / 4, row_tiles - 1 - k.mb * MT) * KC * 4096 + at % 4 * 1024;
     }
     return P;
   };
@@ -345,7 +348,7 @@ void linear_tile_kernel(TileParams p) {
   auto put_a = [&](int buf, const A& d) {
 #pragma unroll
     for (int q = 0; q < LPW; ++q)
-      *reinterpret_cast<u32x4*>(ring + buf * STAGE + (wg * LPW + q) * 1024 + l16) = d.v[q];
+      *reinterpret_cast<u32x4*>(ring + buf * STAGE + (wc * LPW + q) * 1024 + l16) = d.v[q];
   };
   W w[D];
   A a[2];
@@ -373,7 +376,7 @@ void linear_tile_kernel(TileParams p) {
     typedef typename std::conditional<BF16, bf16x8, f16x8>::type frag;
     constexpr int VALU = BF16 ? 16 : 8;                 // instructions of a decode
     auto compute = [&](int buf, const W& w) {
-      const uint8_t* st = ring + buf * STAGE + wr * MT * 4096 + l16;
+      const uint8_t* st = ring + buf * STAGE + l16;
       f16x2 scale[kNT];
 #pragma unroll
       for (int j = 0; j < kNT; ++j) scale[j] = e4m3x2_to_f16x2(w.s[j >> 1] >> ((j & 1) * 16));
@@ -445,9 +448,9 @@ void linear_tile_kernel(TileParams p) {
       for (int j = 0; j < kNT; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          sh[(kw * BM + (wr * MT + i) * 16 + lg * 4 + r) * SW + wc * 64 + j * 16 + ln] = acc[i][j][r];
+          sh[(kw * BM + i * 16 + lg * 4 + r) * SW + wc * 64 + j * 16 + ln] = acc[i][j][r];
     __syncthreads();
-    emit_rows<GATED, MT, WR, MT, BN, KW, THREADS>(p, sh, alpha, done.part(p, KC), done.mb, done.nb, 0);
+    emit_rows<GATED, BM, BN, KW, THREADS>(p, sh, alpha, done.part(p, KC), done.mb, done.nb);
     if (!more) break;
     __syncthreads();                                    // LDS is free for the next piece
   }
@@ -496,20 +499,19 @@ __global__ __launch_bounds__(256) void linear_join_kernel(TileParams p) {
   }
 }
 
-// Cases of launch_tile: row tiles of a wavefront, wavefronts over rows,
-// columns and K, depth of the requests, resident workgroups per CU.
+// Cases of launch_tile: row tiles, wavefronts over columns and over K.
 struct TileCfg {
-  int mt, wr, cw, kw, depth, per_cu;
+  int mt, cw, kw;
 };
-constexpr TileCfg kTileCfgs[] = {{3, 1, 2, 4, 2, 1}, {4, 1, 2, 4, 2, 1}, {3, 1, 4, 2, 2, 1}, {4, 1, 4, 2, 2, 1}};
+constexpr TileCfg kTileCfgs[] = {{3, 2, 4}, {4, 2, 4}, {3, 4, 2}, {4, 4, 2}};
 
 TileSplit tile_split_as(int cfg, int64_t M, int64_t N, int64_t K) {
   const TileCfg c = kTileCfgs[cfg];
   TileSplit t{};
   t.cfg = cfg;
-  t.bm = 16 * c.mt * c.wr;
+  t.bm = 16 * c.mt;
   t.bn = 64 * c.cw;
-  const int KC = (int)(K / kBK), slots = c.per_cu * kCUs;
+  const int KC = (int)(K / kBK), slots = kCUs;   // one workgroup per CU
   t.row_blocks = (int)((M + t.bm - 1) / t.bm);
   t.col_blocks = (int)((N + t.bn - 1) / t.bn);
   const int64_t tiles = (int64_t)t.row_blocks * t.col_blocks;
@@ -529,7 +531,9 @@ TileSplit tile_split_as(int cfg, int64_t M, int64_t N, int64_t K) {
 }
 
 // Row blocks of even height; 128 columns a workgroup where the tiles are few
-// and short, else 256.
+// and short, else 256.  Measured (us, the whole W4A16 layer, 128 / 256 columns):
+// 4096 x 1024 M = 256 15.7 / 19.8, 8192 x 512 M = 256 13.9 / 16.0; longer or
+// more of them: 8192 x 8192 M = 128 38.6 / 36.2, 34816 x 5120 M = 64 54 / 48.
 TileSplit tile_split(int64_t M, int64_t N, int64_t K) {
   const int64_t tiles = (M + 15) / 16, blocks = (tiles + 3) / 4;
   const bool low = (tiles + blocks - 1) / blocks <= 3;
@@ -540,8 +544,8 @@ TileSplit tile_split(int64_t M, int64_t N, int64_t K) {
 template <bool BF16, bool GATED, int CFG>
 hipError_t launch_tile(const TileParams& p, hipStream_t s) {
   constexpr TileCfg c = kTileCfgs[CFG];
-  constexpr int waves = c.wr * c.cw * c.kw;
-  linear_tile_kernel<BF16, GATED, c.mt, c.wr, c.cw, c.kw, c.depth, c.per_cu * waves / 4>
+  constexpr int waves = c.cw * c.kw;
+  linear_tile_kernel<BF16, GATED, c.mt, c.cw, c.kw>
       <<<(unsigned)p.t.grid, waves * kWave, 0, s>>>(p);
   if (p.t.stream > 0)
     linear_join_kernel<GATED><<<(unsigned)(p.t.stream * (p.t.bm / kJoinRows)), 256, 0, s>>>(p);
@@ -559,13 +563,22 @@ hipError_t launch_tiles(const TileParams& p, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// At most 32 rows: the weight stream decides, so the grid is wide (16 NT
-// columns a workgroup) and the KW wavefronts of a workgroup split K.  The next
-// chunk's operands are in flight while the present one is multiplied; the
-// partial sums meet in LDS and leave in rows.  Activations (ACT): bf16 rows as
-// they are, for a handful of rows (more rows would put neighbouring lanes in
-// different lines); codes and scales, likewise; or 16-bit values in the
-// operand layout, MT row tiles.
+// Few rows: the weight stream decides, so the grid is wide (16 NT columns a
+// workgroup) and the KW wavefronts of a workgroup split K.  The next chunk's
+// operands are in flight while the present one is multiplied; the partial sums
+// meet in LDS and leave in rows.  Activations (ACT): bf16 rows as they are, for
+// a handful of rows (more rows would put neighbouring lanes in different
+// lines); codes and scales, likewise; or 16-bit values in the operand layout,
+// MT row tiles.  Measured: one row of W4A16 34816 x 5120, 100 MB of weight,
+// 26.0 us (3.9 TB/s, two loads of 16 bytes a lane in flight per column tile);
+// 131072 x 8192, 604 MB, 5.8 TB/s.
+//
+// W4A4 quantises to codes in one launch, each workgroup taking the maximum over
+// all of x, up to kFewQuantMax elements: 5120 x 17408 M = 4 24.4 us against
+// 27.2 with the maximum in a launch of its own and the operand layout, M = 8
+// 28.7 against 27.5, 8192 x 8192 M = 16 23.5 against 20.5.  W4A16 reads x as it
+// is up to kFewRowsMax rows: M = 16 34816 x 5120 38.0 us against 33.5 with the
+// operand layout, 5120 x 17408 28.8 against 23.9 (4096 x 1024 6.2 against 6.7).
 // ---------------------------------------------------------------------------
 constexpr int64_t kFewQuantMax = 98304, kFewRowsMax = 8;
 enum FewAct { kFewBf16Rows = 0, kFewCodes = 1, kFewBf16Operand = 2, kFewF16Operand = 3 };
@@ -741,7 +754,7 @@ hipError_t launch_operand(const uint16_t* x, int64_t M, int64_t K, bool quant, u
   }
   const int64_t n8 = M * K / 8;
   int n_parts = 0;
-  if (n8 > (1 << 13)) {
+  if (n8 > (1 << 13)) {   // (more than a workgroup reads while a launch would start)
     n_parts = (int)std::min<int64_t>(kAmaxParts, (n8 + 255) / 256);
     linear_amax_kernel<<<(unsigned)n_parts, 256, 0, s>>>(x, n8, parts);
     if (hipError_t e = hipGetLastError()) return e;
@@ -755,6 +768,11 @@ hipError_t launch_operand(const uint16_t* x, int64_t M, int64_t K, bool quant, u
 // Which kernel: linear_few_kernel for few rows, or where one workgroup per CU
 // does the whole product; the grouped kernels' 128 x 256 tiles
 // (launch_linear) once they fill the device; linear_tile_kernel between.
+// Measured (us, the whole W4A16 layer), few / tile: 34816 x 5120 M = 17 41.5 /
+// 43.9, M = 33 62 / 45.7; 8192 x 8192 M = 64 26.4 / 29.4, M = 100 42.9 / 35.4;
+// 4096 x 1024 M = 128 10.4 / 14.8, M = 203 15.9 / 15.3.  Tile / grouped:
+// 8192 x 8192 M = 512 81 / 127, 5120 x 17408 M = 1024 213 / 245, M = 2048 408 /
+// 392, 34816 x 5120 M = 512 211 / 196, M = 1024 402 / 324.
 static bool uses_few(int64_t M, int64_t N) { return M <= 32 || (M + 63) / 64 * (N / 32) <= kCUs; }
 
 bool linear_uses_tiles(int64_t M, int64_t N, int64_t) {

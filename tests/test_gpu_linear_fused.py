@@ -217,6 +217,34 @@ def test_mx_rounds(dev, M, N, K, gated):
     _check_rows("mxfp4", x, wt, bias, "silu", gated, res, got, rows[rows < M])
 
 
+@pytest.mark.parametrize("fmt", ["w4a4", "w4a16"])
+@pytest.mark.parametrize("M,N,K,gated", [
+    # operands of more than 2^31 bytes: on 128-row tiles, and on few columns
+    (65552, 256, 16512, True), (65552, 256, 16512, False), (66000, 128, 16384, False)])
+def test_fused_past_32_bits(dev, fmt, M, N, K, gated):
+    wt = _coded_weight(fmt, N, K, gated)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+    x.view(-1)[:1 << 20] = _x(dev, 1, 1 << 20, 7)[0]
+    block = x.view(-1)[:1 << 20].clone()
+    for at in range(0, M * K, 1 << 20):
+        n = min(1 << 20, M * K - at)
+        x.view(-1)[at:at + n] = block[:n]
+    res = torch.randn(M, N // 2 if gated else N, generator=_gen(dev, N), device=dev).to(torch.bfloat16)
+    got = _call(fmt, x, wt[0], act="silu", residual=res, out_dtype=torch.float32)
+    rows = np.r_[0:8, M // 2, M - 24:M]
+    at = torch.from_numpy(rows).to(dev)
+    xs = x[at]
+    xf = to_np(xs.float()).astype(np.float64)
+    if fmt == "w4a4":
+        gs = onv.global_scale(np.array([[float(x.abs().max())]]))
+        x_hat = onv.dequantize(*onv.quantize(xf, gs), gs)
+    else:
+        x_hat = _operand(fmt, xs)
+    ref, bound = _reference(fmt, xs, wt[1], None, "silu", gated, res[at], got.dtype, x_hat)
+    err = np.abs(to_np(got[at].float()).astype(np.float64) - ref)
+    assert (err <= bound).all(), f"{float((err / bound).max())} times the bound"
+
+
 def _check_rows(fmt, x, wt, bias, act, gated, residual, got, rows):
     """_check on some rows (the activations' global scale is that of all)."""
     at = torch.from_numpy(rows).to(x.device)
