@@ -570,8 +570,7 @@ hipError_t launch_tiles(const TileParams& p, hipStream_t s) {
 // a handful of rows (more rows would put neighbouring lanes in different
 // lines); codes and scales, likewise; or 16-bit values in the operand layout,
 // MT row tiles.  Measured: one row of W4A16 34816 x 5120, 100 MB of weight,
-// 26.0 us (3.9 TB/s, two loads of 16 bytes a lane in flight per column tile);
-// 131072 x 8192, 604 MB, 5.8 TB/s.
+// 25.6 us (3.9 TB/s); 65536 x 8192, 302 MB, 56 us (5.4 TB/s).
 //
 // W4A4 quantises to codes in one launch, each workgroup taking the maximum over
 // all of x, up to kFewQuantMax elements: 5120 x 17408 M = 4 24.4 us against
@@ -600,6 +599,11 @@ __global__ __launch_bounds__(KW * kWave) void linear_few_kernel(FewParams p) {
   constexpr bool OPERAND = ACT >= kFewBf16Operand;
   constexpr int BM = 16 * MT, BN = 16 * NT, SW = BN + 4, AW = CODES ? 1 : 4;
   static_assert(OPERAND || MT == 1, "row tiles come in the operand layout");
+  // Weights that one workgroup reads pass the caches by where nothing else
+  // contends for them: with the operand layout only in the widest layers
+  // (W4A4 8192 x 8192 M = 1 15.5 -> 14.4 us; 5120 x 17408 M = 8, operand
+  // layout, 27.6 -> 29.1).
+  constexpr bool ONCE = !OPERAND || (NT == 4 && KW == 2);
   __shared__ __attribute__((aligned(16))) float sh[KW * BM * SW];
   const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
   const int kw = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -625,7 +629,11 @@ __global__ __launch_bounds__(KW * kWave) void linear_few_kernel(FewParams p) {
   };
   auto load = [&](int c, Chunk& d) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) d.w[j] = *reinterpret_cast<const u32x4*>(wq + ((int64_t)j * KC + c) * 1024);
+    for (int j = 0; j < NT; ++j) {
+      const u32x4* at = reinterpret_cast<const u32x4*>(wq + ((int64_t)j * KC + c) * 1024);
+      if constexpr (ONCE) d.w[j] = __builtin_nontemporal_load(at);
+      else d.w[j] = *at;
+    }
     const int cg = c / GS;
 #pragma unroll
     for (int j = 0; j < NT / 2; ++j)
@@ -810,9 +818,18 @@ hipError_t launch_few_t(const FewParams& p, hipStream_t s) {
 }
 template <int ACT, bool GATED, int MT>
 hipError_t launch_few(const FewParams& p, hipStream_t s) {
-  // 64 columns a workgroup, or 32 where that leaves CUs without one.
-  if constexpr (MT <= 2)
+  // Columns and wavefronts of a workgroup (us, 32 x 4 / 64 x 4 / 64 x 2).  With
+  // two workgroups of 64 columns per CU, a handful of rows take 32 columns and
+  // 4 wavefronts, more rows 64 columns and 4: W4A16 34816 x 5120 M = 1 25.6 /
+  // 28.3 / 32.3, M = 16 34.9 / 33.7 / 36.0; with four, 64 columns and 2:
+  // 65536 x 8192 M = 1 56.3 / 64.6 / 56.6, M = 16 73.2 / 69.4 / 62.7.  Else 32
+  // columns and 8 wavefronts: 8192 x 8192 M = 1 11.3, against 14.0 / 18.3 / 31.
+  if constexpr (MT <= 2) {
+    if constexpr (ACT < kFewBf16Operand)
+      if (p.N / 64 >= 2 * kCUs && p.M <= 4) return launch_few_t<ACT, GATED, MT, 2, 4>(p, s);
+    if (p.N / 64 >= 4 * kCUs) return launch_few_t<ACT, GATED, MT, 4, 2>(p, s);
     if (p.N / 64 >= 2 * kCUs) return launch_few_t<ACT, GATED, MT, 4, 4>(p, s);
+  }
   return launch_few_t<ACT, GATED, MT, 2, 8>(p, s);
 }
 template <int ACT, bool GATED>

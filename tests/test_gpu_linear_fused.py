@@ -217,6 +217,14 @@ def test_mx_rounds(dev, M, N, K, gated):
     _check_rows("mxfp4", x, wt, bias, "silu", gated, res, got, rows[rows < M])
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [
+    # the widest layers: each activation form, one and two row tiles
+    (2, 65536, 128), (6, 65792, 256), (16, 65536, 256), (16, 65536, 6272), (27, 65664, 256)])
+def test_fused_wide(dev, fmt, M, N, K):
+    test_fused_large(dev, fmt, M, N, K)
+
+
 @pytest.mark.parametrize("fmt", ["w4a4", "w4a16"])
 @pytest.mark.parametrize("M,N,K,gated", [
     # operands of more than 2^31 bytes: on 128-row tiles, and on few columns
