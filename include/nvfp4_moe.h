@@ -179,8 +179,10 @@ int moe_route_topk(const float* logits, int32_t T, int32_t E, int32_t topk, int3
  * first H of each row used), wg [E][H] in w_dtype (NVFP4_BF16 or NVFP4_F32:
  * routers stay unquantised), bias float32 [E] or NULL.  Products are exact
  * (float32 weights enter as three bfloat16 parts, 24 significant bits, parts
- * below 2^-126 excepted), sums FP32.  T <= 2^24, 1 <= E <= 1024; H and ldx
- * multiples of 8; x and wg 16-byte aligned. */
+ * below 2^-126 excepted), sums FP32.  Inputs are finite: infinity in x (with
+ * float32 weights) or in a float32 weight gives NaN in its row or column
+ * (a part of the weight is 0 or the difference of infinities).  T <= 2^24,
+ * 1 <= E <= 1024; H and ldx multiples of 8; x and wg 16-byte aligned. */
 int moe_gate(const uint16_t* x, int64_t ldx, const void* wg, int w_dtype, const float* bias, int32_t T, int32_t E,
              int32_t H, float* logits, void* stream);
 

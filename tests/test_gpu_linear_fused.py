@@ -220,7 +220,9 @@ def test_mx_rounds(dev, M, N, K, gated):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,N,K", [
     # the widest layers: each activation form, one and two row tiles
-    (2, 65536, 128), (6, 65792, 256), (16, 65536, 256), (16, 65536, 6272), (27, 65664, 256)])
+    (2, 65536, 128), (6, 65792, 256), (16, 65536, 256), (16, 65536, 6272), (27, 65664, 256),
+    # more tiles than the narrow form of the wide kernel takes
+    (1100, 16384, 128)])
 def test_fused_wide(dev, fmt, M, N, K):
     test_fused_large(dev, fmt, M, N, K)
 
@@ -383,6 +385,73 @@ def test_captured_and_replayed(dev, fmt, M):
         step()
         torch.cuda.synchronize()
         assert torch.equal(got, y)
+
+
+def _workspace(fmt, sizes, dev):
+    """One workspace that is large enough for each of ``sizes`` (M, N, K)."""
+    make = ((lambda *a: ops.mx_linear_workspace(*a, dev)) if fmt == "mxfp4"
+            else (lambda *a: ops.linear_workspace(*a, fmt == "w4a4", dev)))
+    return max((make(*s) for s in sizes), key=lambda t: t.numel())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_one_workspace_for_all(dev, fmt):
+    """Calls with and without an epilogue, of every size class, one after the
+    other in one workspace, equal those in fresh ones; then two captured
+    graphs that share it, replayed in turn."""
+    N, K = 8192, 128
+    w, plain = _weight(fmt, N, K, True)[0], _weight(fmt, N, K, False)[0]
+    Ms = (1100, 3, 80, 20, 300, 1)
+    xs = {M: _x(dev, M, K, M) for M in Ms}
+    res = {M: torch.randn(M, N // 2, generator=_gen(dev, M), device=dev).to(torch.bfloat16) for M in Ms}
+    ws = _workspace(fmt, [(M, N, K) for M in Ms], dev)
+
+    def run(M, ws=None):
+        return (_call(fmt, xs[M], w, act="silu", residual=res[M], ws=ws), _call(fmt, xs[M], plain, ws=ws))
+
+    fresh = {M: run(M) for M in Ms}
+    for _ in range(2):
+        for M in Ms:
+            for got, want in zip(run(M, ws), fresh[M]):
+                assert torch.equal(got, want), M
+    torch.cuda.synchronize()
+    graphs = {}
+    for M in (80, 1100):
+        graphs[M] = torch.cuda.CUDAGraph(), [torch.empty_like(t) for t in fresh[M]]
+        with torch.cuda.graph(graphs[M][0]):
+            for to, t in zip(graphs[M][1], run(M, ws)):
+                to.copy_(t)
+    for i in range(6):
+        M = (80, 1100)[i & 1]
+        for t in graphs[M][1]:
+            t.zero_()
+        graphs[M][0].replay()
+        torch.cuda.synchronize()
+        for got, want in zip(graphs[M][1], fresh[M]):
+            assert torch.equal(got, want), (i, M)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [1, 24, 64, 200])
+def test_two_streams(dev, fmt, M):
+    """Two calls at once, each on its own stream in its own workspace, equal
+    the same calls alone."""
+    N, K = 4096, 1024
+    w = _weight(fmt, N, K, False)[0]
+    xs = [_x(dev, M, K, s) for s in (1, 2)]
+    want = [_call(fmt, x, w, act="gelu") for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ws = [_workspace(fmt, [(M, N, K)], dev) for _ in xs]
+    out = [torch.empty_like(t) for t in want]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, x, o, b in zip(streams, xs, out, ws):
+            with torch.cuda.stream(s):
+                _call(fmt, x, w, act="gelu", out=o, ws=b)
+    torch.cuda.synchronize()
+    for o, t in zip(out, want):
+        assert torch.equal(o, t)
 
 
 def test_guard_bands(dev):
