@@ -12,6 +12,32 @@
 
 namespace nvfp4 {
 
+// z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt 2) / 2: the complementary error
+// function keeps the relative accuracy of the left tail, where 1 + erf cancels.
+// erfc(w / sqrt 2) = e^(-w^2 / 2) f(w), and f(w) (w + c) / 2 is close to a
+// polynomial in u = (w - c) / (w + c), which maps [0, inf) to [-1, 1); degree 8
+// with c = 3.75, a least-maximum fit of its own over w <= 14.2, is within
+// 1.5e-8 of it.  Beyond, the exponential is 0 in FP32 or nearly so.  Against
+// FP64 in FP32 steps of the result: 6 for |z| < 3, growing as z^2 with the
+// exponential.  A quarter of the instructions of erfcf (a 203 x 4096 layer:
+// 2 us of 16).
+__device__ __forceinline__ float gelu_fast(float z) {
+  const float w = fminf(fabsf(z), 100.0f);
+  const float r = __builtin_amdgcn_rcpf(w + 3.75f), u = __builtin_fmaf(r, -7.5f, 1.0f);
+  float q = 0.00044344825f;
+  q = __builtin_fmaf(q, u, 0.0005096253f);
+  q = __builtin_fmaf(q, u, -0.00416902f);
+  q = __builtin_fmaf(q, u, 0.0012000743f);
+  q = __builtin_fmaf(q, u, 0.037492506f);
+  q = __builtin_fmaf(q, u, -0.15152083f);
+  q = __builtin_fmaf(q, u, 0.3529396f);
+  q = __builtin_fmaf(q, u, -0.5881883f);
+  q = __builtin_fmaf(q, u, 0.7502941f);
+  const float e = __builtin_amdgcn_exp2f(w * w * -0.72134752044f);
+  const float p = 0.5f * z;
+  return (p + fabsf(p)) - (w * r) * (q * e);
+}
+
 // The activation of N values.  The choice is the same for the whole launch and
 // stands outside the values, so that the code of the others is stepped over
 // once: instruction fetches of code that is run once are a good part of a
@@ -28,16 +54,9 @@ __device__ __forceinline__ void act_apply(int act, float (&z)[N]) {
 #pragma unroll
       for (int r = 0; r < N; ++r) z[r] = silu_fast(z[r]);
       break;
-    // z Phi(z): the complementary error function keeps the relative accuracy
-    // of the left tail, where 1 + erf cancels.
     case kFnGelu:
-#pragma unroll 1
-      for (int k = 0; k < N; ++k) {   // (rolled: the values turn through one register)
-        const float v = z[0];
 #pragma unroll
-        for (int r = 0; r + 1 < N; ++r) z[r] = z[r + 1];
-        z[N - 1] = 0.5f * v * erfcf(-0.70710678118654752f * v);
-      }
+      for (int r = 0; r < N; ++r) z[r] = gelu_fast(z[r]);
       break;
     // 0.5 z (1 + tanh u) = z / (1 + e^-2u)
     case kFnGeluTanh:
