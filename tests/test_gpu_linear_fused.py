@@ -228,6 +228,13 @@ def test_fused_wide(dev, fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", ["w4a4", "w4a16"])
+@pytest.mark.parametrize("M,N,K", [(4100, 4352, 128), (4100, 4224, 384), (4099, 4352, 256), (2000, 9600, 128)])
+def test_fused_columns_left_over(dev, fmt, M, N, K):
+    """More than a round of tiles: the last columns in narrower ones."""
+    test_fused_large(dev, fmt, M, N, K)
+
+
+@pytest.mark.parametrize("fmt", ["w4a4", "w4a16"])
 @pytest.mark.parametrize("M,N,K,gated", [
     # operands of more than 2^31 bytes: on 128-row tiles, and on few columns
     (65552, 256, 16512, True), (65552, 256, 16512, False), (66000, 128, 16384, False)])
