@@ -44,13 +44,15 @@ def _raw_stream(device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _same_device(device: int, **tensors):
-    """Checks that the tensors (None among them) live on the GPU ``device``."""
+def _same_device(device: int, *tensors) -> bool:
+    """Checks that the tensors (None among them) live on the GPU ``device``;
+    whether that is the current device."""
     if device < 0:
         raise ValueError("tensors must live on the GPU")
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.get_device() != device:
-            raise ValueError(f"{name} lives on {t.device}, not on GPU {device}")
+            raise ValueError(f"a tensor lives on {t.device}, another on GPU {device}")
+    return torch._C._cuda_getDevice() == device
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -116,8 +118,7 @@ def gate_logits(x: torch.Tensor, wg: torch.Tensor, bias: Optional[torch.Tensor] 
     """The router's product: float32 logits [T, E] = x wg^T (+ bias), x bf16
     [T, H], wg [E, H] bf16 or float32, bias float32 [E]."""
     dev = x.get_device()
-    _same_device(dev, wg=wg, bias=bias, out=out)
-    if dev != torch.cuda.current_device():
+    if not _same_device(dev, wg, bias, out):
         with torch.cuda.device(dev):
             return gate_logits(x, wg, bias, out)
     if x.dim() != 2 or wg.dim() != 2 or wg.shape[1] != x.shape[1] or x.dtype != torch.bfloat16:
@@ -125,9 +126,10 @@ def gate_logits(x: torch.Tensor, wg: torch.Tensor, bias: Optional[torch.Tensor] 
     T, H = x.shape
     E = wg.shape[0]
     ld, one = x.stride()
-    if one != 1 or ld % 8 or ld < H or x.data_ptr() % 16:
+    at = x.data_ptr()
+    if one != 1 or ld % 8 or ld < H or at % 16:
         x = x.clone(memory_format=torch.contiguous_format)
-        ld = H
+        at, ld = x.data_ptr(), H
     if bias is not None:
         if bias.shape != (E,) or bias.dtype != torch.float32:
             raise ValueError("bias must be float32 [E]")
@@ -137,7 +139,7 @@ def gate_logits(x: torch.Tensor, wg: torch.Tensor, bias: Optional[torch.Tensor] 
     elif out.shape != (T, E) or out.dtype != torch.float32 or not out.is_contiguous():
         raise ValueError("out must be contiguous float32 [T, E]")
     wg = wg.contiguous()
-    call("moe_gate", x.data_ptr(), ld, wg.data_ptr(), _dtype_code(wg), _ptr(bias), T, E, H, out.data_ptr(),
+    call("moe_gate", at, ld, wg.data_ptr(), _dtype_code(wg), _ptr(bias), T, E, H, out.data_ptr(),
          _raw_stream(dev))
     return out
 
@@ -168,8 +170,7 @@ def route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias: Opt
     -inf or NaN are not available; ids that no expert fills are -1."""
     params = _route_params(score, groups, topk_groups, group_score, renormalize, scale)
     dev = logits.get_device()
-    _same_device(dev, bias=bias, ids=ids, weights=weights)
-    if dev != torch.cuda.current_device():
+    if not _same_device(dev, bias, ids, weights):
         with torch.cuda.device(dev):
             return route_scored(logits, k, score, bias, groups, topk_groups, group_score, renormalize, scale, ids,
                                 weights)
@@ -445,8 +446,7 @@ def _linear_fused(name: str, x, w, scale, bias, act, residual, out_dtype, out, w
     """The fused call ``name`` after its checks; ``scale``: the weight's
     global scale (NVFP4), or None (MXFP4)."""
     dev = x.get_device()
-    _same_device(dev, weight=w.prep, bias=bias, residual=residual, out=out, ws=ws)
-    if dev != torch.cuda.current_device():
+    if not _same_device(dev, w.prep, bias, residual, out, ws):
         with torch.cuda.device(dev):
             return _linear_fused(name, x, w, scale, bias, act, residual, out_dtype, out, ws)
     N, K = w.N, w.K
