@@ -153,9 +153,9 @@ __global__ __launch_bounds__(256) void linear_operand_kernel(const uint16_t* __r
 // x 64 columns each, M = 64, N = 34816, K = 5120 moved 435 MB and took 34 us.
 // The weights of the chunk after next are requested as soon as the registers
 // of the present one are read.  Measured, whole layers: W4A4 34816 x 5120
-// M = 64 47.6 us, of which the activations take 9.6 (maximum, quantisation),
-// the product 33 and the join 5; M = 128 67 us (678 TFLOP/s); W4A16
-// 5120 x 17408 M = 512 123 us (742 TFLOP/s).
+// M = 64 47 us, of which the activations take 9.6 (maximum, quantisation),
+// the product 33 and the join 5; M = 128 66 us (696 TFLOP/s); W4A16
+// 5120 x 17408 M = 512 112 us (812 TFLOP/s).
 // ---------------------------------------------------------------------------
 constexpr int kNT = 4;        // column tiles of a wavefront: 64 columns
 constexpr int kCUs = 256;
@@ -183,7 +183,7 @@ struct TileSplit {
 struct TileParams {
   int M, N, K;
   TileSplit t;
-  const uint16_t* a;     // operand layout
+  const uint16_t* a;     // f16 in the operand layout (W4A4), or bf16 [M][K]
   const uint8_t* w_q;    // streaming layout
   const uint8_t* w_sf;
   const float* g_w;
@@ -267,6 +267,13 @@ struct TileWork {
 // multiply chunk t from LDS buffer t & 1, request chunk t + D's weights into
 // the registers just read, put chunk t + 1's activations into the other
 // buffer.  The next piece's first requests precede the end of the present one.
+//
+// W4A4 activations come in the operand layout, which quantising writes anyway.
+// bf16 rows are taken as they are, four rows' 256 bytes of a chunk a load, and
+// turned around by the LDS writes: the 16-byte unit u = 4 g + s of row m goes to
+// place m ^ u of step s, lane group g, so that neither the writes (16 units of a
+// row) nor the fragment reads (16 rows of a unit) meet in a bank.  Against a
+// launch that makes the operand layout: 203 x 4096 x 1024 14.2 -> 12.3 us, 512 x 5120 x 17408 118 -> 112 us.
 template <bool BF16, bool GATED, int MT, int CW, int KW>
 __global__ __launch_bounds__(CW * KW * kWave) __attribute__((amdgpu_waves_per_eu(CW * KW / 4, CW * KW / 4)))
 void linear_tile_kernel(TileParams p) {
@@ -320,12 +327,14 @@ void linear_tile_kernel(TileParams p) {
                                             kBufferFlags);
     P.s = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w_sf + (int64_t)(nt0 >> 1) * KC * 256), (short)0, 0x7FFFFFFF,
                                             kBufferFlags);
+    // (16 MT rows of either form are MT KC 2048 values)
     P.a = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + (int64_t)k.mb * MT * KC * 2048), (short)0, 0x7FFFFFFF,
                                             kBufferFlags);
 #pragma unroll
     for (int q = 0; q < LPW; ++q) {
       const int at = wc * LPW + q;
-      P.va[q] = l16 + min(at / 4, row_tiles - 1 - k.mb * MT) * KC * 4096 + at % 4 * 1024;
+      if constexpr (BF16) P.va[q] = min(4 * at + lg, p.M - 1 - k.mb * BM) * KC * 256 + ln * 16;
+      else P.va[q] = l16 + min(at / 4, row_tiles - 1 - k.mb * MT) * KC * 4096 + at % 4 * 1024;
     }
     return P;
   };
@@ -343,12 +352,16 @@ void linear_tile_kernel(TileParams p) {
     const int c = P.c_lo + min(t, P.last);
 #pragma unroll
     for (int q = 0; q < LPW; ++q)
-      d.v[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(P.a, P.va[q], c * 4096, 0));
+      d.v[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(P.a, P.va[q], c * (BF16 ? 256 : 4096), 0));
   };
   auto put_a = [&](int buf, const A& d) {
 #pragma unroll
-    for (int q = 0; q < LPW; ++q)
-      *reinterpret_cast<u32x4*>(ring + buf * STAGE + (wc * LPW + q) * 1024 + l16) = d.v[q];
+    for (int q = 0; q < LPW; ++q) {
+      const int at = wc * LPW + q;   // bf16: rows 4 at + lg, unit ln
+      const int to = BF16 ? at / 4 * 4096 + (ln & 3) * 1024 + (ln >> 2) * 256 + ((at % 4 * 4 + lg) ^ ln) * 16
+                          : at * 1024 + l16;
+      *reinterpret_cast<u32x4*>(ring + buf * STAGE + to) = d.v[q];
+    }
   };
   W w[D];
   A a[2];
@@ -376,7 +389,7 @@ void linear_tile_kernel(TileParams p) {
     typedef typename std::conditional<BF16, bf16x8, f16x8>::type frag;
     constexpr int VALU = BF16 ? 16 : 8;                 // instructions of a decode
     auto compute = [&](int buf, const W& w) {
-      const uint8_t* st = ring + buf * STAGE + l16;
+      const uint8_t* st = ring + buf * STAGE;
       f16x2 scale[kNT];
 #pragma unroll
       for (int j = 0; j < kNT; ++j) scale[j] = e4m3x2_to_f16x2(w.s[j >> 1] >> ((j & 1) * 16));
@@ -384,7 +397,7 @@ void linear_tile_kernel(TileParams p) {
       for (int s = 0; s < 4; ++s) {
         frag af[MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) af[i] = *reinterpret_cast<const frag*>(st + i * 4096 + s * 1024);
+        for (int i = 0; i < MT; ++i) af[i] = *reinterpret_cast<const frag*>(st + i * 4096 + s * 1024 + (BF16 ? lg * 256 + ((ln ^ (4 * lg)) ^ s) * 16 : l16));
         __builtin_amdgcn_sched_barrier(0);
         frag bf[kNT];
 #pragma unroll
@@ -533,7 +546,8 @@ TileSplit tile_split_as(int cfg, int64_t M, int64_t N, int64_t K) {
 // Row blocks of even height; 128 columns a workgroup where the tiles are few
 // and short, else 256.  Measured (us, the whole W4A16 layer, 128 / 256 columns):
 // 4096 x 1024 M = 256 15.7 / 19.8, 8192 x 512 M = 256 13.9 / 16.0; longer or
-// more of them: 8192 x 8192 M = 128 38.6 / 36.2, 34816 x 5120 M = 64 54 / 48.
+// more of them: 8192 x 8192 M = 128 38.6 / 36.2, 34816 x 5120 M = 64 54 / 48
+// (all four with a launch for the activations' layout, 2 to 3 us, in front).
 TileSplit tile_split(int64_t M, int64_t N, int64_t K) {
   const int64_t tiles = (M + 15) / 16, blocks = (tiles + 3) / 4;
   const bool low = (tiles + blocks - 1) / blocks <= 3;
@@ -773,18 +787,25 @@ hipError_t launch_operand(const uint16_t* x, int64_t M, int64_t K, bool quant, u
 
 }  // namespace
 
-// Which kernel: linear_few_kernel for few rows, or where one workgroup per CU
-// does the whole product; the grouped kernels' 128 x 256 tiles
+// Which kernel: linear_few_kernel for up to 16 rows, or where its workgroups
+// are few and the contraction is not long; the grouped kernels' 128 x 256 tiles
 // (launch_linear) once they fill the device; linear_tile_kernel between.
-// Measured (us, the whole W4A16 layer), few / tile: 34816 x 5120 M = 17 41.5 /
-// 43.9, M = 33 62 / 45.7; 8192 x 8192 M = 64 26.4 / 29.4, M = 100 42.9 / 35.4;
-// 4096 x 1024 M = 128 10.4 / 14.8, M = 203 15.9 / 15.3.  Tile / grouped:
-// 8192 x 8192 M = 512 81 / 127, 5120 x 17408 M = 1024 213 / 245, M = 2048 408 /
-// 392, 34816 x 5120 M = 512 211 / 196, M = 1024 402 / 324.
-static bool uses_few(int64_t M, int64_t N) { return M <= 32 || (M + 63) / 64 * (N / 32) <= kCUs; }
+// Measured (us, the whole layer, W4A16 and W4A4), few / tile:
+//   12288 x 2048 M = 32 12.6 / 13.9, 17.3 / 19.2; M = 33 15.8 / 14.0, 20.6 / 19.5
+//   16384 x 8192 M = 17 32.5 / 28.2, 36.6 / 32.3
+//   5120 x 17408 M = 17 30.3 / 28.8, 34.5 / 35.3; M = 64 43.3 / 35.6, 47.8 / 42.1
+//   8192 x 8192  M = 64 26.7 / 25.1, 31.3 / 31.5; M = 100 41.9 / 31.3, 46.5 / 35.8
+//   4096 x 1024  M = 128 10.4 / 12.3, 14.9 / 17.6; M = 203 16.0 / 12.6, 20.6 / 18.4
+// and tile / grouped:
+//   34816 x 5120 M = 256 111 / 119, 101 / 119; M = 300 155 / 137, 121 / 122; M = 1024 395 / 313, 335 / 294
+//   5120 x 17408 M = 1024 208 / 245, 185 / 235; M = 2048 388 / 393, 355 / 389
+//   8192 x 8192  M = 512 80 / 129, 73 / 87; M = 1300 205 / 204, 187 / 195; M = 2048 302 / 227, 269 / 230
+static bool uses_few(int64_t M, int64_t N, int64_t K) {
+  return M <= 16 || (K <= 8192 && (M + 63) / 64 * (N / 32) <= (M <= 32 ? 384 : kCUs));
+}
 
-bool linear_uses_tiles(int64_t M, int64_t N, int64_t) {
-  return uses_few(M, N) || M < 512 || (M + 127) / 128 * ((N + 255) / 256) < kCUs;
+bool linear_uses_tiles(int64_t M, int64_t N, int64_t K) {
+  return uses_few(M, N, K) || M <= 256 || (M + 127) / 128 * ((N + 255) / 256) < kCUs;
 }
 
 // Workspace: scale and maxima, the activation operand, partial sums.
@@ -824,7 +845,7 @@ hipError_t launch_few(const FewParams& p, hipStream_t s) {
   // 28.3 / 32.3, M = 16 34.9 / 33.7 / 36.0; with four, 64 columns and 2:
   // 65536 x 8192 M = 1 56.3 / 64.6 / 56.6, M = 16 73.2 / 69.4 / 62.7.  Else 32
   // columns and 8 wavefronts: 8192 x 8192 M = 1 11.3, against 14.0 / 18.3 / 31.
-  if constexpr (MT <= 2) {
+  if constexpr (MT == 1) {
     if constexpr (ACT < kFewBf16Operand)
       if (p.N / 64 >= 2 * kCUs && p.M <= 4) return launch_few_t<ACT, GATED, MT, 2, 4>(p, s);
     if (p.N / 64 >= 4 * kCUs) return launch_few_t<ACT, GATED, MT, 4, 2>(p, s);
@@ -886,18 +907,19 @@ hipError_t launch_linear_few(const uint16_t* x, int64_t M, int64_t N, int64_t K,
 
 hipError_t launch_linear_tiles(const uint16_t* x, int64_t M, int64_t N, int64_t K, bool w4a4, const uint8_t* w_prep,
                                const float* gw, const LinearEpi& ep, void* ws, hipStream_t s) {
-  if (uses_few(M, N)) return launch_linear_few(x, M, N, K, w4a4, w_prep, gw, ep, ws, s);
+  if (uses_few(M, N, K)) return launch_linear_few(x, M, N, K, w4a4, w_prep, gw, ep, ws, s);
   const TileWs L = tile_ws(M, N, K);
   uint8_t* b = static_cast<uint8_t*>(ws);
   float* g = reinterpret_cast<float*>(b);
   uint16_t* a = reinterpret_cast<uint16_t*>(b + L.a);
-  if (hipError_t e = launch_operand(x, M, K, w4a4, reinterpret_cast<uint32_t*>(b + L.parts), g, a, s)) return e;
+  if (w4a4)
+    if (hipError_t e = launch_operand(x, M, K, true, reinterpret_cast<uint32_t*>(b + L.parts), g, a, s)) return e;
   TileParams p{};
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
   p.t = tile_split(M, N, K);
-  p.a = a;
+  p.a = w4a4 ? a : x;
   p.w_q = w_prep;
   p.w_sf = w_prep + (size_t)N * (K / 2);
   p.g_w = gw;
