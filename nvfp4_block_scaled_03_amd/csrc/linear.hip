@@ -427,10 +427,11 @@ void linear_tile_kernel(TileParams p) {
     };
 
     put_a(0, a[0]);
-    // (unrolled so that register sets have constant indices: 2 D trips)
-    for (int t0 = 0; t0 < P.trips; t0 += 2 * D) {
+    // (unrolled so that register sets and LDS buffers have constant indices)
+    static_assert(D == 2, "a period of two trips");
+    for (int t0 = 0; t0 < P.trips; t0 += 2) {
 #pragma unroll
-      for (int d = 0; d < 2 * D; ++d) {
+      for (int d = 0; d < 2; ++d) {
         const int t = t0 + d;
         if (t < P.trips) {
           // (LDS only: the requests in flight are not waited for)
