@@ -7,7 +7,8 @@
 // weight streams from memory straight into registers, one coalesced 16-byte
 // load per lane per 16 columns x 128 k.
 //
-// The activations go through one launch into the operand layout
+// W4A4 activations, and the bf16 ones of 9 rows and more in linear_few_kernel,
+// go through one launch into the operand layout
 //   [M/16 row tiles][K/128 chunks][4 steps][64 lanes][16 B]
 // (lane 16 g + m of step s: row m of the tile, k in [32 g + 8 s, 32 g + 8 s + 8)
 // of the chunk), so that a fragment is one contiguous 1 KiB load.  Row-major

@@ -234,6 +234,14 @@ def test_fused_columns_left_over(dev, fmt, M, N, K):
     test_fused_large(dev, fmt, M, N, K)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N", [(65552, 33024), (17, 1 << 20)])
+def test_fused_large_output(dev, fmt, M, N):
+    """An output of more than 2^31 elements; the widest weight."""
+    test_fused_large(dev, fmt, M, N, 128)
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("fmt", ["w4a4", "w4a16"])
 @pytest.mark.parametrize("M,N,K,gated", [
     # operands of more than 2^31 bytes: on 128-row tiles, and on few columns

@@ -93,6 +93,37 @@ def test_gate_row_stays_its_own(dev):
     assert torch.equal(got[keep], clean[keep])
 
 
+@pytest.mark.parametrize("T", [4, 7])
+def test_gate_rows_far_apart(dev, T):
+    """Rows whose offsets pass 2^31 elements."""
+    H, E, apart = 72, 20, 1 << 30
+    buf = torch.empty(T * apart, dtype=torch.bfloat16, device=dev)
+    x = buf.view(T, apart)[:, :H]
+    x.copy_(torch.randn(T, H, generator=_gen(dev, T), device=dev))
+    wg = torch.randn(E, H, generator=_gen(dev, 1), device=dev)
+    assert torch.equal(ops.gate_logits(x, wg), ops.gate_logits(x.clone(), wg))
+    del buf, x
+    torch.cuda.empty_cache()
+
+
+def test_gate_many_logits(dev):
+    """More than 2^31 logits, few of them checked."""
+    T, H, E = (1 << 21) + 40, 16, 1024
+    x = torch.randn(T, H, generator=_gen(dev, 5), device=dev).to(torch.bfloat16)
+    wg = torch.randn(E, H, generator=_gen(dev, 6), device=dev).to(torch.bfloat16)
+    z = ops.gate_logits(x, wg)
+    for t in (0, T // 2, T - 64):
+        rows = slice(t, t + 64)
+        ref = orr.gate_logits(to_np(x[rows].float()), to_np(wg.float()))
+        bound = H * 2.0 ** -23 * (np.abs(to_np(x[rows].float())) @ np.abs(to_np(wg.float())).T) + 2.0 ** -140
+        assert (np.abs(to_np(z[rows]) - ref) <= bound).all()
+    # and the choice among them
+    ids, w = ops.route_scored(z, 2)
+    _check_route(z[T - 64:], (ids[T - 64:], w[T - 64:]), 2)
+    del z
+    torch.cuda.empty_cache()
+
+
 # ----------------------------------------------------------------- the choice
 def _check_route(logits, got, k, **kw):
     bias = kw.get("bias")
