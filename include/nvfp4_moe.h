@@ -340,9 +340,10 @@ int nvfp4_linear_w4a16(const uint16_t* x, int64_t M, int64_t N, int64_t K, const
  * with dims {T: any, topk: 1, E: 1, H: K, I: N/2, shared: 0} and which = 13;
  * N is then a multiple of 256.  bias float32 [N] in W's row order, or NULL.
  * residual [M][ld_residual] in residual_dtype, or NULL; it may be out itself
- * (same pointer, stride and type) and must not overlap it otherwise.
+ * (same pointer, stride and type, else NVFP4_EINVAL) and must not overlap it
+ * otherwise.
  * out [M][ld_out]; only its N (gated: N/2) columns are written; it must not
- * overlap x, the weight, the bias or the workspace.  Strides in
+ * overlap x (x itself: NVFP4_EINVAL), the weight, the bias or the workspace.  Strides in
  * elements, multiples of 4; residual and out are aligned to 4 elements.
  * M, N, K, x, gw, out_dtype and ws (with its size query) as for the call
  * without an epilogue. */

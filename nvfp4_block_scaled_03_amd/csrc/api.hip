@@ -372,6 +372,8 @@ int check_epilogue(const char* W, const nvfp4_epilogue* e, int64_t M, int64_t N,
     if (!aligned(out, out_dtype == NVFP4_F32 ? 16 : 8) || !aligned(e->bias, 4) ||
         !aligned(e->residual, e->residual_dtype == NVFP4_F32 ? 16 : 8))
       return fail(NVFP4_EINVAL, "%s: EINVAL out and residual aligned to 4 elements, bias to 4 bytes", W);
+    if (e->residual == out && (e->residual_dtype != out_dtype || (M > 1 && e->ld_residual != e->ld_out)))
+      return fail(NVFP4_EINVAL, "%s: EINVAL a residual in place of out has its type and stride", W);
   }
   k->bias = e->bias;
   k->act = e->act;
@@ -402,6 +404,7 @@ int linear_run(const char* W, bool w4a4, const uint16_t* x, int64_t M, int64_t N
   if (!x || !w_prep || !gw || !out) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
   if (!aligned(x, 16) || !aligned(w_prep, 16) || !aligned(ws, 256) || (!epi && !aligned(out, 16)))
     return fail(NVFP4_EINVAL, "%s: EINVAL x, w_prep and out 16-byte, ws 256-byte aligned", W);
+  if (epi && out == x) return fail(NVFP4_EINVAL, "%s: EINVAL out is x", W);
   uint8_t* b = static_cast<uint8_t*>(ws);
   if (epi && nvfp4::linear_uses_tiles(M, N, K))
     return launched(nvfp4::launch_linear_tiles(x, M, N, K, w4a4, w_prep, gw, *epi, b + L.tiles, S(stream)), W);
@@ -541,6 +544,7 @@ int mx_linear_run(const char* W, const uint16_t* x, int64_t M, int64_t N, int64_
   if (!x || !w_prep || !out) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
   if (!aligned(x, 16) || !aligned(w_prep, 16) || !aligned(ws, 256))
     return fail(NVFP4_EINVAL, "%s: EINVAL x and w_prep 16-byte, ws 256-byte aligned", W);
+  if (epi && out == x) return fail(NVFP4_EINVAL, "%s: EINVAL out is x", W);
   uint8_t* aq = static_cast<uint8_t*>(ws);
   uint8_t* ae = aq + mx_ws_codes(M, K);
   hipError_t e = nvfp4::launch_mx_quantize_operand(x, M, K, aq, ae, S(stream));

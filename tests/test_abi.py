@@ -360,3 +360,19 @@ def test_fused_linear_errors(lib):
         assert f(epi(), wsb=0) == _lib.NVFP4_EWORKSPACE and "needed=" in _lib.last_error()
     assert nv(epi(), g=None) == _lib.NVFP4_EINVAL
     assert mx(epi(ld_out=1 << 20), M=8, N=1 << 20, K=1 << 14) == _lib.NVFP4_ESHAPE and "4 GiB" in _lib.last_error()
+
+
+def test_fused_linear_refuses_aliases(lib):
+    """x as the output, and a residual in place of the output with another
+    type or stride."""
+    def run(name, x, out, dt=0, M=8, **kw):
+        e = _lib.Epilogue(**{**dict(act=0, gated=0, ld_out=512), **kw})
+        g = () if name.startswith("mx") else (4096,)
+        return getattr(lib, name)(x, M, 512, 512, 4096, *g, ctypes.byref(e), out, dt, 4096, 1 << 30, None)
+
+    for name in ("nvfp4_linear_fused", "nvfp4_linear_w4a16_fused", "mxfp4_linear_fused"):
+        assert run(name, 8192, 8192) == _lib.NVFP4_EINVAL and "out is x" in _lib.last_error()
+        for kw in (dict(dt=1, residual_dtype=0, ld_residual=512), dict(residual_dtype=1, ld_residual=512),
+                   dict(ld_residual=516)):
+            assert run(name, 4096, 8192, residual=8192, **kw) == _lib.NVFP4_EINVAL
+            assert "type and stride" in _lib.last_error()
