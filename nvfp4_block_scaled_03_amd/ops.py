@@ -446,7 +446,7 @@ def _linear_fused(name: str, x, w, scale, bias, act, residual, out_dtype, out, w
     """The fused call ``name`` after its checks; ``scale``: the weight's
     global scale (NVFP4), or None (MXFP4)."""
     dev = x.get_device()
-    if not _same_device(dev, w.prep, bias, residual, out, ws):
+    if not _same_device(dev, w.prep, scale, bias, residual, out, ws):
         with torch.cuda.device(dev):
             return _linear_fused(name, x, w, scale, bias, act, residual, out_dtype, out, ws)
     N, K = w.N, w.K

@@ -512,3 +512,17 @@ def test_refusals(dev):
         ops.quantize_linear_weight(torch.zeros(384, 256, device=dev), gated=True)
     with pytest.raises(_lib.Nvfp4Error):
         ops.linear(x, w, "w4a16", act="silu", ws=torch.zeros(256, dtype=torch.uint8, device=dev)[:0])
+
+
+def test_refuses_a_scale_elsewhere(dev):
+    w = _weight("w4a16", 512, 256, False)[0]
+    moved = ops.LinearWeight(w.prep, w.g.cpu(), w.N, w.K)
+    with pytest.raises(ValueError):
+        ops.linear(_x(dev, 4, 256, 1), moved, "w4a16", act="silu")
+
+
+def test_refuses_x_as_output(dev):
+    for fmt in FORMATS:
+        w, x = _weight(fmt, 256, 256, False)[0], _x(dev, 4, 256, 1)
+        with pytest.raises(_lib.Nvfp4Error):
+            _call(fmt, x, w, residual=x, out=x)
