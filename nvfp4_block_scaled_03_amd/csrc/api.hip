@@ -318,9 +318,11 @@ int moe_mxfp4_quantize_and_align(const nvfp4_moe_dims* d, const uint16_t* x, uin
 
 // ------------------------------------------------------------------ dense linear
 namespace {
-// Workspace of nvfp4_linear*: 256-byte aligned sub-buffers in this order.
+// Workspace of nvfp4_linear*: 256-byte aligned sub-buffers in this order;
+// plain: their end, all that a call on the grouped kernels uses; total: with
+// the scratch of the fused layers' own kernels.
 struct LinearWs {
-  size_t g, gs, tiles, offsets, sorted_pair, inv_pos, plan, align, a_q, a_sf, a_deq, total;
+  size_t g, gs, tiles, offsets, sorted_pair, inv_pos, plan, align, a_q, a_sf, a_deq, plain, total;
 };
 size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 bool linear_shape_ok(int64_t M, int64_t N, int64_t K) {
@@ -345,6 +347,7 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K, bool w4a4) {
   w.a_q = take(w4a4 ? (size_t)M * (K / 2) : 0);
   w.a_sf = take(w4a4 ? (size_t)M * (K / 16) : 0);
   w.a_deq = take(w4a4 && nvfp4::prefers_decoded((int)M, 1, 1, 0) ? (size_t)M * K * 2 : 0);
+  w.plain = o;
   w.total = std::max(o, w.tiles + up256(nvfp4::linear_tile_ws_bytes(M, N, K)));
   return w;
 }
@@ -397,9 +400,10 @@ int linear_run(const char* W, bool w4a4, const uint16_t* x, int64_t M, int64_t N
                 (long long)N, (long long)K);
   if (out_dtype != 0 && out_dtype != 1) return fail(NVFP4_EINVAL, "%s: EINVAL out_dtype=%d", W, out_dtype);
   const LinearWs L = linear_ws(M, N, K, w4a4);
-  if (ws_bytes < L.total || !ws)
+  const size_t need = epi ? L.total : L.plain;
+  if (ws_bytes < need || !ws)
     return fail(NVFP4_EWORKSPACE, "%s: EWORKSPACE num_experts=1 M=%lld N=%lld K=%lld workspace_size=%zu needed=%zu",
-                W, (long long)M, (long long)N, (long long)K, ws_bytes, L.total);
+                W, (long long)M, (long long)N, (long long)K, ws_bytes, need);
   if (M == 0) return ok();
   if (!x || !w_prep || !gw || !out) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
   if (!aligned(x, 16) || !aligned(w_prep, 16) || !aligned(ws, 256) || (!epi && !aligned(out, 16)))

@@ -376,3 +376,29 @@ def test_fused_linear_refuses_aliases(lib):
                    dict(ld_residual=516)):
             assert run(name, 4096, 8192, residual=8192, **kw) == _lib.NVFP4_EINVAL
             assert "type and stride" in _lib.last_error()
+
+
+def _needed(lib, name, M, N, K):
+    """What a dense call demands of its workspace (from the refusal of an empty one)."""
+    assert getattr(lib, name)(None, M, N, K, None, None, None, 0, 4096, 0, None) == _lib.NVFP4_EWORKSPACE
+    return int(re.search(r"needed=(\d+)", _lib.last_error()).group(1))
+
+
+@pytest.mark.parametrize("N,K", [(34816, 5120), (5120, 17408), (4096, 1024), (128, 128)])
+def test_plain_linear_takes_a_workspace_of_more_rows(lib, N, K):
+    """nvfp4_linear and nvfp4_linear_w4a16 demand what their own kernels use,
+    the permutation of M rows and (W4A4) the quantised activations, and not the
+    fused layers' scratch: a workspace sized for the largest batch serves the
+    smaller ones."""
+    Ms = (1, 3, 16, 17, 64, 100, 256, 257, 300, 1000, 1024, 4096, 8192)
+    for w4a4, name in ((1, "nvfp4_linear"), (0, "nvfp4_linear_w4a16")):
+        sizes = {M: lib.nvfp4_linear_workspace_size(M, N, K, w4a4) for M in Ms}
+        need = {M: _needed(lib, name, M, N, K) for M in Ms}
+        for M in Ms:
+            # offsets, two permutations, plan and counts: 16 bytes a row and what is rounded up;
+            # W4A4: codes, scales and, for tall tiles, the f16 values, 2.5625 bytes an element
+            assert need[M] <= 16 * M + 8192 + w4a4 * (M * K * 41 // 16 + 2048), (M, need[M])
+            for more in (m for m in Ms if m >= M):
+                assert need[M] <= sizes[more], (M, more)
+                assert getattr(lib, name)(None, M, N, K, None, None, None, 0, 4096, sizes[more],
+                                          None) == _lib.NVFP4_EINVAL and "null" in _lib.last_error()
