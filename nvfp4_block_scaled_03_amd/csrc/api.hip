@@ -319,10 +319,10 @@ int moe_mxfp4_quantize_and_align(const nvfp4_moe_dims* d, const uint16_t* x, uin
 // ------------------------------------------------------------------ dense linear
 namespace {
 // Workspace of nvfp4_linear*: 256-byte aligned sub-buffers in this order;
-// plain: their end, all that a call on the grouped kernels uses; total: with
-// the scratch of the fused layers' own kernels.
+// plain: their end, all that a call on the grouped kernels uses; fused: what a
+// fused call uses (on those kernels, or scratch from tiles on).
 struct LinearWs {
-  size_t g, gs, tiles, offsets, sorted_pair, inv_pos, plan, align, a_q, a_sf, a_deq, plain, total;
+  size_t g, gs, tiles, offsets, sorted_pair, inv_pos, plan, align, a_q, a_sf, a_deq, plain, fused;
 };
 size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
 bool linear_shape_ok(int64_t M, int64_t N, int64_t K) {
@@ -348,7 +348,9 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K, bool w4a4) {
   w.a_sf = take(w4a4 ? (size_t)M * (K / 16) : 0);
   w.a_deq = take(w4a4 && nvfp4::prefers_decoded((int)M, 1, 1, 0) ? (size_t)M * K * 2 : 0);
   w.plain = o;
-  w.total = std::max(o, w.tiles + up256(nvfp4::linear_tile_ws_bytes(M, N, K)));
+  w.fused = nvfp4::linear_uses_tiles(M, N, K)
+                ? std::max<size_t>(256, w.tiles + up256(nvfp4::linear_tile_ws_bytes(M, N, K, w4a4)))
+                : o;
   return w;
 }
 
@@ -400,7 +402,7 @@ int linear_run(const char* W, bool w4a4, const uint16_t* x, int64_t M, int64_t N
                 (long long)N, (long long)K);
   if (out_dtype != 0 && out_dtype != 1) return fail(NVFP4_EINVAL, "%s: EINVAL out_dtype=%d", W, out_dtype);
   const LinearWs L = linear_ws(M, N, K, w4a4);
-  const size_t need = epi ? L.total : L.plain;
+  const size_t need = epi ? L.fused : L.plain;
   if (ws_bytes < need || !ws)
     return fail(NVFP4_EWORKSPACE, "%s: EWORKSPACE num_experts=1 M=%lld N=%lld K=%lld workspace_size=%zu needed=%zu",
                 W, (long long)M, (long long)N, (long long)K, ws_bytes, need);
@@ -453,7 +455,8 @@ int linear_run(const char* W, bool w4a4, const uint16_t* x, int64_t M, int64_t N
 
 size_t nvfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4) {
   if (!linear_shape_ok(M, N, K)) return 0;
-  return linear_ws(M, N, K, w4a4 != 0).total;
+  const LinearWs L = linear_ws(M, N, K, w4a4 != 0);
+  return std::max(L.plain, L.fused);
 }
 
 int nvfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,

@@ -810,26 +810,36 @@ bool linear_uses_tiles(int64_t M, int64_t N, int64_t K) {
   return uses_few(M, N, K) || M <= 256 || (M + 127) / 128 * ((N + 255) / 256) < kCUs;
 }
 
-// Workspace: scale and maxima, the activation operand, partial sums.
 namespace {
+// The activations' form for linear_few_kernel.
+FewAct few_act(int64_t M, int64_t K, bool w4a4) {
+  if (w4a4) return M <= 16 && M * K <= kFewQuantMax ? kFewCodes : kFewF16Operand;
+  return M <= kFewRowsMax ? kFewBf16Rows : kFewBf16Operand;
+}
+
+// Workspace of either kernel: W4A4's scale, maxima, the activation operand,
+// partial sums; or the scale and the codes and scales of few rows; bf16 rows
+// taken as they are need none.
 struct TileWs {
   size_t parts, a, part, total;
 };
-TileWs tile_ws(int64_t M, int64_t N, int64_t K) {
-  const TileSplit t = tile_split(M, N, K);
+size_t operand_bytes(int64_t M, int64_t K) { return (size_t)((M + 15) / 16 * 16) * K * 2; }
+TileWs tile_ws(int64_t M, int64_t N, int64_t K, bool w4a4) {
+  const bool few = uses_few(M, N, K);
+  const TileSplit t = few ? TileSplit{} : tile_split(M, N, K);
   TileWs w{};
   w.parts = 256;
   w.a = w.parts + kAmaxParts * 4;
-  w.part = w.a + (size_t)((M + 15) / 16 * 16) * K * 2;
+  w.part = w.a + (few || w4a4 ? operand_bytes(M, K) : 0);
   w.total = w.part + (t.stream ? (size_t)2 * t.grid * t.bm * t.bn * 4 : 0);
+  if (few && few_act(M, K, w4a4) == kFewBf16Rows) w.total = 0;
+  if (few && few_act(M, K, w4a4) == kFewCodes) w.total = 256 + (size_t)M * (K / 2) + (size_t)M * (K / 16);
   return w;
 }
 }  // namespace
 
-static size_t linear_few_ws_bytes(int64_t M, int64_t K) { return 256 + (size_t)M * (K / 2) + (size_t)M * (K / 16); }
-
-size_t linear_tile_ws_bytes(int64_t M, int64_t N, int64_t K) {
-  return M > 0 && linear_uses_tiles(M, N, K) ? std::max(tile_ws(M, N, K).total, linear_few_ws_bytes(M, K)) : 0;
+size_t linear_tile_ws_bytes(int64_t M, int64_t N, int64_t K, bool w4a4) {
+  return M > 0 && linear_uses_tiles(M, N, K) ? tile_ws(M, N, K, w4a4).total : 0;
 }
 
 namespace {
@@ -886,7 +896,8 @@ hipError_t launch_linear_few(const uint16_t* x, int64_t M, int64_t N, int64_t K,
   p.g_w = gw;
   p.g_a = w4a4 ? g : nullptr;
   p.ep = ep;
-  if (w4a4 && M <= 16 && M * K <= kFewQuantMax) {
+  const FewAct act = few_act(M, K, w4a4);
+  if (act == kFewCodes) {
     uint8_t* q = b + 256;
     uint8_t* sf = q + M * (K / 2);
     linear_few_quant_kernel<<<(unsigned)((M * K / 8 + 255) / 256), 256, 0, s>>>(x, M, K, g, q, sf);
@@ -895,11 +906,11 @@ hipError_t launch_linear_few(const uint16_t* x, int64_t M, int64_t N, int64_t K,
     p.a_sf = sf;
     return launch_few_act<kFewCodes>(p, s);
   }
-  if (!w4a4 && M <= kFewRowsMax) {
+  if (act == kFewBf16Rows) {
     p.x = x;
     return launch_few_act<kFewBf16Rows>(p, s);
   }
-  const TileWs L = tile_ws(M, N, K);
+  const TileWs L = tile_ws(M, N, K, w4a4);
   uint16_t* a = reinterpret_cast<uint16_t*>(b + L.a);
   if (hipError_t e = launch_operand(x, M, K, w4a4, reinterpret_cast<uint32_t*>(b + L.parts), g, a, s)) return e;
   p.x = a;
@@ -910,7 +921,7 @@ hipError_t launch_linear_few(const uint16_t* x, int64_t M, int64_t N, int64_t K,
 hipError_t launch_linear_tiles(const uint16_t* x, int64_t M, int64_t N, int64_t K, bool w4a4, const uint8_t* w_prep,
                                const float* gw, const LinearEpi& ep, void* ws, hipStream_t s) {
   if (uses_few(M, N, K)) return launch_linear_few(x, M, N, K, w4a4, w_prep, gw, ep, ws, s);
-  const TileWs L = tile_ws(M, N, K);
+  const TileWs L = tile_ws(M, N, K, w4a4);
   uint8_t* b = static_cast<uint8_t*>(ws);
   float* g = reinterpret_cast<float*>(b);
   uint16_t* a = reinterpret_cast<uint16_t*>(b + L.a);

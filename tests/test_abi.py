@@ -380,7 +380,12 @@ def test_fused_linear_refuses_aliases(lib):
 
 def _needed(lib, name, M, N, K):
     """What a dense call demands of its workspace (from the refusal of an empty one)."""
-    assert getattr(lib, name)(None, M, N, K, None, None, None, 0, 4096, 0, None) == _lib.NVFP4_EWORKSPACE
+    args = (None, M, N, K, None, None)
+    if name.endswith("_fused"):
+        args += (ctypes.byref(_lib.Epilogue(ld_out=N)), 4096)
+    else:
+        args += (None,)
+    assert getattr(lib, name)(*args, 0, 4096, 0, None) == _lib.NVFP4_EWORKSPACE
     return int(re.search(r"needed=(\d+)", _lib.last_error()).group(1))
 
 
@@ -402,3 +407,30 @@ def test_plain_linear_takes_a_workspace_of_more_rows(lib, N, K):
                 assert need[M] <= sizes[more], (M, more)
                 assert getattr(lib, name)(None, M, N, K, None, None, None, 0, 4096, sizes[more],
                                           None) == _lib.NVFP4_EINVAL and "null" in _lib.last_error()
+
+
+def test_fused_linear_demands_what_its_kernel_uses(lib):
+    """The fused layers' workspace by the kernel that runs: bf16 rows as they
+    are need none (256 bytes for any call); a few quantised rows are their
+    codes and scales, the operand layout is 2 bytes an element; partial sums (two
+    a workgroup, 64 x 256 floats each at most) only where K is dealt out."""
+    w16, w4 = "nvfp4_linear_w4a16_fused", "nvfp4_linear_fused"
+    for N, K in ((34816, 5120), (5120, 17408), (4096, 1024), (128, 128)):
+        for M in (1, 5, 8):
+            assert _needed(lib, w16, M, N, K) == 256
+        for M in (9, 16):                                 # operand layout of 16 rows
+            assert 32 * K <= _needed(lib, w16, M, N, K) <= 32 * K + 4096
+        for M in (1, 4, 16):                              # scale, then codes or the operand layout
+            assert M * K * 9 // 16 <= _needed(lib, w4, M, N, K) <= 32 * K + 4096
+        for M in (40, 64, 200, 256):
+            both = _needed(lib, w4, M, N, K), _needed(lib, w16, M, N, K)
+            rows = 16 * ((M + 15) // 16)
+            parts = 2 * 256 * 64 * 256 * 4
+            assert 2 * rows * K <= both[0] <= 2 * rows * K + parts + 4096
+            assert both[1] <= 2 * rows * K + parts + 4096
+            if K <= 2048:                                 # (too few chunks to deal out)
+                assert both[0] <= 2 * rows * K + 4096
+    # one launch on bf16 rows in whole tiles
+    assert _needed(lib, w16, 203, 4096, 1024) <= 4096
+    # tiles that fill the device: the grouped kernels' workspace
+    assert _needed(lib, w16, 4096, 34816, 5120) == _needed(lib, "nvfp4_linear_w4a16", 4096, 34816, 5120)
