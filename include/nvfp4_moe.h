@@ -311,7 +311,9 @@ int moe_quantize_and_align(const nvfp4_moe_dims* dims, const uint16_t* x, float*
  * out: bfloat16 (out_dtype 0, round to nearest even) or float32 (1) [M][N].
  * ws: nvfp4_linear_workspace_size(M, N, K, w4a4) bytes, 256-byte aligned,
  * zero-filled before its first use (the library leaves its counter words
- * zero after every call).  Errors: NVFP4_ESHAPE, NVFP4_EINVAL,
+ * zero after every call).  That many bytes serve every call of up to M rows
+ * with this N, K and w4a4, with and without the epilogue below; a call of
+ * fewer bytes is refused only where its own kernel needs more.  Errors: NVFP4_ESHAPE, NVFP4_EINVAL,
  * NVFP4_EWORKSPACE (message names M, N, K and the sizes). */
 size_t nvfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4);
 int nvfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,

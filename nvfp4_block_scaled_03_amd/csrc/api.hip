@@ -456,7 +456,7 @@ int linear_run(const char* W, bool w4a4, const uint16_t* x, int64_t M, int64_t N
 size_t nvfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4) {
   if (!linear_shape_ok(M, N, K)) return 0;
   const LinearWs L = linear_ws(M, N, K, w4a4 != 0);
-  return std::max(L.plain, L.fused);
+  return std::max(L.plain, L.tiles + up256(nvfp4::linear_tile_ws_bound(M, N, K, w4a4 != 0)));
 }
 
 int nvfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,

@@ -204,6 +204,7 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 // ws of linear_tile_ws_bytes(M, N, K, w4a4), 256-byte aligned, no initial contents.
 bool linear_uses_tiles(int64_t M, int64_t N, int64_t K);
 size_t linear_tile_ws_bytes(int64_t M, int64_t N, int64_t K, bool w4a4);
+size_t linear_tile_ws_bound(int64_t M, int64_t N, int64_t K, bool w4a4);   // of up to M rows
 hipError_t launch_linear_tiles(const uint16_t* x, int64_t M, int64_t N, int64_t K, bool w4a4, const uint8_t* w_prep,
                                const float* gw, const LinearEpi& ep, void* ws, hipStream_t s);
 

@@ -842,6 +842,29 @@ size_t linear_tile_ws_bytes(int64_t M, int64_t N, int64_t K, bool w4a4) {
   return M > 0 && linear_uses_tiles(M, N, K) ? tile_ws(M, N, K, w4a4).total : 0;
 }
 
+// Of every call with up to M rows, growing with M.  Both rules above hold up to
+// some number of rows; the operand grows with the rows, and the partial sums are
+// at most two tiles of 64 x 256 for each workgroup of a layer that deals out K.
+size_t linear_tile_ws_bound(int64_t M, int64_t N, int64_t K, bool w4a4) {
+  auto last = [&](bool (*rule)(int64_t, int64_t, int64_t)) {   // the most rows up to M that it holds for
+    int64_t lo = 0, hi = M;
+    while (lo < hi) {
+      const int64_t m = (lo + hi + 1) / 2;
+      if (rule(m, N, K)) lo = m;
+      else hi = m - 1;
+    }
+    return lo;
+  };
+  const int64_t rows = last(linear_uses_tiles), few = last(uses_few), KC = K / kBK;
+  const int64_t operand = w4a4 ? rows : few > kFewRowsMax ? few : 0;
+  size_t bytes = 256 + kAmaxParts * 4 + operand_bytes(operand, K);
+  if (rows > few && KC > kJoinChunks) {   // (a layer of fewer chunks has nothing to gain from dealing them out)
+    const int64_t tiles = (rows + 47) / 48 * ((N + 255) / 256);
+    bytes += (size_t)2 * std::min<int64_t>(kCUs, std::max<int64_t>(1, tiles * KC / kMinRun)) * 64 * 256 * 4;
+  }
+  return rows > 0 ? bytes : 0;
+}
+
 namespace {
 template <int ACT, bool GATED, int MT, int NT, int KW>
 hipError_t launch_few_t(const FewParams& p, hipStream_t s) {

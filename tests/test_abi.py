@@ -434,3 +434,21 @@ def test_fused_linear_demands_what_its_kernel_uses(lib):
     assert _needed(lib, w16, 203, 4096, 1024) <= 4096
     # tiles that fill the device: the grouped kernels' workspace
     assert _needed(lib, w16, 4096, 34816, 5120) == _needed(lib, "nvfp4_linear_w4a16", 4096, 34816, 5120)
+
+
+@pytest.mark.parametrize("N,K", [(34816, 5120), (5120, 17408), (4096, 1024), (8192, 8192), (128, 128), (384, 16384),
+                                 (12160, 2304), (65536, 640), (1 << 20, 128)])
+def test_linear_workspace_serves_fewer_rows(lib, N, K):
+    """nvfp4_linear_workspace_size(M, ...) bytes serve every call, with or
+    without an epilogue, of up to M rows; the size grows with M."""
+    Ms = sorted({m + d for m in (1, 8, 16, 32, 48, 64, 128, 192, 256, 300, 512, 1024, 1900, 4096, 8192, 32768)
+                 for d in (-1, 0, 1) if m + d > 0})
+    for w4a4 in (0, 1):
+        names = ("nvfp4_linear", "nvfp4_linear_fused") if w4a4 else ("nvfp4_linear_w4a16", "nvfp4_linear_w4a16_fused")
+        before = 0
+        for M in Ms:
+            size = lib.nvfp4_linear_workspace_size(M, N, K, w4a4)
+            assert size >= before, M
+            before = size
+            for n in names:
+                assert _needed(lib, n, M, N, K) <= size, (n, M)
