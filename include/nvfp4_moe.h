@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define NVFP4_MOE_ABI_VERSION 10
+#define NVFP4_MOE_ABI_VERSION 11
 
 /* Status codes. */
 #define NVFP4_OK 0
@@ -312,10 +312,14 @@ int moe_quantize_and_align(const nvfp4_moe_dims* dims, const uint16_t* x, float*
  * ws: nvfp4_linear_workspace_size(M, N, K, w4a4) bytes, 256-byte aligned,
  * zero-filled before its first use (the library leaves its counter words
  * zero after every call).  That many bytes serve every call of up to M rows
- * with this N, K and w4a4, with and without the epilogue below; a call of
- * fewer bytes is refused only where its own kernel needs more.  Errors: NVFP4_ESHAPE, NVFP4_EINVAL,
+ * with this N, K and w4a4, with and without the epilogue below.  One call
+ * demands nvfp4_linear_call_workspace_size(M, N, K, w4a4, fused) bytes (fused:
+ * the calls with an epilogue), as a rule far fewer.  The counter words lie in
+ * the first 512 bytes of W4A4's workspace, and W4A16 has none: nothing else
+ * needs the zeros.  Errors: NVFP4_ESHAPE, NVFP4_EINVAL,
  * NVFP4_EWORKSPACE (message names M, N, K and the sizes). */
 size_t nvfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4);
+size_t nvfp4_linear_call_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4, int fused);
 int nvfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,
                  const float* gw, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream);
 int nvfp4_linear_w4a16(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,

@@ -13,7 +13,7 @@ from ctypes import c_char_p, c_int, c_int32, c_int64, c_size_t, c_void_p
 # variant with different tile settings); the default is the in-tree build.
 LIB_PATH = os.environ.get("NVFP4_MOE_LIB") or os.path.join(
     os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
-ABI_VERSION = 10
+ABI_VERSION = 11
 
 NVFP4_OK = 0
 NVFP4_EINVAL = -1
@@ -72,6 +72,7 @@ SIGNATURES = {
                                        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                        c_void_p, c_size_t, c_void_p]),
     "nvfp4_linear_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int]),
+    "nvfp4_linear_call_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int, c_int]),
     "nvfp4_linear": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int,
                              c_void_p, c_size_t, c_void_p]),
     "nvfp4_linear_w4a16": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,

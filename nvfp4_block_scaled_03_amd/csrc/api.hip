@@ -459,6 +459,12 @@ size_t nvfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4) {
   return std::max(L.plain, L.tiles + up256(nvfp4::linear_tile_ws_bound(M, N, K, w4a4 != 0)));
 }
 
+size_t nvfp4_linear_call_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4, int fused) {
+  if (!linear_shape_ok(M, N, K)) return 0;
+  const LinearWs L = linear_ws(M, N, K, w4a4 != 0);
+  return fused ? L.fused : L.plain;
+}
+
 int nvfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,
                  const float* gw, void* out, int out_dtype, void* ws, size_t ws_bytes, void* stream) {
   return linear_run("nvfp4_linear", true, x, M, N, K, w_prep, gw, nullptr, out, out_dtype, ws, ws_bytes, stream);

@@ -424,8 +424,22 @@ def quantize_linear_weight(w: torch.Tensor, gated: bool = False) -> LinearWeight
 
 
 def linear_workspace(M: int, N: int, K: int, w4a4: bool, device) -> torch.Tensor:
+    """Workspace of every ``linear`` of up to M rows with a weight [N, K]."""
     n = _lib.load().nvfp4_linear_workspace_size(M, N, K, int(w4a4))
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _linear_call_workspace(M: int, N: int, K: int, w4a4: bool, fused: bool, device) -> torch.Tensor:
+    """Workspace of one ``linear`` alone: what that call demands, with zeros
+    where W4A4 counts (its first 512 bytes).  A small one is cleared whole: the
+    time is the host's, and taking a slice of it costs 1 us."""
+    n = _lib.load().nvfp4_linear_call_workspace_size(M, N, K, int(w4a4), int(fused))
+    if w4a4 and n <= 1 << 20:
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    if w4a4:
+        ws.narrow(0, 0, 512).zero_()
+    return ws
 
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
@@ -496,11 +510,11 @@ def linear(x: torch.Tensor, w: LinearWeight, variant: str = "w4a4", out_dtype=to
     if bias is not None or act != "none" or residual is not None or w.gated:
         if variant not in ("w4a4", "w4a16"):
             raise ValueError(f"variant {variant!r}: w4a4 or w4a16")
-        ws = ws if ws is not None else linear_workspace(M, w.N, w.K, w4a4, x.device)
+        ws = ws if ws is not None else _linear_call_workspace(M, w.N, w.K, w4a4, True, x.device)
         return _linear_fused("nvfp4_linear_fused" if w4a4 else "nvfp4_linear_w4a16_fused", x, w, w.g, bias, act,
                              residual, out_dtype, out, ws)
     out = out if out is not None else torch.empty(M, w.N, dtype=out_dtype, device=x.device)
-    ws = ws if ws is not None else linear_workspace(M, w.N, w.K, w4a4, x.device)
+    ws = ws if ws is not None else _linear_call_workspace(M, w.N, w.K, w4a4, False, x.device)
     call("nvfp4_linear" if w4a4 else "nvfp4_linear_w4a16", _p(x.contiguous()), M, w.N, w.K, _p(w.prep),
          _p(w.g), _p(out), _dtype_code(out), _p(ws), ws.numel(), _stream())
     return out

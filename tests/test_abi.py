@@ -452,3 +452,13 @@ def test_linear_workspace_serves_fewer_rows(lib, N, K):
             before = size
             for n in names:
                 assert _needed(lib, n, M, N, K) <= size, (n, M)
+
+
+def test_linear_call_workspace_size(lib):
+    """nvfp4_linear_call_workspace_size says what each call demands."""
+    for N, K in ((34816, 5120), (4096, 1024), (128, 128)):
+        for M in (1, 8, 9, 17, 64, 257, 4096):
+            for i, n in enumerate(("nvfp4_linear_w4a16", "nvfp4_linear_w4a16_fused", "nvfp4_linear",
+                                   "nvfp4_linear_fused")):
+                assert lib.nvfp4_linear_call_workspace_size(M, N, K, i // 2, i % 2) == _needed(lib, n, M, N, K)
+    assert lib.nvfp4_linear_call_workspace_size(4, 100, 128, 0, 1) == 0

@@ -526,3 +526,57 @@ def test_refuses_x_as_output(dev):
         w, x = _weight(fmt, 256, 256, False)[0], _x(dev, 4, 256, 1)
         with pytest.raises(_lib.Nvfp4Error):
             _call(fmt, x, w, residual=x, out=x)
+
+
+@pytest.mark.parametrize("fmt", ["w4a4", "w4a16"])
+@pytest.mark.parametrize("M", [1, 8, 9, 16, 64, 200, 300, 1100])
+def test_default_workspace(dev, fmt, M, monkeypatch):
+    """Calls without a workspace allocate what they demand, clear no more of it
+    than the counter words (or 1 MiB), and equal those in a cleared one, bit for
+    bit, whatever the memory held before."""
+    N, K = 8192, 2304
+    wt = [_coded_weight(fmt, N, K, gated)[0] for gated in (False, True)]
+    x, res = _x(dev, M, K, M), torch.randn(M, N // 2, generator=_gen(dev, M), device=dev)
+    ws = ops.linear_workspace(M, N, K, fmt == "w4a4", dev)
+    calls = [(False, N, lambda ws=None: ops.linear(x, wt[0], fmt, ws=ws)),
+             (True, N // 2, lambda ws=None: ops.linear(x, wt[1], fmt, act="silu", residual=res, ws=ws))]
+    cleared = []
+    zeros, zero_ = torch.zeros, torch.Tensor.zero_
+    monkeypatch.setattr(torch, "zeros", lambda *a, **kw: cleared.append(zeros(*a, **kw)) or cleared[-1])
+    monkeypatch.setattr(torch.Tensor, "zero_", lambda t: cleared.append(t) or zero_(t))
+    for fused, cols, run in calls:
+        want = run(ws)
+        cleared.clear()
+        poison = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device=dev)
+        del poison
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        got = run()
+        torch.cuda.synchronize()
+        n = _lib.load().nvfp4_linear_call_workspace_size(M, N, K, int(fmt == "w4a4"), int(fused))
+        # (the allocator hands out up to 1 MiB more than asked for)
+        assert torch.cuda.max_memory_allocated() - before <= n + 2 * M * cols + (2 << 20)
+        assert sum(t.numel() for t in cleared) <= (max(512, n * (n <= 1 << 20)) if fmt == "w4a4" else 0)
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmt", ["w4a4", "w4a16"])
+@pytest.mark.parametrize("M,N,K", [
+    # every form of the few-row kernel, tiles with and without K dealt out, the grouped kernels
+    (1, 512, 384), (8, 512, 384), (9, 512, 384), (16, 8192, 8192), (100, 512, 384), (200, 4096, 1024),
+    (64, 8192, 2304), (100, 8320, 4224), (45, 8448, 6144), (1100, 8192, 128)])
+def test_demanded_workspace_is_enough(dev, fmt, M, N, K):
+    """In exactly the bytes a call demands, between known bytes that stay."""
+    band = 4096
+    w, x = _coded_weight(fmt, N, K, False)[0], _x(dev, M, K, 1)
+    for kw in ({}, dict(act="silu", bias=torch.zeros(N, device=dev))):
+        n = _lib.load().nvfp4_linear_call_workspace_size(M, N, K, int(fmt == "w4a4"), int(bool(kw)))
+        full = torch.full((2 * band + n,), 0xA5, dtype=torch.uint8, device=dev)
+        if fmt == "w4a4":
+            full[band:band + 512] = 0
+        got = ops.linear(x, w, fmt, ws=full[band:band + n], **kw)
+        assert (full[:band] == 0xA5).all() and (full[band + n:] == 0xA5).all()
+        assert torch.equal(got, ops.linear(x, w, fmt, **kw))
+        with pytest.raises(_lib.Nvfp4Error):
+            ops.linear(x, w, fmt, ws=full[band:band + n - 1], **kw)
