@@ -336,8 +336,8 @@ int nvfp4_linear_w4a16(const uint16_t* x, int64_t M, int64_t N, int64_t K, const
  *   plain:  y[m][n] = act(v[m][n])                            N columns
  *   gated:  y[m][i] = act(v[m][i]) * v[m][N/2 + i]            N/2 columns
  *   out[m][n] = y[m][n] + residual[m][n], rounded once to out_dtype
- * All of it is FP32.  Activations: NVFP4_ACT_RELU max(v, 0), NVFP4_ACT_SILU
- * v / (1 + e^-v), NVFP4_ACT_GELU v Phi(v) (the normal distribution function),
+ * All of it is FP32.  Activations: NVFP4_ACT_RELU max(v, 0) (NaN stays NaN, as
+ * through every other), NVFP4_ACT_SILU v / (1 + e^-v), NVFP4_ACT_GELU v Phi(v) (the normal distribution function),
  * NVFP4_ACT_GELU_TANH v / (1 + e^-2u) with u = sqrt(2/pi) (v + 0.044715 v^3).
  *
  * Plain weights are prepared as for the calls without an epilogue.  Gated

@@ -47,7 +47,7 @@ __device__ __forceinline__ void act_apply(int act, float (&z)[N]) {
   switch (act) {
     case kFnRelu:
 #pragma unroll
-      for (int r = 0; r < N; ++r) z[r] = z[r] > 0.0f ? z[r] : 0.0f;
+      for (int r = 0; r < N; ++r) z[r] = z[r] <= 0.0f ? 0.0f : z[r];   // (NaN stays)
       break;
     // z / (1 + e^-z): the hardware exponential and reciprocal (1 ulp each).
     case kFnSilu:

@@ -580,3 +580,53 @@ def test_demanded_workspace_is_enough(dev, fmt, M, N, K):
         assert torch.equal(got, ops.linear(x, w, fmt, **kw))
         with pytest.raises(_lib.Nvfp4Error):
             ops.linear(x, w, fmt, ws=full[band:band + n - 1], **kw)
+
+
+# One size for each kernel: few rows in each form, tiles, tiles with K dealt out, what fills the device.
+KERNELS = [(3, 512, 384), (12, 512, 384), (100, 512, 384), (70, 768, 5120), (1100, 8192, 128)]
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("M,N,K", KERNELS)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_nan_and_infinity_go_through(dev, fmt, M, N, K, act):
+    """NaN and infinity in bias, residual and (W4A16) x come out where the
+    definition has them, of every activation, plain and gated."""
+    for gated in (False, True):
+        wt = _coded_weight(fmt, N, K, gated)
+        n_out = N // 2 if gated else N
+        x = _x(dev, M, K, 3)
+        if fmt == "w4a16":
+            x[M // 2, 5] = float("nan")
+            x[M - 1, K - 1] = float("inf")
+        bias = torch.randn(N, generator=_gen(dev, 4), device=dev)
+        bias[3], bias[64], bias[n_out - 1] = float("nan"), float("inf"), float("-inf")
+        if gated:
+            bias[n_out + 7] = float("nan")
+            bias[n_out + 65:n_out + 68] = torch.tensor([float("inf"), float("-inf"), 0.0], device=dev)
+        res = torch.randn(M, n_out, generator=_gen(dev, 5), device=dev)
+        res[0, 9], res[M - 1, 10], res[1, 11] = float("nan"), float("inf"), float("-inf")
+        got = to_np(_call(fmt, x, wt[0], bias=bias, act=act, residual=res, out_dtype=torch.float32)).astype(np.float64)
+        rows = np.unique(np.r_[0:min(M, 12), M // 2, M - 1])
+        at = torch.from_numpy(rows).to(dev)
+        if fmt == "w4a4":
+            xf = to_np(x.float()).astype(np.float64)
+            gs = onv.global_scale(xf)
+            x_hat = onv.dequantize(*onv.quantize(xf[rows], gs), gs)
+        else:
+            x_hat = _operand(fmt, x[at])
+        with np.errstate(all="ignore"):
+            ref, bound = _reference(fmt, x[at], wt[1], bias, act, gated, res[at], torch.float32, x_hat)
+            got = got[rows]
+            # An activation below 2^-120 may come out as zero in FP32 (_act_error: e^-z past the largest float
+            # makes the quotient 0), and zero times an infinite up projection is NaN where the definition has an
+            # infinity.
+            lost = np.zeros(ref.shape, bool)
+            if gated:
+                v = x_hat @ wt[1].T + to_np(bias).astype(np.float64)
+                lost = np.isinf(v[:, n_out:]) & (np.abs(olin.activation(v[:, :n_out], act)) < 2.0 ** -120)
+            assert (lost | (np.isnan(got) == np.isnan(ref))).all()
+            assert (lost | (got == ref) | ~np.isinf(ref)).all()
+            fin = np.isfinite(ref)
+            assert fin.any() and np.isnan(ref).any() and np.isinf(ref).any()
+            assert (np.abs(got - ref)[fin] <= bound[fin]).all()
