@@ -70,6 +70,13 @@ __device__ __forceinline__ void act_apply(int act, float (&z)[N]) {
   }
 }
 
+// Rounding of an output to bfloat16 bits.  The sum may hold a caller's NaN of
+// any payload (bias and residual are float32), and the rounding of finite
+// values would carry a payload of ones into the sign: 0x7FFFFFFF to -0.
+__device__ __forceinline__ uint32_t out_bf16_bits(float f) {
+  return f == f ? f32_to_bf16_bits(f) : ((uint32_t)__float_as_int(f) >> 16) | 0x40u;
+}
+
 // Residual values and output stores: element (row, col) and four consecutive
 // columns (col a multiple of 4; pointers and strides keep 4 elements together).
 __device__ __forceinline__ float epi_residual(const LinearEpi& e, int64_t row, int64_t col) {
@@ -81,7 +88,7 @@ __device__ __forceinline__ float epi_residual(const LinearEpi& e, int64_t row, i
 __device__ __forceinline__ void epi_store(const LinearEpi& e, int64_t row, int64_t col, float y) {
   const int64_t o = row * e.ldo + col;
   if (e.out_f32) static_cast<float*>(e.out)[o] = y;
-  else static_cast<uint16_t*>(e.out)[o] = (uint16_t)f32_to_bf16_bits(y);
+  else static_cast<uint16_t*>(e.out)[o] = (uint16_t)out_bf16_bits(y);
 }
 __device__ __forceinline__ void epi_finish4(const LinearEpi& e, int64_t row, int64_t col, f32x4 y) {
   if (e.res) {
@@ -100,8 +107,8 @@ __device__ __forceinline__ void epi_finish4(const LinearEpi& e, int64_t row, int
   if (e.out_f32) {
     *reinterpret_cast<f32x4*>(static_cast<float*>(e.out) + o) = y;
   } else {
-    const uint32_t lo = f32_to_bf16_bits(y[0]) | (f32_to_bf16_bits(y[1]) << 16);
-    const uint32_t hi = f32_to_bf16_bits(y[2]) | (f32_to_bf16_bits(y[3]) << 16);
+    const uint32_t lo = out_bf16_bits(y[0]) | (out_bf16_bits(y[1]) << 16);
+    const uint32_t hi = out_bf16_bits(y[2]) | (out_bf16_bits(y[3]) << 16);
     *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(e.out) + o) = u32x2{lo, hi};
   }
 }
@@ -251,8 +258,8 @@ __device__ __forceinline__ void epi_finish(const LinearEpi& ep, float (&z)[4 * N
     if (ep.out_f32) {
       *reinterpret_cast<f32x4*>(static_cast<float*>(ep.out) + o) = y;
     } else {
-      const uint32_t lo = f32_to_bf16_bits(y[0]) | (f32_to_bf16_bits(y[1]) << 16);
-      const uint32_t hi = f32_to_bf16_bits(y[2]) | (f32_to_bf16_bits(y[3]) << 16);
+      const uint32_t lo = out_bf16_bits(y[0]) | (out_bf16_bits(y[1]) << 16);
+      const uint32_t hi = out_bf16_bits(y[2]) | (out_bf16_bits(y[3]) << 16);
       *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(ep.out) + o) = u32x2{lo, hi};
     }
   }

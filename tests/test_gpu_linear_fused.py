@@ -630,3 +630,25 @@ def test_nan_and_infinity_go_through(dev, fmt, M, N, K, act):
             fin = np.isfinite(ref)
             assert fin.any() and np.isnan(ref).any() and np.isinf(ref).any()
             assert (np.abs(got - ref)[fin] <= bound[fin]).all()
+
+
+@pytest.mark.parametrize("M,N,K", KERNELS)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_every_float_rounds_to_bfloat16(dev, fmt, M, N, K):
+    """All-zero activations: the bf16 output is the float32 residual rounded to
+    the nearest, ties to even, for any bits: subnormal, largest, infinite, and
+    NaN of any payload (which stays NaN)."""
+    w = _coded_weight(fmt, N, K, False)[0]
+    bits = torch.randint(-2 ** 31, 2 ** 31, (M, N), generator=_gen(dev, 6), dtype=torch.int64, device=dev)
+    bits[:, ::7] &= ~0xFFFF                      # on a step, and halfway between two
+    bits[:, ::14] |= 0x8000
+    bits[:, 1::32] &= ~0x7F800000                # subnormal
+    for i, b in enumerate((0x7FFFFFFF, -1, 0x7F800001, 0x7FC00000, 0x7F80FFFF, 0x7F7FFFFF, 0x7F7F7FFF, 0x7F800000,
+                           -0x00800000, 1, 0x8000, 0x7FFF)):
+        bits[i % M, 2 + 16 * i] = b
+    res = bits.to(torch.int32).view(torch.float32)
+    got = _call(fmt, torch.zeros(M, K, dtype=torch.bfloat16, device=dev), w, residual=res).cpu()
+    want = res.cpu().to(torch.bfloat16)
+    nan = torch.isnan(res.cpu())
+    assert nan.any() and torch.equal(torch.isnan(got), nan)
+    assert torch.equal(got[~nan], want[~nan])
