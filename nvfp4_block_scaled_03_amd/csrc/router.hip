@@ -51,9 +51,11 @@ __device__ __forceinline__ SplitW split_f32(const f32x4& lo, const f32x4& hi) {
   return s;
 }
 
-// s_waitcnt immediate: at most n vector memory operations outstanding (the
-// LDS and export counters left at their maxima).
-constexpr int gate_vmcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+// s_waitcnt immediate: at most n vector memory operations outstanding, and no
+// LDS read (the export counter left at its maximum): the next direct load goes
+// into the slot that was read last, and where a group is one wavefront no
+// barrier stands between.
+constexpr int gate_wait(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
 
 template <bool F32W, int RM, int RN, int WR, int WC, int KW, int D>
 __global__ __launch_bounds__(WR * WC * KW * kWave) void gate_kernel(const uint16_t* __restrict__ x, int64_t ldx,
@@ -159,7 +161,8 @@ __global__ __launch_bounds__(WR * WC * KW * kWave) void gate_kernel(const uint16
   // Ring: at the top of trip c the chunks c .. c + D - 2 of the group are in
   // flight; once at most (D - 2) LPW loads remain, chunk c has landed.  The
   // barrier publishes it to the group and says that every wavefront is done
-  // with the slot refilled next; a group of one wavefront needs none.
+  // with the slot refilled next; a group of one wavefront needs none, its own
+  // LDS reads being awaited.
   if (chunks > 0) {
 #pragma unroll
     for (int c = 0; c < D - 1; ++c) issue(c, c);
@@ -167,7 +170,7 @@ __global__ __launch_bounds__(WR * WC * KW * kWave) void gate_kernel(const uint16
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (c0 + d < trips) {
-          __builtin_amdgcn_s_waitcnt(gate_vmcnt((D - 2) * LPW));
+          __builtin_amdgcn_s_waitcnt(gate_wait((D - 2) * LPW));
           if constexpr (G > 1) __syncthreads();
           else asm volatile("" ::: "memory");
           issue(c0 + d + D - 1, (d + D - 1) % D);
@@ -176,7 +179,7 @@ __global__ __launch_bounds__(WR * WC * KW * kWave) void gate_kernel(const uint16
       }
     }
     // The loads past the end land before the ring is used again or given up.
-    __builtin_amdgcn_s_waitcnt(gate_vmcnt(0));
+    __builtin_amdgcn_s_waitcnt(gate_wait(0));
   }
   // The last H % 64 elements (a multiple of 8: a piece is in or out), straight
   // from memory, by the last group.

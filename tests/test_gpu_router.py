@@ -93,6 +93,26 @@ def test_gate_row_stays_its_own(dev):
     assert torch.equal(got[keep], clean[keep])
 
 
+@pytest.mark.parametrize("wdt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,E,H", [(5, 128, 8192), (64, 60, 8256), (120, 16, 16384), (1000, 120, 4096), (2000, 40, 4104)])
+def test_gate_long_ring(dev, T, E, H, wdt):
+    """Many trips around the ring of a one-wavefront group, beside another
+    stream's traffic: the same bits every time."""
+    g = _gen(dev, T)
+    x = torch.randn(T, H, generator=g, device=dev).to(torch.bfloat16)
+    w = (0.05 * torch.randn(E, H, generator=g, device=dev)).to(wdt)
+    first = ops.gate_logits(x, w)
+    _check_gate(x, w, None, first)
+    side, a = torch.cuda.Stream(), torch.empty(1 << 26, device=dev)
+    b = torch.zeros_like(a)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            a.copy_(b)
+        assert torch.equal(ops.gate_logits(x, w), first)
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("T", [4, 7])
 def test_gate_rows_far_apart(dev, T):
     """Rows whose offsets pass 2^31 elements."""
