@@ -18,9 +18,10 @@ namespace nvfp4 {
 // polynomial in u = (w - c) / (w + c), which maps [0, inf) to [-1, 1); degree 8
 // with c = 3.75, a least-maximum fit of its own over w <= 14.2, is within
 // 1.5e-8 of it.  Beyond, the exponential is 0 in FP32 or nearly so.  Against
-// FP64 in FP32 steps of the result: 6 for |z| < 3, growing as z^2 with the
-// exponential.  A quarter of the instructions of erfcf (a 203 x 4096 layer:
-// 2 us of 16).
+// FP64, in FP32 steps of the result (2^20 x 40 arguments a stretch): 8 for
+// -1 < z < 1, 10 down to -3, 33 down to -6, growing as z^2 with the exponential,
+// 125 at -13; 1.5 above 1 and half a step above 3.  A quarter of the
+// instructions of erfcf (a 203 x 4096 layer: 2 us of 16).
 __device__ __forceinline__ float gelu_fast(float z) {
   const float w = fminf(fabsf(z), 100.0f);
   const float r = __builtin_amdgcn_rcpf(w + 3.75f), u = __builtin_fmaf(r, -7.5f, 1.0f);

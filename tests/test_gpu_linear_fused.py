@@ -301,6 +301,31 @@ def test_activations_far_out(dev, act, gated):
     _check("w4a16", x, wt, bias, act, gated, None, got)
 
 
+@pytest.mark.parametrize("lo,hi", [(-0.01, 0.01), (-1, 0), (0, 1), (-3, -1), (1, 3), (-6, -3), (-14, -6), (3, 14)])
+def test_gelu_steps(dev, lo, hi):
+    """GELU over 2^20 arguments a stretch (the bias, on a product of zero).
+
+    z Phi(z) = max(z, 0) - z q e, with H half a step, relative: the reciprocal
+    of a rounded sum is off by 3 H, w r by 4; the polynomial's argument by
+    (1 - u) 3 H + H, 7 at most, times its slope over its value, at most 1.04;
+    its own roundings add 3 and the fit 1 (1.5e-8 of 0.4 or more); the exponential's
+    argument w^2 / 2 is off by 2.5 H and the exponential by 2; two products add
+    2.  In all 20 + 1.25 z^2 half steps of z q e, and one of the sum."""
+    N, K = 1 << 20, 128
+    w = ops.prepare_linear_weight(torch.zeros(N, K // 2, dtype=torch.uint8, device=dev),
+                                  torch.full((N, K // 16), 56, dtype=torch.uint8, device=dev),
+                                  torch.ones(1, device=dev))
+    z = torch.empty(N, device=dev).uniform_(lo, hi, generator=_gen(dev, 3))
+    got = ops.linear(torch.zeros(1, K, dtype=torch.bfloat16, device=dev), w, "w4a16", bias=z, act="gelu",
+                     out_dtype=torch.float32)[0].double()
+    z = z.double()
+    ref = 0.5 * z * torch.special.erfc(-z / 2.0 ** 0.5)
+    tail = 0.5 * z.abs() * torch.special.erfc(z.abs() / 2.0 ** 0.5)
+    bound = HALF * ((20 + 1.25 * z * z) * tail + ref.abs()) + 2.0 ** -120
+    err = (got - ref).abs()
+    assert (err <= bound).all(), float((err / bound).max())
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M", [1, 3, 30, 70, 200])
 def test_nothing_added_is_the_plain_layer(dev, fmt, M):
