@@ -162,8 +162,17 @@ constexpr int kNT = 4;        // column tiles of a wavefront: 64 columns
 constexpr int kCUs = 256;
 // Dealing out chunks pays where it takes more than kJoinChunks chunks (of 0.3
 // to 0.5 us) off the longest path: the join is a launch and a round trip of the
-// partial sums, about 5 us.  A run is at least kMinRun chunks, so that its
-// start (the first loads' way from memory) stays the smaller part.
+// partial sums, about 5 us.  Measured (us, whole tiles / dealt out, W4A16 and
+// W4A4): 9 chunks off (34816 x 2560 M = 64) 30.5 / 33.8, 32.2 / 38.6; 14 (34816 x
+// 3840) 40.7 / 39.9, 40.2 / 43.0; 16 (8192 x 8192 M = 330) 73 / 69, 68 / 67; 18
+// (34816 x 5120 M = 64) 51 / 46, 48.5 / 48.3; 32 (8192 x 8192 M = 200) 72 / 47,
+// 67 / 49.  Where the tiles are fewer than the CUs, a run is kMinRun chunks or
+// more, so that its start (the first loads' way from memory) stays the smaller
+// part: runs of 4 / 8 / 16, W4A16, 2560 x 4096 M = 200 27.1 / 22.6 / 27.8, 1280 x
+// 17408 M = 100 29.3 / 25.2 / 31.5, 640 x 16384 M = 64 22.3 / 21.6 / 26.4.  The few
+// tiles left over from whole rounds are dealt to all workgroups all the same,
+// down to runs of one chunk: 32896 x 4096 M = 100 (258 tiles) 61 us, 80 in whole
+// tiles.
 constexpr int kJoinChunks = 16, kMinRun = 8;
 
 // s_waitcnt immediate: at most n vector memory operations outstanding (the

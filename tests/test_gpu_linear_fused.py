@@ -234,6 +234,14 @@ def test_fused_columns_left_over(dev, fmt, M, N, K):
     test_fused_large(dev, fmt, M, N, K)
 
 
+@pytest.mark.parametrize("fmt", ["w4a4", "w4a16"])
+@pytest.mark.parametrize("M,N,K", [(100, 32896, 2432), (250, 16640, 2432), (150, 22016, 2560)])
+def test_fused_runs_of_a_chunk(dev, fmt, M, N, K):
+    """A few tiles more than workgroups (258 and 260): those left over are dealt
+    out in runs of a chunk or none."""
+    test_fused_large(dev, fmt, M, N, K)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,N", [(65552, 33024), (17, 1 << 20)])
 def test_fused_large_output(dev, fmt, M, N):
