@@ -175,10 +175,6 @@ constexpr int kCUs = 256;
 // tiles.
 constexpr int kJoinChunks = 16, kMinRun = 8;
 
-// s_waitcnt immediate: at most n vector memory operations outstanding (the
-// LDS and export counters left at their maxima).
-constexpr int vmcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
-
 // How a layer is cut up, from its sizes.
 struct TileSplit {
   int cfg;           // launch_tile's case
