@@ -94,6 +94,25 @@ def test_gate_row_stays_its_own(dev):
 
 
 @pytest.mark.parametrize("wdt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,E,H", [(1, 24, 256), (3, 24, 256), (4, 130, 2056), (40, 24, 256), (300, 130, 520),
+                                   (1100, 128, 128), (4100, 128, 72)])
+def test_gate_row_whatever_its_place(dev, T, E, H, wdt):
+    """At one T a row's logits are the same bits in any place and beside any
+    other rows, NaN and infinity among them."""
+    g = _gen(dev, T)
+    x = torch.randn(T, H, generator=g, device=dev).to(torch.bfloat16)
+    w = torch.randn(E, H, generator=g, device=dev).to(wdt)
+    b = torch.randn(E, generator=g, device=dev)
+    want = ops.gate_logits(x, w, b)
+    at = torch.randperm(T, generator=g, device=dev)
+    assert torch.equal(ops.gate_logits(x[at], w, b), want[at])
+    keep = torch.arange(T, device=dev) % 3 == 0
+    other = torch.randn(T, H, generator=g, device=dev).to(torch.bfloat16)
+    other[1::6], other[4::6] = float("nan"), float("inf")
+    assert torch.equal(ops.gate_logits(torch.where(keep[:, None], x, other), w, b)[keep], want[keep])
+
+
+@pytest.mark.parametrize("wdt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,E,H", [(5, 128, 8192), (64, 60, 8256), (120, 16, 16384), (1000, 120, 4096), (2000, 40, 4104)])
 def test_gate_long_ring(dev, T, E, H, wdt):
     """Many trips around the ring of a one-wavefront group, beside another
