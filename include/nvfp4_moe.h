@@ -315,8 +315,8 @@ int moe_quantize_and_align(const nvfp4_moe_dims* dims, const uint16_t* x, float*
  * with this N, K and w4a4, with and without the epilogue below.  One call
  * demands nvfp4_linear_call_workspace_size(M, N, K, w4a4, fused) bytes (fused:
  * the calls with an epilogue), as a rule far fewer.  The counter words lie in
- * the first 512 bytes of W4A4's workspace, and W4A16 has none: nothing else
- * needs the zeros.  Errors: NVFP4_ESHAPE, NVFP4_EINVAL,
+ * the first 512 bytes of W4A4's workspace, and W4A16 has none and leaves them
+ * alone: nothing else needs the zeros, and one workspace serves both in turn.  Errors: NVFP4_ESHAPE, NVFP4_EINVAL,
  * NVFP4_EWORKSPACE (message names M, N, K and the sizes). */
 size_t nvfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4);
 size_t nvfp4_linear_call_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4, int fused);

@@ -334,8 +334,11 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K, bool w4a4) {
   LinearWs w{};
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += up256(bytes); return at; };
-  w.g = take(w4a4 ? 4 : 0);
-  w.gs = take(w4a4 ? nvfp4_global_scale_workspace_size(1, std::max<int64_t>(M * K, 8)) : 0);
+  // W4A4: the scale and, in bytes that no W4A16 call writes (its first 8 are
+  // offsets, the next from 256 on), the counter words.
+  w.g = take(w4a4 ? 256 : 0);
+  take(w4a4 ? 256 : 0);
+  w.gs = w.g + 64;
   // The fused layers' own kernels use what follows the counter words, which
   // stay zero between calls of either kind.
   w.tiles = o;

@@ -685,3 +685,22 @@ def test_every_float_rounds_to_bfloat16(dev, fmt, M, N, K):
     nan = torch.isnan(res.cpu())
     assert nan.any() and torch.equal(torch.isnan(got), nan)
     assert torch.equal(got[~nan], want[~nan])
+
+
+def test_one_workspace_for_both_kinds(dev):
+    """W4A4 and W4A16 calls, with and without an epilogue, in turn in one
+    workspace; what W4A4 counts in (64 bytes in) is zero after each."""
+    N, K = 512, 8192                                # (M K > 2^18 from 33 rows on: the scale is counted together)
+    w = _coded_weight("w4a16", N, K, False)[0]
+    Ms = (40, 1, 1100, 16, 300)
+    xs = {M: _x(dev, M, K, M) for M in Ms}
+    xs[300].zero_()
+    bias = torch.randn(N, generator=_gen(dev, 1), device=dev)
+    ws = max((ops.linear_workspace(M, N, K, True, dev) for M in Ms), key=lambda t: t.numel())
+    for _ in range(2):
+        for M in Ms:
+            for fmt in ("w4a16", "w4a4"):
+                for kw in ({}, dict(bias=bias)):
+                    got = ops.linear(xs[M], w, fmt, ws=ws, **kw)
+                    assert (ws[64:72] == 0).all(), (M, fmt, kw)
+                    assert torch.equal(got, ops.linear(xs[M], w, fmt, **kw)), (M, fmt)
