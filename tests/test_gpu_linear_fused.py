@@ -704,3 +704,19 @@ def test_one_workspace_for_both_kinds(dev):
                     got = ops.linear(xs[M], w, fmt, ws=ws, **kw)
                     assert (ws[64:72] == 0).all(), (M, fmt, kw)
                     assert torch.equal(got, ops.linear(xs[M], w, fmt, **kw)), (M, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["w4a4", "mxfp4"])
+@pytest.mark.parametrize("M,N,K", KERNELS)
+def test_quantised_nan_is_the_plain_layers(dev, fmt, M, N, K):
+    """NaN in quantised activations: the same operand as without an epilogue
+    (a NaN takes no part in a block's scale and becomes a zero)."""
+    wt = _coded_weight(fmt, N, K, False)
+    x = _x(dev, M, K, 3)
+    x[::2, 5], x[M - 1, K - 16:] = float("nan"), float("nan")
+    got = _call(fmt, x, wt[0], bias=torch.zeros(N, device=dev), out_dtype=torch.float32)
+    want = _call(fmt, x, wt[0], out_dtype=torch.float32)
+    clean = torch.where(torch.isnan(x), torch.zeros_like(x), x)
+    assert torch.isfinite(got).all()
+    assert torch.equal(got, _call(fmt, clean, wt[0], bias=torch.zeros(N, device=dev), out_dtype=torch.float32))
+    assert torch.equal(want, _call(fmt, clean, wt[0], out_dtype=torch.float32))
