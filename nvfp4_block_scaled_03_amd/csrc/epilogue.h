@@ -71,11 +71,13 @@ __device__ __forceinline__ void act_apply(int act, float (&z)[N]) {
   }
 }
 
-// Rounding of an output to bfloat16 bits.  The sum may hold a caller's NaN of
-// any payload (bias and residual are float32), and the rounding of finite
-// values would carry a payload of ones into the sign: 0x7FFFFFFF to -0.
+// Rounding of an output to bfloat16 bits by the hardware conversion: to the
+// nearest, ties to even, and NaN of any payload stays NaN (a caller's bias or
+// residual may hold one; integer rounding would carry a payload of ones into the
+// sign, 0x7FFFFFFF to -0, and with a test for it cost 5120 x 17408 M = 4096 653
+// against 649 us).
 __device__ __forceinline__ uint32_t out_bf16_bits(float f) {
-  return f == f ? f32_to_bf16_bits(f) : ((uint32_t)__float_as_int(f) >> 16) | 0x40u;
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
 // Residual values and output stores: element (row, col) and four consecutive
