@@ -148,15 +148,15 @@ __global__ __launch_bounds__(256) void linear_operand_kernel(const uint16_t* __r
 //
 // A workgroup's CW x KW wavefronts: each owns 16 MT rows x 64 columns, and the
 // KW groups split the chunks of a run.  The activations of a chunk go into LDS
-// once for the group's wavefronts, double buffered.  What bounds the kernel
-// where weights do not is the traffic from L2 to the CUs, about 12 TB/s over
-// the device: with each wavefront loading its own activation fragments, 64 rows
-// x 64 columns each, M = 64, N = 34816, K = 5120 moved 435 MB and took 34 us.
-// The weights of the chunk after next are requested as soon as the registers
-// of the present one are read.  Measured, whole layers: W4A4 34816 x 5120
-// M = 64 47 us, of which the activations take 9.6 (maximum, quantisation),
-// the product 33 and the join 5; M = 128 66 us (696 TFLOP/s); W4A16
-// 5120 x 17408 M = 512 112 us (812 TFLOP/s).
+// once for the group's wavefronts, double buffered: M = 64, N = 34816, K = 5120
+// moves 190 MB from L2 to the CUs, 435 MB with each wavefront loading its own
+// fragments, 64 rows x 64 columns.  The weights of the chunk after next are
+// requested as soon as the registers of the present one are read.  Measured,
+// whole layers: W4A4 34816 x 5120 M = 64 48 us, of which the activations take 9
+// (maximum, quantisation), the product 34 and the join 6; M = 128 67 us (680
+// TFLOP/s); W4A16 5120 x 17408 M = 512 113 us (807 TFLOP/s).  What bounds it at M = 64:
+// the weight stream (21 us alone) and the matrix work (16 us) run in good part
+// one after the other, for the epilogue's LDS leaves room for one workgroup a CU.
 // ---------------------------------------------------------------------------
 constexpr int kNT = 4;        // column tiles of a wavefront: 64 columns
 constexpr int kCUs = 256;
@@ -551,10 +551,10 @@ TileSplit tile_split_as(int cfg, int64_t M, int64_t N, int64_t K) {
 }
 
 // Row blocks of even height; 128 columns a workgroup where the tiles are few
-// and short, else 256.  Measured (us, the whole W4A16 layer, 128 / 256 columns):
-// 4096 x 1024 M = 256 15.7 / 19.8, 8192 x 512 M = 256 13.9 / 16.0; longer or
-// more of them: 8192 x 8192 M = 128 38.6 / 36.2, 34816 x 5120 M = 64 54 / 48
-// (all four with a launch for the activations' layout, 2 to 3 us, in front).
+// and short, else 256.  Measured (us, the whole layer, W4A16 and W4A4, 128 / 256
+// columns): 4096 x 1024 M = 256 13.5 / 17.2, 19.2 / 22.5; 8192 x 512 M = 256 12.0 /
+// 13.8, 17.7 / 19.8; longer or more of them: 8192 x 8192 M = 128 36.3 / 34.5, 38.6 /
+// 38.3; 34816 x 5120 M = 64 53.8 / 46.5, 53.1 / 49.3.
 TileSplit tile_split(int64_t M, int64_t N, int64_t K) {
   const int64_t tiles = (M + 15) / 16, blocks = (tiles + 3) / 4;
   const bool low = (tiles + blocks - 1) / blocks <= 3;
@@ -752,8 +752,8 @@ __global__ __launch_bounds__(KW * kWave) void linear_few_kernel(FewParams p) {
 }
 
 // Activations of a few rows as codes: the global scale is taken by every
-// workgroup from all of x (at most 16 rows: 2^18 elements at K = 16384), so
-// that quantising is one launch.
+// workgroup from all of x (at most 16 rows and kFewQuantMax elements), so that
+// quantising is one launch.
 __global__ __launch_bounds__(256) void linear_few_quant_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                                float* __restrict__ g, uint8_t* __restrict__ q,
                                                                uint8_t* __restrict__ sf) {
@@ -798,15 +798,15 @@ hipError_t launch_operand(const uint16_t* x, int64_t M, int64_t K, bool quant, u
 // are few and the contraction is not long; the grouped kernels' 128 x 256 tiles
 // (launch_linear) once they fill the device; linear_tile_kernel between.
 // Measured (us, the whole layer, W4A16 and W4A4), few / tile:
-//   12288 x 2048 M = 32 12.6 / 13.9, 17.3 / 19.2; M = 33 15.8 / 14.0, 20.6 / 19.5
-//   16384 x 8192 M = 17 32.5 / 28.2, 36.6 / 32.3
-//   5120 x 17408 M = 17 30.3 / 28.8, 34.5 / 35.3; M = 64 43.3 / 35.6, 47.8 / 42.1
-//   8192 x 8192  M = 64 26.7 / 25.1, 31.3 / 31.5; M = 100 41.9 / 31.3, 46.5 / 35.8
-//   4096 x 1024  M = 128 10.4 / 12.3, 14.9 / 17.6; M = 203 16.0 / 12.6, 20.6 / 18.4
+//   12288 x 2048 M = 32 13.2 / 14.6, 17.5 / 19.7; M = 33 16.3 / 14.5, 20.9 / 20.0
+//   16384 x 8192 M = 17 33.2 / 29.6, 37.2 / 33.0
+//   5120 x 17408 M = 17 30.8 / 30.4, 34.8 / 36.0; M = 64 43.5 / 35.7, 48.1 / 41.7
+//   8192 x 8192  M = 64 27.3 / 25.6, 31.6 / 31.7; M = 100 42.6 / 31.0, 46.4 / 35.8
+//   4096 x 1024  M = 128 10.3 / 12.4, 14.7 / 17.7; M = 203 15.8 / 12.5, 20.1 / 18.1
 // and tile / grouped:
-//   34816 x 5120 M = 256 111 / 119, 101 / 119; M = 300 155 / 137, 121 / 122; M = 1024 395 / 313, 335 / 294
-//   5120 x 17408 M = 1024 208 / 245, 185 / 235; M = 2048 388 / 393, 355 / 389
-//   8192 x 8192  M = 512 80 / 129, 73 / 87; M = 1300 205 / 204, 187 / 195; M = 2048 302 / 227, 269 / 230
+//   34816 x 5120 M = 256 131 / 132, 109 / 121; M = 300 147 / 137, 126 / 128; M = 1024 407 / 336, 342 / 316
+//   5120 x 17408 M = 1024 202 / 248, 187 / 239; M = 2048 399 / 404, 367 / 397
+//   8192 x 8192  M = 512 81 / 132, 76 / 90; M = 1300 213 / 210, 190 / 199; M = 2048 310 / 247, 274 / 239
 static bool uses_few(int64_t M, int64_t N, int64_t K) {
   return M <= 16 || (K <= 8192 && (M + 63) / 64 * (N / 32) <= (M <= 32 ? 384 : kCUs));
 }
