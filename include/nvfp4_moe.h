@@ -315,9 +315,10 @@ int moe_quantize_and_align(const nvfp4_moe_dims* dims, const uint16_t* x, float*
  * with this N, K and w4a4, with and without the epilogue below.  One call
  * demands nvfp4_linear_call_workspace_size(M, N, K, w4a4, fused) bytes (fused:
  * the calls with an epilogue), as a rule far fewer.  The counter words lie in
- * the first 512 bytes of W4A4's workspace, and W4A16 has none and leaves them
- * alone: nothing else needs the zeros, and one workspace serves both in turn.  Errors: NVFP4_ESHAPE, NVFP4_EINVAL,
- * NVFP4_EWORKSPACE (message names M, N, K and the sizes). */
+ * the first 512 bytes of W4A4's workspace; W4A16 has none and leaves them
+ * alone.  Nothing else needs the zeros, and one workspace serves both in turn.
+ * Errors: NVFP4_ESHAPE, NVFP4_EINVAL, NVFP4_EWORKSPACE (message names M, N, K
+ * and the sizes). */
 size_t nvfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4);
 size_t nvfp4_linear_call_workspace_size(int64_t M, int64_t N, int64_t K, int w4a4, int fused);
 int nvfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep,
@@ -336,9 +337,10 @@ int nvfp4_linear_w4a16(const uint16_t* x, int64_t M, int64_t N, int64_t K, const
  *   plain:  y[m][n] = act(v[m][n])                            N columns
  *   gated:  y[m][i] = act(v[m][i]) * v[m][N/2 + i]            N/2 columns
  *   out[m][n] = y[m][n] + residual[m][n], rounded once to out_dtype
- * All of it is FP32.  Activations: NVFP4_ACT_RELU max(v, 0) (NaN stays NaN, as
- * through every other), NVFP4_ACT_SILU v / (1 + e^-v), NVFP4_ACT_GELU v Phi(v) (the normal distribution function),
- * NVFP4_ACT_GELU_TANH v / (1 + e^-2u) with u = sqrt(2/pi) (v + 0.044715 v^3).
+ * All of it is FP32.  Activations: NVFP4_ACT_RELU max(v, 0),
+ * NVFP4_ACT_SILU v / (1 + e^-v), NVFP4_ACT_GELU v Phi(v) (the normal
+ * distribution function), NVFP4_ACT_GELU_TANH v / (1 + e^-2u) with u =
+ * sqrt(2/pi) (v + 0.044715 v^3).  NaN goes through each of them.
  *
  * Plain weights are prepared as for the calls without an epilogue.  Gated
  * weights W [N][K], rows [0, N/2) gate and [N/2, N) up, are prepared as one

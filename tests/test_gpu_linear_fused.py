@@ -720,3 +720,31 @@ def test_quantised_nan_is_the_plain_layers(dev, fmt, M, N, K):
     assert torch.isfinite(got).all()
     assert torch.equal(got, _call(fmt, clean, wt[0], bias=torch.zeros(N, device=dev), out_dtype=torch.float32))
     assert torch.equal(want, _call(fmt, clean, wt[0], out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [1, 16, 64, 300])
+def test_default_workspace_captured(dev, fmt, M):
+    """Calls without a workspace or an output, captured once: every replay on
+    new inputs equals the eager calls, with eager work in between."""
+    N, K = 1024, 5120                      # (W4A4 clears a small workspace whole, a larger one where it counts)
+    plain, gated = _weight(fmt, N, K, False)[0], _weight(fmt, N, K, True)[0]
+    x = _x(dev, M, K, 1)
+
+    def step():
+        return _call(fmt, x, plain), _call(fmt, x, gated, act="silu")
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for i in range(4):
+        x.copy_(_x(dev, M, K, 20 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        got_now = [t.clone() for t in got]
+        want = step()
+        torch.cuda.synchronize()
+        for a, b in zip(got_now, want):
+            assert torch.equal(a, b), i
