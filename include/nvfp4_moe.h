@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define NVFP4_MOE_ABI_VERSION 11
+#define NVFP4_MOE_ABI_VERSION 12
 
 /* Status codes. */
 #define NVFP4_OK 0
@@ -84,6 +84,7 @@ extern "C" {
 /* Element types of dense inputs/outputs. */
 #define NVFP4_BF16 0
 #define NVFP4_F32 1
+#define NVFP4_I8 2   /* int8 codes with a float32 scale per row (int8_linear) */
 
 /* Layer dimensions (host struct).
  *   T      tokens (>= 0)
@@ -411,6 +412,112 @@ int mxfp4_prep_weights(int64_t N, int64_t K, const uint8_t* q, const uint8_t* ex
 size_t mxfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K);
 int mxfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* w_prep, void* out,
                  int out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Root-mean-square norm, with the residual's addition and 8-bit rows.       */
+/* ------------------------------------------------------------------------ */
+/* The norm in front of a layer, for rows x [rows][H]:
+ *   h    = x + residual, rounded to the residual's type (h = x without one)
+ *   rstd = 1 / sqrt(mean h^2 + eps)
+ *   y    = h rstd weight
+ * written as y (bfloat16 or float32), or in 8 bits with a scale per row
+ *   v = h weight,  q = 127 v / max|v| to the nearest whole number (ties to the
+ *   even one), s = rstd max|v| / 127:  y = q s to half a step,
+ * or both (a NULL output is not made; one of y and q is).  h is written where
+ * it is given (only with a residual): the residual stream of the next layer.  It
+ * may be the residual or x itself (same type and stride), and y may be x itself;
+ * outputs must not overlap inputs or each other otherwise.
+ * The sum of squares, the norm's factor and the scale are FP64, decisions of
+ * codes exact (v is exact in FP64).  A row of zeros has codes and scale 0.  A
+ * row with NaN or infinity in h or v has scale NaN (its codes mean nothing), so
+ * that what is computed from it is NaN too.
+ * Types bfloat16 or float32, each its own.  H a multiple of 8, at most 32768;
+ * strides at least H, multiples of 8; x, residual, weight, h, y 16-byte, q
+ * (contiguous [rows][H]) 8-byte aligned.  rows < 2^31. */
+typedef struct rms_norm_args {   /* host struct */
+  const void* x;
+  int64_t ldx;
+  const void* residual;
+  int64_t ld_residual;
+  const void* weight;
+  void* h;
+  int64_t ld_h;
+  void* y;
+  int64_t ld_y;
+  int8_t* q;
+  float* s;
+  int32_t x_dtype;
+  int32_t residual_dtype;   /* and h's */
+  int32_t w_dtype;
+  int32_t y_dtype;
+  float eps;                /* >= 0 */
+} rms_norm_args;
+int rms_norm(const rms_norm_args* args, int64_t rows, int64_t H, void* stream);
+
+/* The same codes of the rows of x as they are: q = 127 x / max|x| to the nearest
+ * whole number (ties to the even one), s = max|x| / 127 (correctly rounded).
+ * x [rows][ldx] bfloat16 or float32; the rest as above with K for H. */
+int int8_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ldx, int8_t* q, float* s, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Dense int8 linear layer (W8A8).                                           */
+/* ------------------------------------------------------------------------ */
+/* y [M][N] = sx[m] sw[n] sum_k xq[m][k] wq[n][k], then the epilogue of
+ * nvfp4_linear_fused (bias, activation plain or gated, residual, one rounding):
+ * for the projections beside the experts that do not bear 4 bits.  The sums are
+ * int32 and exact; the rest is FP32.  Results repeat bit for bit.
+ *   weights: wq int8 [N][K] with float32 scales sw [N] (int8_quantize of W's rows;
+ *     any codes, -128 too), rearranged once by int8_prep_weights (gated 1: rows
+ *     [0, N/2) gate, [N/2, N) up) into prep (int8_prep_weights_size bytes, 16-byte
+ *     aligned); sw stays in W's row order.
+ *   x: int8 codes [M][ldx] with scales sx [M] (x_dtype NVFP4_I8; rms_norm's or
+ *     int8_quantize's; ldx a multiple of 16), or bfloat16 [M][ldx] (NVFP4_BF16;
+ *     sx unused, ldx a multiple of 8), quantised as by int8_quantize into the
+ *     workspace: the same results.  16-byte aligned.
+ *   epi: as for nvfp4_linear_fused (its gated is the weight's), or NULL: the
+ *     product alone into contiguous out.
+ * N a multiple of 4 (gated: of 8), at most 2^20; K a multiple of 16 below 131072
+ * (so that no sum passes 31 bits), bfloat16 x at most 32768; M <= 2^24,
+ * M N <= 2^40.  A row or column whose scale is NaN gives NaN.
+ * ws: int8_linear_workspace_size(M, N, K, x_dtype) bytes, 256-byte aligned, no
+ * initial contents; it serves every call of fewer rows, and bfloat16's serves
+ * int8 codes too. */
+size_t int8_prep_weights_size(int64_t N, int64_t K, int gated);
+int int8_prep_weights(int64_t N, int64_t K, int gated, const int8_t* q, uint8_t* prep, void* stream);
+size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int x_dtype);
+int int8_linear(const void* x, int x_dtype, int64_t ldx, const float* sx, int64_t M, int64_t N, int64_t K,
+                const uint8_t* w_prep, const float* sw, const nvfp4_epilogue* epi, void* out, int out_dtype, void* ws,
+                size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rows by expert and back, with gradients.                                  */
+/* ------------------------------------------------------------------------ */
+/* The movement that the grouped GEMMs do inside, for experts computed
+ * elsewhere (other ranks, other precisions, training), by moe_align's
+ * expert_offsets and inv_pos for the same T, topk, E and shared (dims' H and I
+ * play no part: rows have `width` elements of their own).  f runs over the pairs
+ * of moe_align, t is the token of f, w_f = topk_w[t][j], 1 for the shared expert
+ * and everywhere if topk_w is NULL; pairs without a row (inv_pos -1) are left out:
+ *   moe_permute             rows[inv_pos[f]] = x[t]
+ *   moe_unpermute           out[t] = sum_f w_f rows[inv_pos[f]]   (FP32, in the
+ *                           order of j, the shared row last, one rounding)
+ *   moe_unpermute_backward  d_rows[inv_pos[f]] = w_f d_out[t],
+ *                           d_w[t][j] = sum_i d_out[t][i] rows[inv_pos[f]][i]
+ *                           (0 without a row; float32; either may be NULL)
+ * The gradient of moe_permute is moe_unpermute of the rows' gradients with
+ * topk_w NULL.  x [T][ldx], rows and d_rows [P][width], out and d_out [T][width],
+ * bfloat16 or float32 (rows, d_rows in dtype; out, d_out in out_dtype), 16-byte
+ * aligned; width a multiple of 8, at most 2^20, ldx >= width a multiple of 8,
+ * T width <= 2^40.  Rows behind the last kept one (expert_offsets[E + shared]) are
+ * cleared with zero_tail and left as they were without.  No output may overlap an input. */
+int moe_permute(const nvfp4_moe_dims* dims, const void* x, int dtype, int64_t width, int64_t ldx,
+                const int32_t* expert_offsets, const int32_t* inv_pos, void* rows, int zero_tail, void* stream);
+int moe_unpermute(const nvfp4_moe_dims* dims, const void* rows, int dtype, int64_t width,
+                  const int32_t* expert_offsets, const int32_t* inv_pos, const float* topk_w, void* out, int out_dtype,
+                  void* stream);
+int moe_unpermute_backward(const nvfp4_moe_dims* dims, const void* d_out, int out_dtype, const void* rows, int dtype,
+                           int64_t width, const int32_t* expert_offsets, const int32_t* inv_pos, const float* topk_w,
+                           void* d_rows, float* d_w, int zero_tail, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Weight preparation (offline).                                             */

@@ -13,7 +13,7 @@ from ctypes import c_char_p, c_int, c_int32, c_int64, c_size_t, c_void_p
 # variant with different tile settings); the default is the in-tree build.
 LIB_PATH = os.environ.get("NVFP4_MOE_LIB") or os.path.join(
     os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
-ABI_VERSION = 11
+ABI_VERSION = 12
 
 NVFP4_OK = 0
 NVFP4_EINVAL = -1
@@ -22,6 +22,7 @@ NVFP4_EWORKSPACE = -3
 NVFP4_ELAUNCH = -4
 NVFP4_BF16 = 0
 NVFP4_F32 = 1
+NVFP4_I8 = 2
 
 
 class Dims(ctypes.Structure):
@@ -40,6 +41,13 @@ class RouteParams(ctypes.Structure):
 class Epilogue(ctypes.Structure):
     _fields_ = [("act", c_int32), ("gated", c_int32), ("bias", c_void_p), ("residual", c_void_p),
                 ("residual_dtype", c_int32), ("ld_residual", c_int64), ("ld_out", c_int64)]
+
+
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("ldx", c_int64), ("residual", c_void_p), ("ld_residual", c_int64),
+                ("weight", c_void_p), ("h", c_void_p), ("ld_h", c_int64), ("y", c_void_p), ("ld_y", c_int64),
+                ("q", c_void_p), ("s", c_void_p), ("x_dtype", c_int32), ("residual_dtype", c_int32),
+                ("w_dtype", c_int32), ("y_dtype", c_int32), ("eps", ctypes.c_float)]
 
 
 _P = ctypes.POINTER(Dims)
@@ -117,6 +125,17 @@ SIGNATURES = {
                                               c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                               c_void_p, c_int, c_void_p]),
     "grouped_gemm_runs_in_parts": (c_int, [_P]),
+    "rms_norm": (c_int, [ctypes.POINTER(RmsNormArgs), c_int64, c_int64, c_void_p]),
+    "int8_quantize": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
+    "int8_prep_weights_size": (c_size_t, [c_int64, c_int64, c_int]),
+    "int8_prep_weights": (c_int, [c_int64, c_int64, c_int, c_void_p, c_void_p, c_void_p]),
+    "int8_linear_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int]),
+    "int8_linear": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, _E,
+                            c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "moe_permute": (c_int, [_P, c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_void_p]),
+    "moe_unpermute": (c_int, [_P, c_void_p, c_int, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p]),
+    "moe_unpermute_backward": (c_int, [_P, c_void_p, c_int, c_void_p, c_int, c_int64, c_void_p, c_void_p, c_void_p,
+                                       c_void_p, c_void_p, c_int, c_void_p]),
 }
 # The *_part calls: the named call's arguments with int part before the stream.
 for _name in ("grouped_gemm1_swiglu", "grouped_gemm2_combine", "grouped_gemm1_swiglu_w4a16",

@@ -14,7 +14,9 @@
 
 #include "../../include/nvfp4_moe.h"
 #include "launch.h"
+#include "int8.h"
 #include "mx.h"
+#include "permute.h"
 
 namespace {
 
@@ -360,7 +362,7 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K, bool w4a4) {
 // Checks the epilogue of a fused layer (sizes and enums always, pointers where
 // there are rows) and fills the kernels' form of it.
 int check_epilogue(const char* W, const nvfp4_epilogue* e, int64_t M, int64_t N, int64_t K, void* out, int out_dtype,
-                   nvfp4::LinearEpi* k) {
+                   nvfp4::LinearEpi* k, int gated_n = 256) {
   if (!e) return fail(NVFP4_EINVAL, "%s: EINVAL epi is NULL", W);
   if (e->act < NVFP4_ACT_NONE || e->act > NVFP4_ACT_GELU_TANH || (e->gated != 0 && e->gated != 1))
     return fail(NVFP4_EINVAL, "%s: EINVAL act=%d gated=%d", W, e->act, e->gated);
@@ -368,9 +370,9 @@ int check_epilogue(const char* W, const nvfp4_epilogue* e, int64_t M, int64_t N,
     return fail(NVFP4_EINVAL, "%s: EINVAL out_dtype=%d", W, out_dtype);
   if (e->residual && e->residual_dtype != NVFP4_BF16 && e->residual_dtype != NVFP4_F32)
     return fail(NVFP4_EINVAL, "%s: EINVAL residual_dtype=%d", W, e->residual_dtype);
-  if (e->gated && N % 256)
-    return fail(NVFP4_ESHAPE, "%s: ESHAPE M=%lld N=%lld K=%lld (gated: N a multiple of 256)", W, (long long)M,
-                (long long)N, (long long)K);
+  if (e->gated && N % gated_n)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE M=%lld N=%lld K=%lld (gated: N a multiple of %d)", W, (long long)M,
+                (long long)N, (long long)K, gated_n);
   const int64_t n_out = e->gated ? N / 2 : N;
   if (e->ld_out < n_out || e->ld_out % 4 || (e->residual && (e->ld_residual < n_out || e->ld_residual % 4)))
     return fail(NVFP4_ESHAPE, "%s: ESHAPE N=%lld ld_out=%lld ld_residual=%lld (at least the output columns, multiples "
@@ -987,6 +989,243 @@ int grouped_gemm2_combine_mxfp4_part(const nvfp4_moe_dims* d, const uint8_t* a2_
   return grouped_gemm2_combine_mxfp4_impl("grouped_gemm2_combine_mxfp4_part", part, d, a2_q, a2_e,
                                           expert_offsets, inv_pos, plan, topk_w, w2_prep, out, out_dtype, ws,
                                           ws_bytes, stream);
+}
+
+// ------------------------------------------------------------------ norm and 8-bit rows
+int rms_norm(const rms_norm_args* a, int64_t rows, int64_t H, void* stream) {
+  const char* W = "rms_norm";
+  if (!a) return fail(NVFP4_EINVAL, "%s: EINVAL args is NULL", W);
+  auto type_ok = [](int t) { return t == NVFP4_BF16 || t == NVFP4_F32; };
+  if (!type_ok(a->x_dtype) || !type_ok(a->w_dtype) || (a->residual && !type_ok(a->residual_dtype)) ||
+      (a->y && !type_ok(a->y_dtype)))
+    return fail(NVFP4_EINVAL, "%s: EINVAL x_dtype=%d residual_dtype=%d w_dtype=%d y_dtype=%d", W, a->x_dtype,
+                a->residual_dtype, a->w_dtype, a->y_dtype);
+  if (!(a->eps >= 0.0f && a->eps < INFINITY)) return fail(NVFP4_EINVAL, "%s: EINVAL eps=%g", W, (double)a->eps);
+  if (rows < 0 || rows > INT32_MAX || H < 8 || H % 8 || H > nvfp4::kNormMaxH)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE rows=%lld H=%lld (rows < 2^31, H a multiple of 8, at most %d)", W, (long long)rows,
+                (long long)H, nvfp4::kNormMaxH);
+  auto stride_ok = [&](const void* p, int64_t ld) { return !p || (ld >= H && ld % 8 == 0); };
+  if (!stride_ok(a->x ? a->x : a, a->ldx) || !stride_ok(a->residual, a->ld_residual) || !stride_ok(a->h, a->ld_h) ||
+      !stride_ok(a->y, a->ld_y))
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE H=%lld ldx=%lld ld_residual=%lld ld_h=%lld ld_y=%lld (at least H, multiples of 8)",
+                W, (long long)H, (long long)a->ldx, (long long)a->ld_residual, (long long)a->ld_h, (long long)a->ld_y);
+  if (rows == 0) return ok();
+  if (!a->x || !a->weight || (!a->y && !a->q) || (a->q && !a->s) || (a->h && !a->residual))
+    return fail(NVFP4_EINVAL, "%s: EINVAL null pointer (x, weight, y or q; s with q; h only with a residual)", W);
+  if (!aligned(a->x, 16) || !aligned(a->residual, 16) || !aligned(a->weight, 16) || !aligned(a->h, 16) ||
+      !aligned(a->y, 16) || !aligned(a->q, 8) || !aligned(a->s, 4))
+    return fail(NVFP4_EINVAL, "%s: EINVAL misaligned pointer (x, residual, weight, h, y 16 B, q 8 B, s 4 B)", W);
+  if (a->h && (a->h == a->residual || a->h == a->x)) {
+    const bool r = a->h == a->residual;
+    if ((!r && a->x_dtype != a->residual_dtype) || (rows > 1 && a->ld_h != (r ? a->ld_residual : a->ldx)))
+      return fail(NVFP4_EINVAL, "%s: EINVAL h in place of x or the residual has its type and stride", W);
+  }
+  if (a->y && (a->y == a->h || a->y == a->residual))
+    return fail(NVFP4_EINVAL, "%s: EINVAL y is h or the residual", W);
+  if (a->y == a->x && a->y && (a->y_dtype != a->x_dtype || (rows > 1 && a->ld_y != a->ldx)))
+    return fail(NVFP4_EINVAL, "%s: EINVAL y in place of x has its type and stride", W);
+  nvfp4::NormArgs k{};
+  k.rows = rows;
+  k.H = (int)H;
+  k.eps = a->eps;
+  k.x = a->x;
+  k.x_f32 = a->x_dtype == NVFP4_F32;
+  k.ldx = a->ldx;
+  k.res = a->residual;
+  k.res_f32 = a->residual_dtype == NVFP4_F32;
+  k.ldr = a->ld_residual;
+  k.w = a->weight;
+  k.w_f32 = a->w_dtype == NVFP4_F32;
+  k.h = a->h;
+  k.ldh = a->ld_h;
+  k.y = a->y;
+  k.y_f32 = a->y_dtype == NVFP4_F32;
+  k.ldy = a->ld_y;
+  k.q = a->q;
+  k.s = a->s;
+  return launched(nvfp4::launch_rms_norm(k, S(stream)), W);
+}
+
+namespace {
+hipError_t quantize_rows(const void* x, int dtype, int64_t rows, int64_t K, int64_t ldx, int8_t* q, float* s,
+                         void* stream) {
+  nvfp4::NormArgs k{};
+  k.rows = rows;
+  k.H = (int)K;
+  k.x = x;
+  k.x_f32 = dtype == NVFP4_F32;
+  k.ldx = ldx;
+  k.q = q;
+  k.s = s;
+  return nvfp4::launch_int8_quantize(k, S(stream));
+}
+}  // namespace
+
+int int8_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ldx, int8_t* q, float* s, void* stream) {
+  const char* W = "int8_quantize";
+  if (dtype != NVFP4_BF16 && dtype != NVFP4_F32) return fail(NVFP4_EINVAL, "%s: EINVAL dtype=%d", W, dtype);
+  if (rows < 0 || rows > INT32_MAX || K < 8 || K % 8 || K > nvfp4::kNormMaxH || ldx < K || ldx % 8)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE rows=%lld K=%lld ldx=%lld (rows < 2^31, K and ldx multiples of 8, K at most %d)",
+                W, (long long)rows, (long long)K, (long long)ldx, nvfp4::kNormMaxH);
+  if (rows == 0) return ok();
+  if (!x || !q || !s) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
+  if (!aligned(x, 16) || !aligned(q, 8) || !aligned(s, 4))
+    return fail(NVFP4_EINVAL, "%s: EINVAL misaligned pointer (x 16 B, q 8 B, s 4 B)", W);
+  return launched(quantize_rows(x, dtype, rows, K, ldx, q, s, stream), W);
+}
+
+// ------------------------------------------------------------------ int8 layers
+namespace {
+// |sum| <= 128 * 128 K < 2^31; rows of codes in whole 16-byte units.
+bool int8_weight_ok(int64_t N, int64_t K, int gated) {
+  return (gated == 0 || gated == 1) && N >= 1 && N <= (int64_t(1) << 20) && N % (gated ? 8 : 4) == 0 && K >= 16 &&
+         K % 16 == 0 && K < 131072;
+}
+bool int8_shape_ok(int64_t M, int64_t N, int64_t K, int x_dtype, int gated) {
+  return int8_weight_ok(N, K, gated) && M >= 0 && M <= (int64_t(1) << 24) && M * N <= (int64_t(1) << 40) &&
+         (x_dtype == NVFP4_I8 || K <= nvfp4::kNormMaxH);
+}
+// Workspace: codes and scales of bfloat16 activations.
+size_t int8_ws_codes(int64_t M, int64_t K) { return up256((size_t)M * (size_t)K); }
+}  // namespace
+
+size_t int8_prep_weights_size(int64_t N, int64_t K, int gated) {
+  return int8_weight_ok(N, K, gated) ? nvfp4::int8_prep_bytes(N, K, gated) : 0;
+}
+
+int int8_prep_weights(int64_t N, int64_t K, int gated, const int8_t* q, uint8_t* prep, void* stream) {
+  const char* W = "int8_prep_weights";
+  if (!int8_weight_ok(N, K, gated))
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE N=%lld K=%lld gated=%d (N a multiple of 4, gated of 8, at most 2^20; K a multiple "
+                "of 16 below 131072)", W, (long long)N, (long long)K, gated);
+  if (!q || !prep) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
+  if (!aligned(q, 16) || !aligned(prep, 16))
+    return fail(NVFP4_EINVAL, "%s: EINVAL q and prep must be 16-byte aligned", W);
+  return launched(nvfp4::launch_int8_prep(N, K, gated, q, prep, S(stream)), W);
+}
+
+size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int x_dtype) {
+  if ((x_dtype != NVFP4_BF16 && x_dtype != NVFP4_I8) || !int8_shape_ok(M, N, K, x_dtype, 0)) return 0;
+  return x_dtype == NVFP4_BF16 ? int8_ws_codes(M, K) + up256((size_t)M * 4) : 0;
+}
+
+int int8_linear(const void* x, int x_dtype, int64_t ldx, const float* sx, int64_t M, int64_t N, int64_t K,
+                const uint8_t* w_prep, const float* sw, const nvfp4_epilogue* epi, void* out, int out_dtype, void* ws,
+                size_t ws_bytes, void* stream) {
+  const char* W = "int8_linear";
+  if (x_dtype != NVFP4_BF16 && x_dtype != NVFP4_I8) return fail(NVFP4_EINVAL, "%s: EINVAL x_dtype=%d", W, x_dtype);
+  const nvfp4_epilogue plain = {NVFP4_ACT_NONE, 0, nullptr, nullptr, 0, 0, N};
+  const nvfp4_epilogue* e = epi ? epi : &plain;
+  const int64_t unit = x_dtype == NVFP4_I8 ? 16 : 8;
+  if (!int8_shape_ok(M, N, K, x_dtype, e->gated) || ldx < K || ldx % unit)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE M=%lld N=%lld K=%lld ldx=%lld gated=%d (N a multiple of 4, gated of 8, at most "
+                "2^20; K a multiple of 16 below 131072, bfloat16 x: at most %d; M <= 2^24, M N <= 2^40; ldx >= K a multiple "
+                "of %d)", W, (long long)M, (long long)N, (long long)K, (long long)ldx, e->gated, nvfp4::kNormMaxH, (int)unit);
+  nvfp4::Int8Args a{};
+  if (int r = check_epilogue(W, e, M, N, K, out, out_dtype, &a.ep, 8)) return r;
+  const size_t need = int8_linear_workspace_size(M, N, K, x_dtype);
+  if (M > 0 && need > 0 && (ws_bytes < need || !ws))
+    return fail(NVFP4_EWORKSPACE, "%s: EWORKSPACE M=%lld N=%lld K=%lld workspace_size=%zu needed=%zu", W, (long long)M,
+                (long long)N, (long long)K, ws_bytes, need);
+  if (M == 0) return ok();
+  if (!x || !w_prep || !sw || (x_dtype == NVFP4_I8 && !sx)) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
+  if (!aligned(x, 16) || !aligned(w_prep, 16) || !aligned(ws, 256) || !aligned(sx, 4) || !aligned(sw, 4))
+    return fail(NVFP4_EINVAL, "%s: EINVAL x and w_prep 16-byte, ws 256-byte, scales 4-byte aligned", W);
+  if (out == x) return fail(NVFP4_EINVAL, "%s: EINVAL out is x", W);
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.a = static_cast<const int8_t*>(x);
+  a.lda = ldx;
+  a.sx = sx;
+  a.w = w_prep;
+  a.sw = sw;
+  if (x_dtype == NVFP4_BF16) {
+    int8_t* q = static_cast<int8_t*>(ws);
+    float* s = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + int8_ws_codes(M, K));
+    const hipError_t err = quantize_rows(x, NVFP4_BF16, M, K, ldx, q, s, stream);
+    if (err != hipSuccess) return launched(err, W);
+    a.a = q;
+    a.lda = K;
+    a.sx = s;
+  }
+  return launched(nvfp4::launch_int8_linear(a, S(stream)), W);
+}
+
+// ------------------------------------------------------------------ rows by expert
+namespace {
+// Dimensions of the permutation, and rows of W elements.
+int check_permute(const char* W, const nvfp4_moe_dims* d, int64_t width, nvfp4::PermuteArgs* k) {
+  if (!d) return fail(NVFP4_EINVAL, "%s: EINVAL dims is NULL", W);
+  nvfp4_moe_dims any = *d;   // H and I play no part: rows have a width of their own
+  any.H = any.I = 128;
+  if (int r = check_dims(&any, W)) return r;
+  if (width < 8 || width % 8 || width > (int64_t(1) << 20) || d->T * (width / 4) > (int64_t(1) << 38))
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE width=%lld (a multiple of 8, at most 2^20; T width <= 2^40)", W, (long long)width);
+  k->T = d->T;
+  k->topk = d->topk;
+  k->shared = d->shared;
+  k->slots = d->E + d->shared;
+  k->W = width;
+  return NVFP4_OK;
+}
+}  // namespace
+
+int moe_permute(const nvfp4_moe_dims* d, const void* x, int dtype, int64_t width, int64_t ldx,
+                const int32_t* expert_offsets, const int32_t* inv_pos, void* rows, int zero_tail, void* stream) {
+  const char* W = "moe_permute";
+  nvfp4::PermuteArgs k{};
+  if (int r = check_permute(W, d, width, &k)) return r;
+  if (dtype != NVFP4_BF16 && dtype != NVFP4_F32) return fail(NVFP4_EINVAL, "%s: EINVAL dtype=%d", W, dtype);
+  if (ldx < width || ldx % 8)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE width=%lld ldx=%lld (ldx at least the width, a multiple of 8)", W,
+                (long long)width, (long long)ldx);
+  if (d->T == 0) return ok();
+  if (!x || !expert_offsets || !inv_pos || !rows) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
+  if (!aligned(x, 16) || !aligned(rows, 16)) return fail(NVFP4_EINVAL, "%s: EINVAL x and rows 16-byte aligned", W);
+  if (x == rows) return fail(NVFP4_EINVAL, "%s: EINVAL rows is x", W);
+  k.offsets = expert_offsets;
+  k.inv_pos = inv_pos;
+  return launched(nvfp4::launch_permute(k, x, dtype == NVFP4_F32, ldx, rows, zero_tail != 0, S(stream)), W);
+}
+
+int moe_unpermute(const nvfp4_moe_dims* d, const void* rows, int dtype, int64_t width, const int32_t* expert_offsets,
+                  const int32_t* inv_pos, const float* topk_w, void* out, int out_dtype, void* stream) {
+  const char* W = "moe_unpermute";
+  nvfp4::PermuteArgs k{};
+  if (int r = check_permute(W, d, width, &k)) return r;
+  if ((dtype != NVFP4_BF16 && dtype != NVFP4_F32) || (out_dtype != NVFP4_BF16 && out_dtype != NVFP4_F32))
+    return fail(NVFP4_EINVAL, "%s: EINVAL dtype=%d out_dtype=%d", W, dtype, out_dtype);
+  if (d->T == 0) return ok();
+  if (!rows || !expert_offsets || !inv_pos || !out) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
+  if (!aligned(rows, 16) || !aligned(out, 16) || !aligned(topk_w, 4))
+    return fail(NVFP4_EINVAL, "%s: EINVAL rows and out 16-byte, topk_w 4-byte aligned", W);
+  if (out == rows) return fail(NVFP4_EINVAL, "%s: EINVAL out is rows", W);
+  k.offsets = expert_offsets;
+  k.inv_pos = inv_pos;
+  k.w = topk_w;
+  return launched(nvfp4::launch_unpermute(k, rows, dtype == NVFP4_F32, out, out_dtype == NVFP4_F32, S(stream)), W);
+}
+
+int moe_unpermute_backward(const nvfp4_moe_dims* d, const void* d_out, int out_dtype, const void* rows, int dtype,
+                           int64_t width, const int32_t* expert_offsets, const int32_t* inv_pos, const float* topk_w,
+                           void* d_rows, float* d_w, int zero_tail, void* stream) {
+  const char* W = "moe_unpermute_backward";
+  nvfp4::PermuteArgs k{};
+  if (int r = check_permute(W, d, width, &k)) return r;
+  if ((dtype != NVFP4_BF16 && dtype != NVFP4_F32) || (out_dtype != NVFP4_BF16 && out_dtype != NVFP4_F32))
+    return fail(NVFP4_EINVAL, "%s: EINVAL dtype=%d out_dtype=%d", W, dtype, out_dtype);
+  if (d->T == 0) return ok();
+  if (!d_out || !expert_offsets || !inv_pos || (!d_rows && !d_w) || (d_w && !rows))
+    return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
+  if (!aligned(d_out, 16) || !aligned(rows, 16) || !aligned(d_rows, 16) || !aligned(topk_w, 4) || !aligned(d_w, 4))
+    return fail(NVFP4_EINVAL, "%s: EINVAL d_out, rows and d_rows 16-byte, topk_w and d_w 4-byte aligned", W);
+  if (d_rows && (d_rows == rows || d_rows == d_out)) return fail(NVFP4_EINVAL, "%s: EINVAL d_rows is rows or d_out", W);
+  k.offsets = expert_offsets;
+  k.inv_pos = inv_pos;
+  k.w = topk_w;
+  return launched(nvfp4::launch_unpermute_backward(k, d_out, out_dtype == NVFP4_F32, rows, dtype == NVFP4_F32, d_rows,
+                                                   d_w, zero_tail != 0, S(stream)), W);
 }
 
 // ------------------------------------------------------------------ GEMM2 without allocation

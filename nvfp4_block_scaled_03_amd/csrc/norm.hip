@@ -1,0 +1,304 @@
+// Root-mean-square norm with the residual's addition and 8-bit codes
+// (rms_norm), and the codes of rows as they are (int8_quantize), for gfx950.
+//
+//   h = x + residual, rounded to the residual's type (h = x without one)
+//   rstd = 1 / sqrt(mean h^2 + eps),  y = h rstd w
+//   v = h w,  q = rne(127 v / max |v|),  s = rstd max |v| / 127
+//
+// The norm's factor leaves the codes alone (it scales a row and its maximum),
+// so they are decided on v: a quotient 127 v / max |v| halfway between two
+// codes, frequent where h and w are bfloat16, goes to the even one.  A
+// candidate k = floor(t) from an approximate quotient is settled by the sign
+// of 254 |v| - (2 k + 1) max |v|; near a whole number the candidate may be one
+// off, which the comparison sets right.  With bfloat16 h and w all of it is exact
+// in FP32 (v has 16 bits, 254 v 23, (2 k + 1) max |v| 24); with float32 ones v is
+// exact in FP64.  FP64 too where a row's magnitudes come near the ends of FP32.
+//
+// A row stays in registers between its two uses: one read, one write.  Bound:
+// bytes.
+#include "common.h"
+#include "int8.h"
+
+namespace nvfp4 {
+namespace {
+
+struct Raw8 {
+  u32x4 lo, hi;   // 8 elements as stored (bfloat16: lo alone)
+};
+template <bool F32>
+__device__ __forceinline__ Raw8 load8(const void* p, int64_t i) {
+  Raw8 r;
+  if constexpr (F32) {
+    const u32x4* at = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
+    r.lo = at[0];
+    r.hi = at[1];
+  } else {
+    r.lo = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void unpack8(const Raw8& r, float (&v)[8]) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = __int_as_float((int)r.lo[j]);
+      v[4 + j] = __int_as_float((int)r.hi[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_bits_to_f32(r.lo[j] & 0xFFFFu);
+      v[2 * j + 1] = __int_as_float((int)(r.lo[j] & 0xFFFF0000u));
+    }
+  }
+}
+// (the hardware conversion: nearest, ties to even, NaN stays NaN)
+__device__ __forceinline__ uint32_t bf16_of(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
+  if constexpr (F32) {
+    f32x4* at = reinterpret_cast<f32x4*>(static_cast<float*>(p) + i);
+    at[0] = f32x4{v[0], v[1], v[2], v[3]};
+    at[1] = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    u32x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = bf16_of(v[2 * j]) | (bf16_of(v[2 * j + 1]) << 16);
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = o;
+  }
+}
+
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v, int off) { return (uint32_t)__shfl_xor((int)v, off); }
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v, int off) {
+  return (uint64_t)lane_xor((uint32_t)(v >> 32), off) << 32 | lane_xor((uint32_t)v, off);
+}
+__device__ __forceinline__ double lane_xor(double v, int off) {
+  return __longlong_as_double((long long)lane_xor((uint64_t)__double_as_longlong(v), off));
+}
+
+// Reductions over the WAVES wavefronts of a row (every thread gets the result).
+template <int WAVES, class T, class Op>
+__device__ __forceinline__ T row_reduce(T v, T* red, const Op& op) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v = op(v, lane_xor(v, off));
+  if constexpr (WAVES > 1) {
+    const int wv = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[wv] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int k = 1; k < WAVES; ++k) v = op(v, red[k]);
+  }
+  return v;
+}
+
+// |code| of one value: k = floor(t), one more beyond k + 1/2 (at it: if k is odd).
+__device__ __forceinline__ int code_f32(float a, float top, float inv) {
+  const float k = floorf(a * inv);
+  const float d = __builtin_fmaf(-(2.0f * k + 1.0f), top, 254.0f * a);
+  const int c = (int)k;
+  return c + (d > 0.0f || (d == 0.0f && (c & 1)));
+}
+__device__ __forceinline__ int code_f64(double a, double top, double inv) {
+  const double k = floor(a * inv);
+  const double d = __builtin_fma(-(2.0 * k + 1.0), top, 254.0 * a);
+  const int c = (int)k;
+  return min(c + (d > 0.0 || (d == 0.0 && (c & 1))), 127);
+}
+
+__device__ __forceinline__ uint64_t magnitude_bits(double v) {
+  return (uint64_t)__double_as_longlong(v) & 0x7FFFFFFFFFFFFFFFull;
+}
+
+constexpr float kTiny = 8.673617379884035e-19f, kHuge = 1.2676506002282294e30f;   // 2^-60, 2^100
+
+// TPR threads a row (64: a wavefront, four rows a workgroup), VPT pieces of 8
+// elements a thread.  RES: 0 none, 1 bfloat16, 2 float32.  NORM false: the codes
+// of x itself.
+template <bool NORM, bool XF32, int RES, int TPR, int VPT>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(NormArgs p) {
+  constexpr int ROWS = TPR < 256 ? 256 / TPR : 1, WAVES = TPR / 64;
+  constexpr bool HF32 = RES == 2 || (RES == 0 && XF32);   // type of h
+  __shared__ double red_d[WAVES > 1 ? WAVES : 1];
+  __shared__ uint64_t red_l[WAVES > 1 ? WAVES : 1];
+  __shared__ uint32_t red_u[WAVES > 1 ? WAVES : 1];
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+  if (ROWS > 1 && row >= p.rows) return;   // (whole wavefronts)
+  const int V = p.H / 8;
+  constexpr bool KEEP_W = VPT <= 2;   // the weights stay in registers (else they are read twice, from the caches)
+  Raw8 xr[VPT], rr[VPT], wr[KEEP_W ? VPT : 1];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * TPR + t;
+    if (v < V) {
+      xr[i] = load8<XF32>(p.x, row * p.ldx + v * 8);
+      if constexpr (RES != 0) rr[i] = load8<RES == 2>(p.res, row * p.ldr + v * 8);
+      if constexpr (NORM && KEEP_W) wr[i] = p.w_f32 ? load8<true>(p.w, v * 8) : load8<false>(p.w, v * 8);
+    }
+  }
+  const bool wide = HF32 || (NORM && p.w_f32);   // v needs FP64
+  float h[VPT][8];
+  double ss = 0.0;
+  uint32_t top_bits = 0;
+  uint64_t top64 = 0;   // magnitudes as bits: NaN above infinity above the rest
+  auto weights = [&](int i, float (&w)[8]) {
+    if constexpr (NORM) {
+      Raw8 r;
+      if constexpr (KEEP_W) r = wr[i];
+      else r = p.w_f32 ? load8<true>(p.w, (i * TPR + t) * 8) : load8<false>(p.w, (i * TPR + t) * 8);
+      if (p.w_f32) unpack8<true>(r, w);
+      else unpack8<false>(r, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * TPR + t;
+    if (v < V) {
+      unpack8<XF32>(xr[i], h[i]);
+      if constexpr (RES != 0) {
+        float r[8];
+        unpack8<RES == 2>(rr[i], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          h[i][j] += r[j];
+          if constexpr (!HF32) h[i][j] = __int_as_float((int)(bf16_of(h[i][j]) << 16));
+        }
+        if (p.h) store8<HF32>(p.h, row * p.ldh + v * 8, h[i]);
+      }
+      if constexpr (NORM) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)h[i][j], (double)h[i][j], ss);
+      }
+      if (p.q) {
+        float w[8];
+        weights(i, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          top_bits = max(top_bits, (uint32_t)__float_as_int(h[i][j] * w[j]) & 0x7FFFFFFFu);
+        if (wide) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top64 = max(top64, magnitude_bits((double)h[i][j] * (double)w[j]));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
+    }
+  }
+  double rstd = 1.0;
+  if constexpr (NORM) {
+    ss = row_reduce<WAVES>(ss, red_d, [](double a, double b) { return a + b; });
+    rstd = 1.0 / sqrt(ss / p.H + (double)p.eps);
+  }
+  const float rs = (float)rstd;
+  bool far = NORM && !(rs >= kTiny && rs <= kHuge);   // (NaN too)
+  double top = 0.0;
+  if (p.q) {
+    auto larger = [](auto a, auto b) { return a > b ? a : b; };
+    top_bits = row_reduce<WAVES>(top_bits, red_u, larger);
+    const float tf = __int_as_float((int)top_bits);
+    far = far || !(tf >= kTiny && tf <= kHuge);
+    if (far && !wide) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        if (i * TPR + t < V) {
+          float w[8];
+          weights(i, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top64 = max(top64, magnitude_bits((double)h[i][j] * (double)w[j]));
+        }
+      }
+    }
+    if (far || wide) top = __longlong_as_double((long long)row_reduce<WAVES>(top64, red_l, larger));
+    else top = tf;
+    // (a row with NaN or infinity: scale NaN)
+    if (t == 0) p.s[row] = top < (double)INFINITY ? (float)(rstd * top / 127.0) : __builtin_nanf("");
+  }
+  const float top32 = (float)top, inv32 = 127.0f / top32;
+  const double inv64 = 127.0 / top;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * TPR + t;
+    if (v >= V) continue;
+    float w[8];
+    weights(i, w);
+    if (NORM && p.y) {
+      float y[8];
+      if (!far) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rs * w[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = (float)((double)h[i][j] * rstd * (double)w[j]);
+      }
+      if (p.y_f32) store8<true>(p.y, row * p.ldy + v * 8, y);
+      else store8<false>(p.y, row * p.ldy + v * 8, y);
+    }
+    if (p.q) {
+      int c[8];
+      if (!(far || wide)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float vj = h[i][j] * w[j];
+          const int k = code_f32(fabsf(vj), top32, inv32);
+          c[j] = vj < 0.0f ? -k : k;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const double vj = (double)h[i][j] * (double)w[j];
+          const int k = top > 0.0 ? code_f64(fabs(vj), top, inv64) : 0;
+          c[j] = vj < 0.0 ? -k : k;
+        }
+      }
+      u32x2 o;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        o[j] = (c[4 * j] & 0xFF) | (c[4 * j + 1] & 0xFF) << 8 | (c[4 * j + 2] & 0xFF) << 16 | (c[4 * j + 3] & 0xFF) << 24;
+      *reinterpret_cast<u32x2*>(p.q + row * p.H + v * 8) = o;
+    }
+  }
+}
+
+template <bool NORM, bool XF32, int RES, int TPR, int VPT>
+hipError_t launch_rows_t(const NormArgs& a, hipStream_t s) {
+  constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
+  const int64_t grid = (a.rows + ROWS - 1) / ROWS;
+  row_kernel<NORM, XF32, RES, TPR, VPT><<<(unsigned)grid, TPR < 256 ? 256 : TPR, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <bool NORM, bool XF32, int RES>
+hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
+  const int V = a.H / 8;
+  if (V <= 64) return launch_rows_t<NORM, XF32, RES, 64, 1>(a, s);
+  if (V <= 256) return launch_rows_t<NORM, XF32, RES, 256, 1>(a, s);
+  if (V <= 512) return launch_rows_t<NORM, XF32, RES, 256, 2>(a, s);
+  if (V <= 1024) return launch_rows_t<NORM, XF32, RES, 256, 4>(a, s);
+  if (V <= 2048) return launch_rows_t<NORM, XF32, RES, 1024, 2>(a, s);
+  return launch_rows_t<NORM, XF32, RES, 1024, 4>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+  const int res = !a.res ? 0 : a.res_f32 ? 2 : 1;
+  if (a.x_f32) {
+    if (res == 0) return launch_rows<true, true, 0>(a, s);
+    if (res == 1) return launch_rows<true, true, 1>(a, s);
+    return launch_rows<true, true, 2>(a, s);
+  }
+  if (res == 0) return launch_rows<true, false, 0>(a, s);
+  if (res == 1) return launch_rows<true, false, 1>(a, s);
+  return launch_rows<true, false, 2>(a, s);
+}
+
+hipError_t launch_int8_quantize(const NormArgs& a, hipStream_t s) {
+  return a.x_f32 ? launch_rows<false, true, 0>(a, s) : launch_rows<false, false, 0>(a, s);
+}
+
+}  // namespace nvfp4

@@ -8,12 +8,12 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import functools
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
 from . import _lib
-from ._lib import NVFP4_BF16, NVFP4_F32, Dims, Epilogue, RouteParams, call
+from ._lib import NVFP4_BF16, NVFP4_F32, NVFP4_I8, Dims, Epilogue, RmsNormArgs, RouteParams, call
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -193,6 +193,8 @@ def route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias: Opt
         weights = torch.empty(T, k, dtype=torch.float32, device=logits.device)
     elif weights.shape != (T, k) or weights.dtype != torch.float32 or not weights.is_contiguous():
         raise ValueError("weights must be contiguous float32 [T, k]")
+    else:
+        _written(weights)
     call("moe_route", params, logits.data_ptr(), _dtype_code(logits), ld, _ptr(bias), T, E, k, ids.data_ptr(),
          weights.data_ptr(), _raw_stream(dev))
     return ids, weights
@@ -205,6 +207,20 @@ class Alignment:
     inv_pos: torch.Tensor
     plan: torch.Tensor
     workspace: torch.Tensor
+
+
+def _written(*ts):
+    """Tells autograd that the library wrote into tensors of the caller, which a
+    graph may have saved."""
+    torch._C._increment_version(ts)
+
+
+def _alignment(d: Dims, al: Optional[Alignment], device) -> Alignment:
+    """``al`` to be written anew, or a fresh one."""
+    if al is None:
+        return alloc_alignment(d, device)
+    _written(al.offsets, al.inv_pos)
+    return al
 
 
 def alloc_alignment(d: Dims, device) -> Alignment:
@@ -222,7 +238,7 @@ def alloc_alignment(d: Dims, device) -> Alignment:
 
 def moe_align(d: Dims, topk_ids: torch.Tensor, al: Optional[Alignment] = None) -> Alignment:
     _need_cuda(topk_ids)
-    al = al or alloc_alignment(d, topk_ids.device)
+    al = _alignment(d, al, topk_ids.device)
     call("moe_align", ctypes.byref(d), _p(topk_ids.contiguous()), _p(al.offsets),
          _p(al.sorted_pair), _p(al.inv_pos), _p(al.plan), _p(al.workspace),
          al.workspace.numel(), _stream())
@@ -233,7 +249,7 @@ def route_and_align(d: Dims, logits: torch.Tensor, al: Optional[Alignment] = Non
     """Router (top-k + softmax over the selection) and moe_align in one call:
     (topk_ids int32 [T, topk], topk_w float32 [T, topk], Alignment)."""
     _need_cuda(logits)
-    al = al or alloc_alignment(d, logits.device)
+    al = _alignment(d, al, logits.device)
     ids = torch.empty(max(d.T, 1), d.topk, dtype=torch.int32, device=logits.device)
     wts = torch.empty(max(d.T, 1), d.topk, dtype=torch.float32, device=logits.device)
     call("moe_route_and_align", ctypes.byref(d), _p(logits.contiguous().float()), _p(ids), _p(wts),
@@ -248,7 +264,7 @@ def quantize_and_align(d: Dims, x: torch.Tensor, topk_ids: torch.Tensor, al: Opt
     one call: (g, codes, scales, Alignment); ``deq`` optionally receives the
     exact f16 values."""
     _need_cuda(x, topk_ids)
-    al = al or alloc_alignment(d, x.device)
+    al = _alignment(d, al, x.device)
     g = torch.empty(1, dtype=torch.float32, device=x.device)
     q = torch.empty(max(d.T, 1), d.H // 2, dtype=torch.uint8, device=x.device)
     sf = torch.empty(max(d.T, 1), d.H // 16, dtype=torch.uint8, device=x.device)
@@ -264,7 +280,7 @@ def mx_quantize_and_align(d: Dims, x: torch.Tensor, topk_ids: torch.Tensor, al: 
     """OCP MXFP4 quantisation and moe_align of bf16 ``x`` [T, H] in one call:
     (codes [T, H/2], E8M0 bytes [T, H/32], Alignment)."""
     _need_cuda(x, topk_ids)
-    al = al or alloc_alignment(d, x.device)
+    al = _alignment(d, al, x.device)
     q = torch.empty(max(d.T, 1), d.H // 2, dtype=torch.uint8, device=x.device)
     ex = torch.empty(max(d.T, 1), d.H // 32, dtype=torch.uint8, device=x.device)
     call("moe_mxfp4_quantize_and_align", ctypes.byref(d), _p(x.contiguous()), _p(q), _p(ex),
@@ -276,7 +292,7 @@ def mx_quantize_and_align(d: Dims, x: torch.Tensor, topk_ids: torch.Tensor, al: 
 def scale_and_align(d: Dims, x: torch.Tensor, topk_ids: torch.Tensor, al: Optional[Alignment] = None):
     """Activation global scale of bf16 ``x`` [T, H] and moe_align in one call: (g, Alignment)."""
     _need_cuda(x, topk_ids)
-    al = al or alloc_alignment(d, x.device)
+    al = _alignment(d, al, x.device)
     g = torch.empty(1, dtype=torch.float32, device=x.device)
     wsb = _lib.load().nvfp4_global_scale_workspace_size(1, d.T * d.H)
     gs_ws = torch.zeros(max(wsb, 16), dtype=torch.uint8, device=x.device)
@@ -582,6 +598,347 @@ def mx_linear(x: torch.Tensor, w: MxLinearWeight, out_dtype=torch.bfloat16, out:
     return out
 
 
+# ---------------------------------------------------------------- norm and int8 layers
+def _no_gradient(name: str, *tensors):
+    """Refuses a call that autograd would take for a differentiable one."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} has no gradient: call it under torch.no_grad()")
+
+
+def _rows8(t: torch.Tensor) -> bool:
+    """Whether the rows of t [rows, n] lie apart and can be read and written
+    eight elements at a time."""
+    return (t.stride(1) == 1 and t.data_ptr() % 16 == 0
+            and (t.shape[0] <= 1 or (t.stride(0) >= t.shape[1] and t.stride(0) % 8 == 0)))
+
+
+class NormOut(NamedTuple):
+    """What rms_norm makes; None for what was not asked for."""
+    y: Optional[torch.Tensor]   # the norm [T, H]
+    h: Optional[torch.Tensor]   # x + residual [T, H], the residual's type
+    q: Optional[torch.Tensor]   # int8 codes of the norm [T, H]
+    s: Optional[torch.Tensor]   # float32 scales [T]: y = q s to half a step
+
+
+NORM_OUTPUTS = {"y": (True, False), "int8": (False, True), "both": (True, True)}
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+             outputs: str = "y", out_dtype=torch.bfloat16, y: Optional[torch.Tensor] = None,
+             h: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+             s: Optional[torch.Tensor] = None) -> NormOut:
+    """Root-mean-square norm of the rows of x [T, H] (+ residual): h = x +
+    residual, y = h / sqrt(mean h^2 + eps) * weight.  ``outputs``: "y" (in
+    ``out_dtype``), "int8" (codes with a scale per row, as int8_linear takes
+    them) or "both".  x, residual and weight bf16 or float32; ``h``, ``y``, ``q``
+    and ``s`` take the results (``h`` may be ``residual`` or ``x``, ``y`` may be
+    ``x``).  No gradient."""
+    if outputs not in NORM_OUTPUTS:
+        raise ValueError(f"outputs must be one of {sorted(NORM_OUTPUTS)}")
+    dev = x.get_device()
+    if not _same_device(dev, weight, residual, y, h, q, s):
+        with torch.cuda.device(dev):
+            return rms_norm(x, weight, eps, residual, outputs, out_dtype, y, h, q, s)
+    _no_gradient("rms_norm", x, weight, residual)
+    if x.dim() != 2 or weight.shape != x.shape[1:]:
+        raise ValueError("x must be [T, H] and weight [H]")
+    T, H = x.shape
+    want_y, want_q = NORM_OUTPUTS[outputs]
+    a = RmsNormArgs(eps=eps, x_dtype=_dtype_code(x), w_dtype=_dtype_code(weight))
+    if residual is not None:
+        if residual.shape != (T, H):
+            raise ValueError(f"residual must be [{T}, {H}]")
+        if h is None:
+            h = torch.empty(T, H, dtype=residual.dtype, device=x.device)
+        elif h.shape != (T, H) or h.dtype != residual.dtype or not _rows8(h):
+            raise ValueError(f"h must be [{T}, {H}] in the residual's type, with rows of consecutive elements, 16-byte "
+                             "aligned, strides multiples of 8")
+        a.residual_dtype = _dtype_code(residual)
+        if not _rows8(residual):
+            residual = residual.clone(memory_format=torch.contiguous_format)
+        a.residual, a.ld_residual = residual.data_ptr(), _row_stride(residual)
+        a.h, a.ld_h = h.data_ptr(), _row_stride(h)
+    elif h is not None:
+        raise ValueError("h is made only with a residual")
+    if not _rows8(x):
+        x = x.clone(memory_format=torch.contiguous_format)
+    a.x, a.ldx = x.data_ptr(), _row_stride(x)
+    weight = weight.contiguous()
+    if weight.data_ptr() % 16:
+        weight = weight.clone()
+    a.weight = weight.data_ptr()
+    if want_y:
+        if y is None:
+            y = torch.empty(T, H, dtype=out_dtype, device=x.device)
+        elif y.shape != (T, H) or not _rows8(y):
+            raise ValueError(f"y must be [{T}, {H}] with rows of consecutive elements, 16-byte aligned, strides multiples "
+                             "of 8")
+        a.y, a.ld_y, a.y_dtype = y.data_ptr(), _row_stride(y), _dtype_code(y)
+    elif y is not None:
+        raise ValueError(f"y is not made with outputs={outputs!r}")
+    if want_q:
+        q, s = _int8_rows(T, H, x.device, q, s)
+        a.q, a.s = q.data_ptr(), s.data_ptr()
+    elif q is not None or s is not None:
+        raise ValueError(f"q and s are not made with outputs={outputs!r}")
+    call("rms_norm", a, T, H, _raw_stream(dev))
+    return NormOut(y, h, q, s)
+
+
+def _int8_rows(T: int, H: int, device, q, s):
+    if q is None:
+        q = torch.empty(T, H, dtype=torch.int8, device=device)
+    elif q.shape != (T, H) or q.dtype != torch.int8 or not q.is_contiguous():
+        raise ValueError(f"q must be contiguous int8 [{T}, {H}]")
+    if s is None:
+        s = torch.empty(T, dtype=torch.float32, device=device)
+    elif s.shape != (T,) or s.dtype != torch.float32 or not s.is_contiguous():
+        raise ValueError(f"s must be contiguous float32 [{T}]")
+    return q, s
+
+
+def int8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None):
+    """Codes and scales of the rows of x [rows, K] (bf16 or float32): (q int8
+    [rows, K], s float32 [rows]), q = 127 x / max|x| to the nearest, ties to even."""
+    dev = x.get_device()
+    if not _same_device(dev, q, s):
+        with torch.cuda.device(dev):
+            return int8_quantize(x, q, s)
+    _no_gradient("int8_quantize", x)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, K]")
+    rows, K = x.shape
+    if not _rows8(x):
+        x = x.clone(memory_format=torch.contiguous_format)
+    q, s = _int8_rows(rows, K, x.device, q, s)
+    call("int8_quantize", x.data_ptr(), _dtype_code(x), rows, K, _row_stride(x), q.data_ptr(), s.data_ptr(),
+         _raw_stream(dev))
+    return q, s
+
+
+class Int8LinearWeight:
+    """An int8 weight W [N, K] with a scale per row, prepared for int8_linear;
+    ``gated`` as for LinearWeight."""
+
+    def __init__(self, prep: torch.Tensor, s: torch.Tensor, N: int, K: int, gated: bool = False):
+        self.prep, self.s, self.N, self.K, self.gated = prep, s, N, K, gated
+
+
+def prepare_int8_weight(q: torch.Tensor, s: torch.Tensor, gated: bool = False) -> Int8LinearWeight:
+    """From codes int8 [N, K] and scales float32 [N]."""
+    dev = q.get_device()
+    if not _same_device(dev, s):
+        with torch.cuda.device(dev):
+            return prepare_int8_weight(q, s, gated)
+    if q.dim() != 2 or q.dtype != torch.int8 or s.shape != q.shape[:1] or s.dtype != torch.float32:
+        raise ValueError("q must be int8 [N, K] and s float32 [N]")
+    N, K = q.shape
+    q = q.contiguous()
+    if q.data_ptr() % 16:
+        q = q.clone()
+    n = _lib.load().int8_prep_weights_size(N, K, int(gated))
+    prep = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+    call("int8_prep_weights", N, K, int(gated), q.data_ptr(), prep.data_ptr(), _raw_stream(dev))
+    return Int8LinearWeight(prep, s.contiguous(), N, K, gated)
+
+
+def quantize_int8_weight(w: torch.Tensor, gated: bool = False) -> Int8LinearWeight:
+    """FP32 or bf16 W [N, K] -> codes with a scale per row on the GPU, prep."""
+    q, s = int8_quantize(w.detach())
+    return prepare_int8_weight(q, s, gated)
+
+
+def int8_linear_workspace(M: int, N: int, K: int, device) -> torch.Tensor:
+    """Workspace of every ``int8_linear`` of up to M rows with a weight [N, K]."""
+    n = _lib.load().int8_linear_workspace_size(M, N, K, NVFP4_BF16)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def int8_linear(x: torch.Tensor, w: Int8LinearWeight, s: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                bias: Optional[torch.Tensor] = None, act: str = "none",
+                residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [M, N] = x W^T in 8 bits: x int8 codes [M, K] with scales ``s`` float32
+    [M] (rms_norm's or int8_quantize's), or bf16, quantised in the call;
+    ``bias``, ``act``, ``residual`` and gated weights as for ``linear``."""
+    dev = x.get_device()
+    if not _same_device(dev, w.prep, w.s, s, bias, residual, out, ws):
+        with torch.cuda.device(dev):
+            return int8_linear(x, w, s, out_dtype, out, ws, bias, act, residual)
+    _no_gradient("int8_linear", x, bias, residual)
+    N, K = w.N, w.K
+    if x.dim() != 2 or x.shape[1] != K or x.dtype not in (torch.bfloat16, torch.int8):
+        raise ValueError(f"x must be int8 or bfloat16 [M, {K}]")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    M, n_out = x.shape[0], N // 2 if w.gated else N
+    codes = x.dtype == torch.int8
+    if codes:
+        if s is None or s.shape != (M,) or s.dtype != torch.float32:
+            raise ValueError(f"int8 x comes with its scales s, float32 [{M}]")
+        s = s.contiguous()
+    elif s is not None:
+        raise ValueError("scales belong to int8 x")
+    unit = 16 if codes else 8
+    if x.stride(1) != 1 or x.data_ptr() % 16 or (M > 1 and (x.stride(0) < K or x.stride(0) % unit)):
+        x = x.clone(memory_format=torch.contiguous_format)
+    if out is None:
+        out = torch.empty(M, n_out, dtype=out_dtype, device=x.device)
+    elif out.shape != (M, n_out) or not _rows4(out):
+        raise ValueError(f"out must be [{M}, {n_out}] with rows of consecutive elements, starts and strides "
+                         "multiples of 4")
+    epi = Epilogue(ACTIVATIONS[act], int(w.gated), ld_out=_row_stride(out))
+    if bias is not None:
+        if bias.shape != (N,) or bias.dtype != torch.float32:
+            raise ValueError(f"bias must be float32 [{N}]")
+        bias = bias.contiguous()
+        epi.bias = bias.data_ptr()
+    if residual is not None:
+        if residual.shape != (M, n_out):
+            raise ValueError(f"residual must be [{M}, {n_out}]")
+        if not _rows4(residual):
+            residual = residual.clone(memory_format=torch.contiguous_format)
+        epi.residual, epi.residual_dtype = residual.data_ptr(), _dtype_code(residual)
+        epi.ld_residual = _row_stride(residual)
+    x_dtype = NVFP4_I8 if codes else NVFP4_BF16
+    if ws is None:
+        n = _lib.load().int8_linear_workspace_size(M, N, K, x_dtype)
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+    call("int8_linear", x.data_ptr(), x_dtype, _row_stride(x), _ptr(s), M, N, K, w.prep.data_ptr(), w.s.data_ptr(), epi,
+         out.data_ptr(), _dtype_code(out), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+         _raw_stream(dev))
+    return out
+
+
+# ---------------------------------------------------------------- rows by expert
+def _pairs(d: Dims) -> int:
+    return d.T * (d.topk + d.shared)
+
+
+def _permute(d: Dims, x, offsets, inv_pos, out):
+    T, W = x.shape
+    fresh = out is None
+    if fresh:
+        out = torch.empty(_pairs(d), W, dtype=x.dtype, device=x.device)
+    if not _rows8(x):
+        x = x.clone(memory_format=torch.contiguous_format)
+    call("moe_permute", d, x.data_ptr(), _dtype_code(x), W, _row_stride(x), offsets.data_ptr(), inv_pos.data_ptr(),
+         out.data_ptr(), int(fresh), _raw_stream(x.get_device()))
+    return out
+
+
+def _unpermute(d: Dims, rows, offsets, inv_pos, topk_w, out, out_dtype):
+    W = rows.shape[1]
+    if out is None:
+        out = torch.empty(d.T, W, dtype=out_dtype or rows.dtype, device=rows.device)
+    call("moe_unpermute", d, rows.data_ptr(), _dtype_code(rows), W, offsets.data_ptr(), inv_pos.data_ptr(),
+         _ptr(topk_w), out.data_ptr(), _dtype_code(out), _raw_stream(rows.get_device()))
+    return out
+
+
+def _whole(t: torch.Tensor) -> torch.Tensor:
+    """t contiguous and 16-byte aligned."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+class _Permute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, d, offsets, inv_pos):
+        ctx.d = Dims.from_buffer_copy(d)
+        ctx.save_for_backward(offsets, inv_pos)
+        return _permute(d, x, offsets, inv_pos, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_rows):
+        return _unpermute(ctx.d, _whole(d_rows), *ctx.saved_tensors, None, None, None), None, None, None
+
+
+class _Unpermute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, topk_w, d, offsets, inv_pos, out_dtype):
+        ctx.d = Dims.from_buffer_copy(d)
+        # (the rows enter only the weights' gradient)
+        keep = rows if topk_w is not None and ctx.needs_input_grad[1] else None
+        ctx.dtype = rows.dtype
+        ctx.save_for_backward(keep, topk_w, offsets, inv_pos)
+        return _unpermute(d, rows, offsets, inv_pos, topk_w, None, out_dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_out):
+        rows, topk_w, offsets, inv_pos = ctx.saved_tensors
+        d, d_out = ctx.d, _whole(d_out)
+        W, dev = d_out.shape[1], d_out.device
+        d_rows = torch.empty(_pairs(d), W, dtype=ctx.dtype, device=dev) if ctx.needs_input_grad[0] else None
+        d_w = torch.empty(d.T, d.topk, dtype=torch.float32, device=dev) if rows is not None else None
+        call("moe_unpermute_backward", d, d_out.data_ptr(), _dtype_code(d_out), _ptr(rows),
+             NVFP4_BF16 if ctx.dtype == torch.bfloat16 else NVFP4_F32, W, offsets.data_ptr(), inv_pos.data_ptr(),
+             _ptr(topk_w), _ptr(d_rows), _ptr(d_w), 1, _raw_stream(d_out.get_device()))
+        return d_rows, d_w, None, None, None, None
+
+
+def _check_alignment(d: Dims, al: Alignment):
+    # (an empty batch keeps one word of inv_pos)
+    if al.inv_pos.numel() != max(_pairs(d), 1) or al.offsets.numel() != d.E + d.shared + 1:
+        raise ValueError(f"the alignment is not one of {d}")
+
+
+def moe_permute(d: Dims, x: torch.Tensor, al: Alignment, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows of x [T, width] (bf16 or float32) in the order of their experts: row
+    p is that of the token of ``al.sorted_pair[p]``.  ``al``: moe_align's for the
+    T, topk, E and shared of ``d`` (whose H plays no part).  Rows behind the last
+    kept pair are zeros, in ``out`` [P, width] left as they were.  Differentiable
+    in x (without ``out``)."""
+    dev = x.get_device()
+    if not _same_device(dev, al.offsets, al.inv_pos, out):
+        with torch.cuda.device(dev):
+            return moe_permute(d, x, al, out)
+    if x.dim() != 2 or x.shape[0] != d.T:
+        raise ValueError(f"x must be [{d.T}, width]")
+    _check_alignment(d, al)
+    if out is not None:
+        _no_gradient("moe_permute with out", x, out)
+        if out.shape != (_pairs(d), x.shape[1]) or out.dtype != x.dtype or not out.is_contiguous() \
+                or out.data_ptr() % 16:
+            raise ValueError(f"out must be contiguous, 16-byte aligned [{_pairs(d)}, {x.shape[1]}] in the type of x")
+    elif x.requires_grad and torch.is_grad_enabled():
+        return _Permute.apply(x, d, al.offsets, al.inv_pos)
+    return _permute(d, x, al.offsets, al.inv_pos, out)
+
+
+def moe_unpermute(d: Dims, rows: torch.Tensor, al: Alignment, topk_w: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
+    """Every token's rows summed, [T, width]: out[t] = sum_j topk_w[t, j] row of
+    pair (t, j), plus the shared expert's row (FP32, rounded once to
+    ``out_dtype``, the rows' type by default).  ``rows`` [P, width] in moe_permute's
+    order; without ``topk_w`` (float32 [T, topk]) every weight is 1.  Differentiable
+    in rows and topk_w (without ``out``); a saved tensor that a call of this
+    module writes through ``out`` before the backward pass is not noticed."""
+    dev = rows.get_device()
+    if not _same_device(dev, al.offsets, al.inv_pos, topk_w, out):
+        with torch.cuda.device(dev):
+            return moe_unpermute(d, rows, al, topk_w, out, out_dtype)
+    if rows.dim() != 2 or rows.shape[0] != _pairs(d):
+        raise ValueError(f"rows must be [{_pairs(d)}, width]")
+    _check_alignment(d, al)
+    if topk_w is not None:
+        if topk_w.shape != (d.T, d.topk) or topk_w.dtype != torch.float32:
+            raise ValueError(f"topk_w must be float32 [{d.T}, {d.topk}]")
+        topk_w = topk_w.contiguous()
+    rows = _whole(rows)
+    if out is not None:
+        _no_gradient("moe_unpermute with out", rows, topk_w, out)
+        if out.shape != (d.T, rows.shape[1]) or not out.is_contiguous() or out.data_ptr() % 16:
+            raise ValueError(f"out must be contiguous, 16-byte aligned [{d.T}, {rows.shape[1]}]")
+    elif torch.is_grad_enabled() and (rows.requires_grad or (topk_w is not None and topk_w.requires_grad)):
+        return _Unpermute.apply(rows, topk_w, d, al.offsets, al.inv_pos, out_dtype)
+    return _unpermute(d, rows, al.offsets, al.inv_pos, topk_w, out, out_dtype)
+
+
 # ---------------------------------------------------------------- MXFP4 layer
 @dataclasses.dataclass
 class MxExpertWeights:
@@ -676,6 +1033,7 @@ class MxMoELayer:
 
     def forward(self, x, topk_ids, topk_w, out=None, out_dtype=torch.bfloat16, weights=None, marks=None):
         d, w, s = self.d, weights or self.w, _stream()
+        _written(self.al.offsets, self.al.inv_pos)
         if out is None:
             out = torch.empty(d.T, d.H, dtype=out_dtype, device=x.device)
         call("moe_mxfp4_quantize_and_align", ctypes.byref(d), _p(x), _p(self.a1_q), _p(self.a1_e), _p(topk_ids),
@@ -787,6 +1145,7 @@ class MoELayer:
         GEMM1, between the GEMMs and after GEMM2 + combine."""
         d, w = self.d, weights or self.w
         self.x_last, self.tw_last = x, topk_w
+        _written(self.al.offsets, self.al.inv_pos)
         if out is None:
             out = torch.empty(d.T, d.H, dtype=out_dtype, device=x.device)
         s = _stream()
