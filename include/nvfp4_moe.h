@@ -477,8 +477,8 @@ int int8_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ldx
  *   epi: as for nvfp4_linear_fused (its gated is the weight's), or NULL: the
  *     product alone into contiguous out.
  * N a multiple of 4 (gated: of 8), at most 2^20; K a multiple of 16 below 131072
- * (so that no sum passes 31 bits), bfloat16 x at most 32768; M <= 2^24,
- * M N <= 2^40.  A row or column whose scale is NaN gives NaN.
+ * (so that no sum passes 31 bits), bfloat16 x at most 32768; ldx at most 2^22;
+ * M <= 2^24, M N <= 2^40.  A row or column whose scale is NaN gives NaN.
  * ws: int8_linear_workspace_size(M, N, K, x_dtype) bytes, 256-byte aligned, no
  * initial contents; it serves every call of fewer rows, and bfloat16's serves
  * int8 codes too. */

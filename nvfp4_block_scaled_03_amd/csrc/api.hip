@@ -1085,7 +1085,7 @@ bool int8_shape_ok(int64_t M, int64_t N, int64_t K, int x_dtype, int gated) {
   return int8_weight_ok(N, K, gated) && M >= 0 && M <= (int64_t(1) << 24) && M * N <= (int64_t(1) << 40) &&
          (x_dtype == NVFP4_I8 || K <= nvfp4::kNormMaxH);
 }
-// Workspace: codes and scales of bfloat16 activations.
+// Workspace: sums of a K in parts, then codes and scales of bfloat16 activations.
 size_t int8_ws_codes(int64_t M, int64_t K) { return up256((size_t)M * (size_t)K); }
 }  // namespace
 
@@ -1106,7 +1106,9 @@ int int8_prep_weights(int64_t N, int64_t K, int gated, const int8_t* q, uint8_t*
 
 size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int x_dtype) {
   if ((x_dtype != NVFP4_BF16 && x_dtype != NVFP4_I8) || !int8_shape_ok(M, N, K, x_dtype, 0)) return 0;
-  return x_dtype == NVFP4_BF16 ? int8_ws_codes(M, K) + up256((size_t)M * 4) : 0;
+  // (whole 64-column blocks: a gated layer of N may have one more)
+  const size_t part = up256(std::max(nvfp4::int8_part_bytes(M, N, false), nvfp4::int8_part_bytes(M, N, N % 8 == 0)));
+  return part + (x_dtype == NVFP4_BF16 ? int8_ws_codes(M, K) + up256((size_t)M * 4) : 0);
 }
 
 int int8_linear(const void* x, int x_dtype, int64_t ldx, const float* sx, int64_t M, int64_t N, int64_t K,
@@ -1117,10 +1119,11 @@ int int8_linear(const void* x, int x_dtype, int64_t ldx, const float* sx, int64_
   const nvfp4_epilogue plain = {NVFP4_ACT_NONE, 0, nullptr, nullptr, 0, 0, N};
   const nvfp4_epilogue* e = epi ? epi : &plain;
   const int64_t unit = x_dtype == NVFP4_I8 ? 16 : 8;
-  if (!int8_shape_ok(M, N, K, x_dtype, e->gated) || ldx < K || ldx % unit)
+  if (!int8_shape_ok(M, N, K, x_dtype, e->gated) || ldx < K || ldx % unit ||
+      ldx > (int64_t(1) << 22))
     return fail(NVFP4_ESHAPE, "%s: ESHAPE M=%lld N=%lld K=%lld ldx=%lld gated=%d (N a multiple of 4, gated of 8, at most "
                 "2^20; K a multiple of 16 below 131072, bfloat16 x: at most %d; M <= 2^24, M N <= 2^40; ldx >= K a multiple "
-                "of %d)", W, (long long)M, (long long)N, (long long)K, (long long)ldx, e->gated, nvfp4::kNormMaxH, (int)unit);
+                "of %d, at most 2^22)", W, (long long)M, (long long)N, (long long)K, (long long)ldx, e->gated, nvfp4::kNormMaxH, (int)unit);
   nvfp4::Int8Args a{};
   if (int r = check_epilogue(W, e, M, N, K, out, out_dtype, &a.ep, 8)) return r;
   const size_t need = int8_linear_workspace_size(M, N, K, x_dtype);
@@ -1140,9 +1143,11 @@ int int8_linear(const void* x, int x_dtype, int64_t ldx, const float* sx, int64_
   a.sx = sx;
   a.w = w_prep;
   a.sw = sw;
+  a.part = static_cast<int*>(ws);
   if (x_dtype == NVFP4_BF16) {
-    int8_t* q = static_cast<int8_t*>(ws);
-    float* s = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + int8_ws_codes(M, K));
+    uint8_t* at = static_cast<uint8_t*>(ws) + int8_linear_workspace_size(M, N, K, NVFP4_I8);
+    int8_t* q = reinterpret_cast<int8_t*>(at);
+    float* s = reinterpret_cast<float*>(at + int8_ws_codes(M, K));
     const hipError_t err = quantize_rows(x, NVFP4_BF16, M, K, ldx, q, s, stream);
     if (err != hipSuccess) return launched(err, W);
     a.a = q;

@@ -48,8 +48,11 @@ struct Int8Args {
   const float* sx;     // [M]
   const uint8_t* w;    // streaming layout
   const float* sw;     // [N]
+  int* part;           // partial sums of a split K
   LinearEpi ep;
 };
+// Bytes of part that every call of up to M rows is content with.
+size_t int8_part_bytes(int64_t M, int64_t N, bool gated);
 hipError_t launch_int8_linear(const Int8Args& a, hipStream_t s);
 
 }  // namespace nvfp4

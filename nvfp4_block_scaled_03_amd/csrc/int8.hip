@@ -49,9 +49,10 @@ __global__ __launch_bounds__(256) void int8_prep_kernel(int64_t N, int64_t K, bo
 }
 
 // ---------------------------------------------------------------------------
-// 16 MT rows x 16 NT columns a workgroup, whose KW wavefronts split K.  Both
-// operands come straight from memory into registers, the next chunk's while the
-// present one is multiplied; the partial sums meet in LDS and leave in whole rows.
+// A handful of rows: 16 MT rows x 16 NT columns a workgroup, whose KW wavefronts
+// split K.  Both operands come straight from memory into registers, the next
+// chunk's while the present one is multiplied; the partial sums meet in LDS and
+// leave in whole rows.
 // ---------------------------------------------------------------------------
 template <bool GATED, int MT, int NT, int KW>
 __global__ __launch_bounds__(KW * 64) void int8_few_kernel(Int8Args p) {
@@ -147,11 +148,316 @@ hipError_t launch_few_t(const Int8Args& p, hipStream_t s) {
   int8_few_kernel<GATED, MT, NT, KW><<<(unsigned)(groups * 8 * rb), KW * 64, 0, s>>>(p);
   return hipGetLastError();
 }
+// ---------------------------------------------------------------------------
+// Tiles of BM = 16 TM WR rows x BN = 16 TN WC columns for many rows: WR x WC
+// wavefronts of 16 TM x 16 TN each.  Both operands travel from memory straight
+// into a ring of D LDS stages of 128 k.
+//
+// Activations are taken row-major: eight neighbouring lanes fetch the 128
+// bytes of a row, a whole cache line, and a row's eight 16-byte units are
+// swizzled by the row, so that the 16 rows of a fragment (one unit each) fall
+// into distinct banks.  A stage's weights are whole operands as they lie.
+// ---------------------------------------------------------------------------
+constexpr int kMaxParts = 4;                          // of K
+constexpr int64_t kPartBytes = int64_t(16) << 20;     // their sums, at most
+
+// s_waitcnt immediate: at most n vector memory operations outstanding.
+constexpr int wait_loads(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+
+template <bool GATED, bool SPLIT, int WR, int WC, int TM, int TN, int D, int OCC>
+__global__ __launch_bounds__(WR * WC * 64) __attribute__((amdgpu_waves_per_eu(WR * WC * OCC / 4, WR * WC * OCC / 4)))
+void int8_tile_kernel(Int8Args p, int nb0, int TNB, int S) {
+  constexpr int W = WR * WC, BM = 16 * TM * WR, BN = 16 * TN * WC, SW = BN + 4;
+  constexpr int LA = BM / 8, LB = BN / 8;          // 1 KiB loads of a stage
+  constexpr int PA = LA / W, PB = LB / W;          // of which each wavefront issues
+  static_assert(LA % W == 0 && LB % W == 0, "whole loads per wavefront");
+  static_assert(D >= 2 && (D - 1) * (PA + PB) <= 63, "ring depth");
+  constexpr int STAGE = (LA + LB) * 1024;
+  constexpr int PARTS = TM % 2 == 0 ? 2 : TM, PM = TM / PARTS, EPI = BM / PARTS * SW * 4;   // (the epilogue's)
+  constexpr int LDS = D * STAGE > EPI ? D * STAGE : EPI;
+  static_assert(LDS * OCC <= 160 * 1024, "LDS of the workgroups on a CU");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[LDS];
+  const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), wr = wv / WC, wc = wv % WC;
+  const int KC = (int)int8_chunks(p.K), NS = KC / 2, tiles = (int)int8_tiles(p.N, GATED);
+  // Workgroups go to the 8 XCDs in turn: the ones of an XCD take neighbours of a
+  // list that walks groups of GM row blocks column block by column block.
+  constexpr int GM = 8;
+  const int TMB = (p.M + BM - 1) / BM, total = TMB * TNB;   // column blocks nb0 .. nb0 + TNB - 1
+  const int per_xcd = (total * S + 7) / 8;
+  int L = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
+  if ((int)(blockIdx.x / 8) >= per_xcd || L >= total * S) return;
+  auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  const int part = SPLIT ? uniform(L / total) : 0;   // of the S parts of K
+  L -= part * total;
+  const int c_lo = SPLIT ? uniform(NS * part / S) : 0, n_st = SPLIT ? uniform(NS * (part + 1) / S) - c_lo : NS;   // stages
+  const int grp = L / (GM * TNB), gh = min(GM, TMB - grp * GM), Lg = L - grp * GM * TNB;
+  const int mb = uniform(grp * GM + Lg % gh), nb = uniform(nb0 + Lg / gh);
+
+  // Sources: a lane's offset within the block's rows or tiles; a stage adds to
+  // the scalar base.  Rows and tiles past the end repeat the last ones (never
+  // stored).
+  const int8_t* const a0 = p.a + (int64_t)mb * BM * p.lda;
+  const uint8_t* const w0 = p.w + (int64_t)nb * (BN / 16) * KC * 1024;
+  uint32_t ra[PA], ua[PA], vb[PB];
+#pragma unroll
+  for (int q = 0; q < PA; ++q) {
+    const int r = 8 * (wv * PA + q) + (lane >> 3);
+    ra[q] = (uint32_t)(min(r, p.M - 1 - mb * BM) * (int)p.lda);
+    ua[q] = (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) * 16);
+  }
+#pragma unroll
+  for (int q = 0; q < PB; ++q) {
+    const int i = wv * PB + q;                     // tile i / 2, chunk i % 2 of the stage
+    vb[q] = (uint32_t)((min(i >> 1, tiles - 1 - nb * (BN / 16)) * KC + (i & 1)) * 1024 + lane * 16);
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  // Assembly: the compiler would wait for every direct load before any later
+  // LDS read.  Completion is awaited explicitly below.
+  auto issue = [&](int c, int slot) {
+    c = c_lo + min(c, n_st - 1);                   // past the end: the last stage, not used
+    const uint32_t base = lds0 + slot * STAGE;
+    // (past K the weights are zeros: any bytes of the row will do; a stage begins
+    // before K, so the row's last unit lies at or behind that)
+    const uint32_t last = (uint32_t)(p.K - 16 - 128 * c);
+    const int8_t* const as = a0 + (int64_t)c * 128;
+    const uint8_t* const ws = w0 + (int64_t)c * 2048;
+#pragma unroll
+    for (int q = 0; q < PA; ++q)
+      asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(ra[q] + min(ua[q], last)), "s"(as),
+                   "{m0}"(base + (wv * PA + q) * 1024) : "memory");
+#pragma unroll
+    for (int q = 0; q < PB; ++q)
+      asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(vb[q]), "s"(ws),
+                   "{m0}"(base + LA * 1024 + (wv * PB + q) * 1024) : "memory");
+  };
+
+  i32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  struct Frags {
+    i32x4 a[TM], b[TN];
+  };
+  // Fragments of chunk s of a stage: row 16 i + ln, unit 4 s + lg at its
+  // swizzled place; column tile j as it lies.
+  const int at_a = wr * TM * 2048 + ln * 128, at_b = LA * 1024 + wc * TN * 2048 + lane * 16, sw = (ln >> 1) & 7;
+  auto read = [&](int slot, int s, Frags& f) {
+    const uint8_t* const st = lds + slot * STAGE;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) f.b[j] = *reinterpret_cast<const i32x4*>(st + at_b + j * 2048 + s * 1024);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(st + at_a + i * 2048 + ((4 * s + lg) ^ sw) * 16);
+  };
+  auto multiply = [&](const Frags& f) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+  };
+  Frags f0, f1;
+#pragma unroll
+  for (int c = 0; c < D; ++c) issue(c, c);
+  __builtin_amdgcn_s_waitcnt(wait_loads((D - 1) * (PA + PB)));
+  __syncthreads();
+  read(0, 0, f0);
+  read(0, 1, f1);
+  multiply(f0);
+  // Trip c: stage c + 1 has landed and everybody holds what is left of stage c
+  // in registers; refill its slot, and read ahead of the products.
+  for (int c0 = 0; c0 < n_st - 1; c0 += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (c0 + d < n_st - 1) {
+        __builtin_amdgcn_s_waitcnt(wait_loads((D - 2) * (PA + PB)));
+        __syncthreads();
+        issue(c0 + d + D, d);
+        read((d + 1) % D, 0, f0);
+        multiply(f1);
+        read((d + 1) % D, 1, f1);
+        multiply(f0);
+      }
+    }
+  }
+  multiply(f1);
+  // (stages past the end may still be in flight)
+  __builtin_amdgcn_s_waitcnt(wait_loads(0));
+
+  const int64_t m0 = (int64_t)mb * BM + wr * 16 * TM;
+  if constexpr (SPLIT) {
+    // The part's sums, in streaming columns.
+    const int64_t NP = (int64_t)tiles * 16;
+    int* const at = p.part + (int64_t)part * p.M * NP + (int64_t)(nb * (BN / 16) + wc * TN) * 16 + ln;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      if (nb * (BN / 16) + wc * TN + j >= tiles) break;
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int64_t row = m0 + i * 16 + lg * 4 + r;
+          if (row < p.M) at[row * NP + j * 16] = acc[i][j][r];
+        }
+    }
+    return;
+  }
+  // Part of the rows at a time through LDS, so that they leave, and residuals
+  // come, in whole rows.
+  float* const sh = reinterpret_cast<float*>(lds);
+  float swv[TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int64_t r = weight_row(nb * (BN / 16) + wc * TN + j, ln, p.N, GATED);
+    swv[j] = r < 0 ? 0.0f : p.sw[r];
+  }
+#pragma unroll
+  for (int h = 0; h < PARTS; ++h) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PM; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float sx = p.sx[min(m0 + (h * PM + i) * 16 + lg * 4 + r, (int64_t)p.M - 1)];
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          sh[((wr * PM + i) * 16 + lg * 4 + r) * SW + (wc * TN + j) * 16 + ln] = (float)acc[h * PM + i][j][r] * (sx * swv[j]);
+      }
+    __syncthreads();
+    emit_tile<GATED, WR * 16 * PM, BN, W * 64>(
+        p.ep, p.M, p.N, nb,
+        [&](int r) { return (int64_t)mb * BM + (r / (16 * PM)) * 16 * TM + h * 16 * PM + r % (16 * PM); },
+        [&](int at) { return *reinterpret_cast<const f32x4*>(sh + at); });
+  }
+}
+
+// Adds the S parts of four output columns and finishes them.
 template <bool GATED>
-hipError_t launch_few(const Int8Args& p, hipStream_t s) {
-  if (p.M <= 16) return launch_few_t<GATED, 1, 4, 4>(p, s);
-  if (p.M <= 32) return launch_few_t<GATED, 2, 4, 4>(p, s);
-  return launch_few_t<GATED, 4, 4, 4>(p, s);
+__global__ __launch_bounds__(256) void int8_join_kernel(Int8Args p, int S) {
+  const int64_t n_out = GATED ? p.N / 2 : p.N, NP = int8_tiles(p.N, GATED) * 16;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = n_out / 4;
+  const int64_t row[1] = {i / quads}, col = (i - row[0] * quads) * 4;
+  if (row[0] >= p.M) return;
+  EpiIn<1> in;
+  epi_request<GATED>(p.ep, row[0], col, in);
+  const float sx = p.sx[row[0]];
+  auto sum = [&](int64_t at, const float* sw) {
+    i32x4 v = {0, 0, 0, 0};
+    for (int k = 0; k < S; ++k) v += *reinterpret_cast<const i32x4*>(p.part + ((int64_t)k * p.M + row[0]) * NP + at);
+    return f32x4{(float)v[0] * (sx * sw[0]), (float)v[1] * (sx * sw[1]), (float)v[2] * (sx * sw[2]),
+                 (float)v[3] * (sx * sw[3])};
+  };
+  const int64_t src = GATED ? (col >> 4) * 32 + (col & 15) : col;
+  const f32x4 v = sum(src, p.sw + col), up[1] = {GATED ? sum(src + 16, p.sw + p.ep.half + col) : v};
+  float z[4] = {v[0], v[1], v[2], v[3]};
+  epi_finish<GATED, 1>(p.ep, z, up, in, row, col);
+}
+
+// Column blocks nb0 .. nb0 + nbs - 1 of 16 TN WC columns; K in S parts (SPLIT:
+// of all columns).
+template <bool GATED, bool SPLIT, int WR, int WC, int TM, int TN, int D, int OCC>
+hipError_t launch_tile_t(const Int8Args& p, int nb0, int nbs, int S, hipStream_t s) {
+  S = std::min(S, (int)int8_chunks(p.K) / 2);   // (a stage or more in every part)
+  const int64_t rb = (p.M + 16 * TM * WR - 1) / (16 * TM * WR);
+  int8_tile_kernel<GATED, SPLIT, WR, WC, TM, TN, D, OCC>
+      <<<(unsigned)((rb * nbs * S + 7) / 8 * 8), WR * WC * 64, 0, s>>>(p, nb0, nbs, S);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !SPLIT) return e;
+  const int64_t quads = (int64_t)p.M * (GATED ? p.N / 2 : p.N) / 4;
+  int8_join_kernel<GATED><<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(p, S);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// The choice.  A kernel's time, in us, follows the tiles that a CU gets: with
+// u = ceil(tiles / 256) of them, `occ` at a time,
+//   a + (u / 2) (f2 + b2 stages) + (u % 2) (f1 + b1 stages)     (occ 1: u (f1 + b1 stages))
+// with stages of 128 k; a K in S parts divides the stages, multiplies the tiles
+// and costs a launch and the sums' way through memory, 2.4 + 4 S M N / 2.2e6.  No
+// kernel is faster than its weights come: 3 + N K / 5.0e6.  Fitted to 1600
+// timings in graphs of 11 weights from 2048 x 512 to 34816 x 5120 with M = 16 ..
+// 4096; the choice by it is 1 % slower than the best one on average, 15 % at most.
+// E.g. (us, 16 / 32 / 64 / 128 x 64, 256 x 128, 256 x 256): 4096 x 4096 M = 32
+// 9.3 / 10.6 / 11.4 / 15.5 / - / -, M = 512 42 / 26.5 / 18.9 / 17.7 / 30.5 / 54,
+// M = 4096 - / - / - / 102 / 76 / 65; K in 1 / 2 / 4 parts: 5120 x 17408 M = 16
+// 30.2 / 22.3 / 25.8 (16 x 64), M = 128 60.6 / 37.5 / 40.1 (128 x 64).
+// ---------------------------------------------------------------------------
+struct TileCost {
+  int bm, bn, occ, max_parts;
+  float a, f1, b1, f2, b2;
+};
+constexpr TileCost kTiles[] = {
+    {16, 64, 2, kMaxParts, 2.4f, 0.90f, 0.175f, 1.38f, 0.277f}, {32, 64, 2, kMaxParts, 2.6f, 0.64f, 0.217f, 1.33f, 0.318f},
+    {64, 64, 2, kMaxParts, 2.8f, 1.07f, 0.240f, 2.33f, 0.415f}, {128, 64, 2, kMaxParts, 3.0f, 1.70f, 0.367f, 3.25f, 0.657f},
+    {256, 128, 1, 1, 1.5f, 6.93f, 0.722f, 0.0f, 0.0f},          {256, 256, 1, 1, 1.5f, 11.7f, 1.283f, 0.0f, 0.0f},
+};
+constexpr int kTileKinds = sizeof(kTiles) / sizeof(kTiles[0]);
+
+float tile_cost(const TileCost& t, int64_t M, int64_t columns, int64_t K, int S) {
+  const int64_t n = (M + t.bm - 1) / t.bm * ((columns + t.bn - 1) / t.bn) * S, u = (n + 255) / 256;
+  const float st = (float)(((K + 127) / 128 + S - 1) / S), n2 = (float)(u / t.occ), n1 = (float)(u % t.occ);
+  float c = t.a + (t.occ == 1 ? n2 * (t.f1 + t.b1 * st) : n2 * (t.f2 + t.b2 * st) + n1 * (t.f1 + t.b1 * st));
+  if (S > 1) c += 2.4f + 4.0f * S * M * columns / 2.2e6f;
+  return std::max(c, 3.0f + (float)columns * K / 5.0e6f);
+}
+
+struct Choice {
+  int kind, parts;
+  float cost;
+};
+// The fastest kind for `columns` streaming columns.
+Choice choose(int64_t M, int64_t columns, int64_t K, int max_parts) {
+  Choice best = {0, 1, 3.0e38f};
+  for (int kind = 0; kind < kTileKinds; ++kind)
+    for (int S = 1; S <= std::min(max_parts, kTiles[kind].max_parts); S *= 2) {
+      if (S > 1 && (S > (K + 127) / 128 || (int64_t)S * M * columns * 4 > kPartBytes)) break;
+      const float c = tile_cost(kTiles[kind], M, columns, K, S);
+      if (c < best.cost) best = {kind, S, c};
+    }
+  return best;
+}
+
+template <bool GATED>
+hipError_t launch_kind(const Int8Args& p, int kind, int parts, int64_t col0, int64_t cols, hipStream_t s) {
+  const int bn = kTiles[kind].bn, nb0 = (int)(col0 / bn), nbs = (int)((cols + bn - 1) / bn);
+  switch (kind) {
+    case 0:
+      return parts > 1 ? launch_tile_t<GATED, true, 1, 2, 1, 2, 6, 2>(p, nb0, nbs, parts, s)
+                       : launch_tile_t<GATED, false, 1, 2, 1, 2, 6, 2>(p, nb0, nbs, 1, s);
+    case 1:
+      return parts > 1 ? launch_tile_t<GATED, true, 2, 2, 1, 2, 4, 2>(p, nb0, nbs, parts, s)
+                       : launch_tile_t<GATED, false, 2, 2, 1, 2, 4, 2>(p, nb0, nbs, 1, s);
+    case 2:
+      return parts > 1 ? launch_tile_t<GATED, true, 2, 2, 2, 2, 4, 2>(p, nb0, nbs, parts, s)
+                       : launch_tile_t<GATED, false, 2, 2, 2, 2, 4, 2>(p, nb0, nbs, 1, s);
+    case 3:
+      return parts > 1 ? launch_tile_t<GATED, true, 2, 2, 4, 2, 3, 2>(p, nb0, nbs, parts, s)
+                       : launch_tile_t<GATED, false, 2, 2, 4, 2, 3, 2>(p, nb0, nbs, 1, s);
+    case 4: return launch_tile_t<GATED, false, 4, 2, 4, 4, 3, 1>(p, nb0, nbs, 1, s);
+    default: return launch_tile_t<GATED, false, 2, 4, 8, 4, 2, 1>(p, nb0, nbs, 1, s);
+  }
+}
+
+template <bool GATED>
+hipError_t launch_chosen(const Int8Args& p, hipStream_t s) {
+  // A handful of rows: x straight from the caches (us, against 16 x 64 tiles:
+  // 34816 x 5120 M = 1 33 to 37 / 38.1, M = 8 35.8 / 38.6, M = 16 43.0 / 39.5; 5120 x
+  // 5120 8.7 / 10.3, 8.7 / 10.9, 10.1 / 11.5; 16384 x 2048 10.3 / 9.0, 10.8 / 8.8).
+  if (p.M <= 8) return launch_few_t<GATED, 1, 2, 8>(p, s);
+  const int64_t columns = int8_tiles(p.N, GATED) * 16;
+  const Choice one = choose(p.M, columns, p.K, kMaxParts);
+  // Whole rounds of 256 x 256 tiles, and the columns left over by another kernel
+  // (4096 x 5120 x 17408: 393 us in 256 x 256 tiles, 347 in 256 x 128).
+  const int64_t rb = (p.M + 255) / 256, cb = (columns + 255) / 256, whole = rb * cb / 256 * 256 / rb;
+  if (whole > 0 && whole < cb) {
+    const int64_t rest = columns - whole * 256;
+    const Choice two = choose(p.M, rest, p.K, 1);
+    if (tile_cost(kTiles[kTileKinds - 1], p.M, whole * 256, p.K, 1) + two.cost < one.cost) {
+      const hipError_t e = launch_kind<GATED>(p, kTileKinds - 1, 1, 0, whole * 256, s);
+      return e != hipSuccess ? e : launch_kind<GATED>(p, two.kind, 1, whole * 256, rest, s);
+    }
+  }
+  return launch_kind<GATED>(p, one.kind, one.parts, 0, columns, s);
 }
 
 }  // namespace
@@ -167,8 +473,12 @@ hipError_t launch_int8_prep(int64_t N, int64_t K, bool gated, const int8_t* q, u
   return hipGetLastError();
 }
 
+size_t int8_part_bytes(int64_t M, int64_t N, bool gated) {
+  return (size_t)std::min<int64_t>(kMaxParts * M * int8_tiles(N, gated) * 64, kPartBytes);
+}
+
 hipError_t launch_int8_linear(const Int8Args& p, hipStream_t s) {
-  return p.ep.gated ? launch_few<true>(p, s) : launch_few<false>(p, s);
+  return p.ep.gated ? launch_chosen<true>(p, s) : launch_chosen<false>(p, s);
 }
 
 }  // namespace nvfp4

@@ -782,7 +782,7 @@ def int8_linear(x: torch.Tensor, w: Int8LinearWeight, s: Optional[torch.Tensor] 
     elif s is not None:
         raise ValueError("scales belong to int8 x")
     unit = 16 if codes else 8
-    if x.stride(1) != 1 or x.data_ptr() % 16 or (M > 1 and (x.stride(0) < K or x.stride(0) % unit)):
+    if x.stride(1) != 1 or x.data_ptr() % 16 or (M > 1 and (x.stride(0) < K or x.stride(0) % unit or x.stride(0) > 1 << 22)):
         x = x.clone(memory_format=torch.contiguous_format)
     if out is None:
         out = torch.empty(M, n_out, dtype=out_dtype, device=x.device)

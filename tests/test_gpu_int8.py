@@ -146,7 +146,9 @@ def test_epilogues(dev, M, cfg):
 
 # every kernel of the larger sizes, with left-over rows and columns
 @pytest.mark.parametrize("M,N,K", [(64, 8200, 1040), (130, 4104, 2064), (700, 2056, 1040), (1030, 4104, 528),
-                                   (2049, 1032, 272), (4100, 8200, 144), (600, 40000, 80), (16, 65544, 208)])
+                                   (2049, 1032, 272), (4100, 8200, 144), (600, 40000, 80), (16, 65544, 208),
+                                   (17, 1032, 8208), (129, 1032, 8208), (40, 520, 8208), (300, 1032, 8208),
+                                   (4096, 4360, 1040), (4100, 4360, 2064), (2100, 16400, 528), (700, 136, 16400)])
 @pytest.mark.parametrize("cfg", [CONFIGS[1], CONFIGS[5]], ids=["plain", "gated"])
 def test_larger_layers(dev, M, N, K, cfg):
     act, gated, with_bias, rt, ot = cfg
@@ -187,15 +189,16 @@ def _rows_of_large(dev, M, N, K, cfg):
     return got
 
 
-def test_codes_at_their_ends(dev):
+@pytest.mark.parametrize("M", [2, 20, 100, 300])
+def test_codes_at_their_ends(dev, M):
     """|sum| up to 2^14 K just below 2^31, either sign."""
     K = 131056
-    xq = torch.full((2, K), -128, dtype=torch.int8, device=dev)
+    xq = torch.full((M, K), -128, dtype=torch.int8, device=dev)
     wq = torch.full((8, K), -128, dtype=torch.int8, device=dev)
     wq[1::2] = 127
     one = lambda n: torch.ones(n, device=dev)
-    got = ops.int8_linear(xq, ops.prepare_int8_weight(wq, one(8)), one(2), out_dtype=F32)
-    want = torch.tensor([16384.0 * K, -16256.0 * K]).repeat(2, 4)
+    got = ops.int8_linear(xq, ops.prepare_int8_weight(wq, one(8)), one(M), out_dtype=F32)
+    want = torch.tensor([16384.0 * K, -16256.0 * K]).repeat(M, 4)
     assert torch.equal(got.cpu(), want.float())
 
 
