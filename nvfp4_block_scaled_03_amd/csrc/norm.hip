@@ -69,28 +69,63 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
   }
 }
 
-__device__ __forceinline__ uint32_t lane_xor(uint32_t v, int off) { return (uint32_t)__shfl_xor((int)v, off); }
-__device__ __forceinline__ uint64_t lane_xor(uint64_t v, int off) {
-  return (uint64_t)lane_xor((uint32_t)(v >> 32), off) << 32 | lane_xor((uint32_t)v, off);
+// Reductions over a row's lanes: DPP steps within 16 lanes, the four groups by
+// lane reads (every lane gets the result).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
 }
-__device__ __forceinline__ double lane_xor(double v, int off) {
-  return __longlong_as_double((long long)lane_xor((uint64_t)__double_as_longlong(v), off));
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp64(uint64_t v) {
+  return (uint64_t)dpp32<CTRL>((uint32_t)(v >> 32)) << 32 | dpp32<CTRL>((uint32_t)v);
+}
+__device__ __forceinline__ uint64_t lane64(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+// What a row's lanes gather: the sum of squares and the largest magnitude (as
+// bits: NaN above infinity above the rest).
+struct Gathered {
+  double ss;
+  uint64_t top;
+  __device__ __forceinline__ void add(double s, uint64_t t) {
+    ss += s;
+    top = max(top, t);
+  }
+};
+__device__ __forceinline__ uint64_t bits_of(double v) { return (uint64_t)__double_as_longlong(v); }
+__device__ __forceinline__ double of_bits(uint64_t v) { return __longlong_as_double((long long)v); }
+__device__ __forceinline__ void reduce16(Gathered& g) {
+  g.add(of_bits(dpp64<0xB1>(bits_of(g.ss))), dpp64<0xB1>(g.top));     // lane ^ 1
+  g.add(of_bits(dpp64<0x4E>(bits_of(g.ss))), dpp64<0x4E>(g.top));     // lane ^ 2
+  g.add(of_bits(dpp64<0x141>(bits_of(g.ss))), dpp64<0x141>(g.top));   // mirror of 8
+  g.add(of_bits(dpp64<0x140>(bits_of(g.ss))), dpp64<0x140>(g.top));   // mirror of 16
+}
+template <int WAVES>
+__device__ __forceinline__ void row_reduce(Gathered& g, Gathered* red) {
+  reduce16(g);
+  Gathered r = {of_bits(lane64(bits_of(g.ss), 0)), lane64(g.top, 0)};
+#pragma unroll
+  for (int l = 16; l < 64; l += 16) r.add(of_bits(lane64(bits_of(g.ss), l)), lane64(g.top, l));
+  g = r;
+  if constexpr (WAVES > 1) {
+    static_assert(WAVES <= 16, "a result per lane of a group");
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = g;
+    __syncthreads();
+    const int l = threadIdx.x & 15;
+    g = red[l % WAVES];
+    if (l >= WAVES) g.ss = 0.0;
+    reduce16(g);
+  }
 }
 
-// Reductions over the WAVES wavefronts of a row (every thread gets the result).
-template <int WAVES, class T, class Op>
-__device__ __forceinline__ T row_reduce(T v, T* red, const Op& op) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = op(v, lane_xor(v, off));
-  if constexpr (WAVES > 1) {
-    const int wv = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) red[wv] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int k = 1; k < WAVES; ++k) v = op(v, red[k]);
-  }
-  return v;
+// 1 / sqrt(x) by two Newton steps on the hardware's estimate (2^-14 or better).
+__device__ __forceinline__ double rsqrt64(double x) {
+  const double y0 = __builtin_amdgcn_rsq(x), hx = 0.5 * x;
+  double y = y0 * __builtin_fma(-hx * y0, y0, 1.5);
+  y = y * __builtin_fma(-hx * y, y, 1.5);
+  y = y * __builtin_fma(-hx * y, y, 1.5);
+  return x > 0.0 && x < (double)INFINITY ? y : y0;
 }
 
 // |code| of one value: k = floor(t), one more beyond k + 1/2 (at it: if k is odd).
@@ -120,9 +155,7 @@ template <bool NORM, bool XF32, int RES, int TPR, int VPT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(NormArgs p) {
   constexpr int ROWS = TPR < 256 ? 256 / TPR : 1, WAVES = TPR / 64;
   constexpr bool HF32 = RES == 2 || (RES == 0 && XF32);   // type of h
-  __shared__ double red_d[WAVES > 1 ? WAVES : 1];
-  __shared__ uint64_t red_l[WAVES > 1 ? WAVES : 1];
-  __shared__ uint32_t red_u[WAVES > 1 ? WAVES : 1];
+  __shared__ Gathered red[WAVES > 1 ? WAVES : 1], red2[WAVES > 1 ? WAVES : 1];
   const int t = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
   if (ROWS > 1 && row >= p.rows) return;   // (whole wavefronts)
@@ -140,9 +173,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(NormArgs p) 
   }
   const bool wide = HF32 || (NORM && p.w_f32);   // v needs FP64
   float h[VPT][8];
-  double ss = 0.0;
+  Gathered g = {0.0, 0};
   uint32_t top_bits = 0;
-  uint64_t top64 = 0;   // magnitudes as bits: NaN above infinity above the rest
   auto weights = [&](int i, float (&w)[8]) {
     if constexpr (NORM) {
       Raw8 r;
@@ -172,17 +204,18 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(NormArgs p) 
       }
       if constexpr (NORM) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)h[i][j], (double)h[i][j], ss);
+        for (int j = 0; j < 8; ++j) g.ss = __builtin_fma((double)h[i][j], (double)h[i][j], g.ss);
       }
       if (p.q) {
         float w[8];
         weights(i, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          top_bits = max(top_bits, (uint32_t)__float_as_int(h[i][j] * w[j]) & 0x7FFFFFFFu);
         if (wide) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top64 = max(top64, magnitude_bits((double)h[i][j] * (double)w[j]));
+          for (int j = 0; j < 8; ++j) g.top = max(g.top, magnitude_bits((double)h[i][j] * (double)w[j]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            top_bits = max(top_bits, (uint32_t)__float_as_int(h[i][j] * w[j]) & 0x7FFFFFFFu);
         }
       }
     } else {
@@ -190,37 +223,31 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(NormArgs p) 
       for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
     }
   }
-  double rstd = 1.0;
-  if constexpr (NORM) {
-    ss = row_reduce<WAVES>(ss, red_d, [](double a, double b) { return a + b; });
-    rstd = 1.0 / sqrt(ss / p.H + (double)p.eps);
-  }
+  if (!wide) g.top = top_bits;
+  row_reduce<WAVES>(g, red);
+  const double rstd = NORM ? rsqrt64(g.ss / p.H + (double)p.eps) : 1.0;
   const float rs = (float)rstd;
   bool far = NORM && !(rs >= kTiny && rs <= kHuge);   // (NaN too)
   double top = 0.0;
   if (p.q) {
-    auto larger = [](auto a, auto b) { return a > b ? a : b; };
-    top_bits = row_reduce<WAVES>(top_bits, red_u, larger);
-    const float tf = __int_as_float((int)top_bits);
-    far = far || !(tf >= kTiny && tf <= kHuge);
-    if (far && !wide) {
+    top = wide ? of_bits(g.top) : (double)__int_as_float((int)(uint32_t)g.top);
+    far = far || !(top >= kTiny && top <= kHuge);
+    if (far && !wide) {   // (the same for the whole row)
+      g = {0.0, 0};
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         if (i * TPR + t < V) {
           float w[8];
           weights(i, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top64 = max(top64, magnitude_bits((double)h[i][j] * (double)w[j]));
+          for (int j = 0; j < 8; ++j) g.top = max(g.top, magnitude_bits((double)h[i][j] * (double)w[j]));
         }
       }
+      row_reduce<WAVES>(g, red2);
+      top = of_bits(g.top);
     }
-    if (far || wide) top = __longlong_as_double((long long)row_reduce<WAVES>(top64, red_l, larger));
-    else top = tf;
-    // (a row with NaN or infinity: scale NaN)
-    if (t == 0) p.s[row] = top < (double)INFINITY ? (float)(rstd * top / 127.0) : __builtin_nanf("");
   }
-  const float top32 = (float)top, inv32 = 127.0f / top32;
-  const double inv64 = 127.0 / top;
+  const float top32 = (float)top, inv32 = 127.0f * __builtin_amdgcn_rcpf(top32);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = i * TPR + t;
@@ -249,6 +276,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(NormArgs p) 
           c[j] = vj < 0.0f ? -k : k;
         }
       } else {
+        const double inv64 = 127.0 / top;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const double vj = (double)h[i][j] * (double)w[j];
@@ -263,6 +291,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(NormArgs p) 
       *reinterpret_cast<u32x2*>(p.q + row * p.H + v * 8) = o;
     }
   }
+  // (a row with NaN or infinity: scale NaN)
+  if (p.q && t == 0) p.s[row] = top < (double)INFINITY ? (float)(rstd * top / 127.0) : __builtin_nanf("");
 }
 
 template <bool NORM, bool XF32, int RES, int TPR, int VPT>
@@ -272,15 +302,31 @@ hipError_t launch_rows_t(const NormArgs& a, hipStream_t s) {
   row_kernel<NORM, XF32, RES, TPR, VPT><<<(unsigned)grid, TPR < 256 ? 256 : TPR, 0, s>>>(a);
   return hipGetLastError();
 }
+// Threads and pieces a thread.  Few rows: as many threads as there are pieces,
+// for the latency (H = 5120, both outputs, us: 1 row 256 x 3 6.4, 512 x 2 4.7, 1024 x
+// 1 4.2; 256 rows 8.3, 6.6, 6.0; 17408 1024 x 3 7.7, 256 x 9 14.9).  Many rows: more
+// pieces a thread, for fewer reductions and barriers a byte (8192 rows of 4096,
+// both outputs / codes alone: 256 x 2 60.5 / 24.0, 1024 x 1 66.1 / 35.4; of 8192 256 x
+// 4 121.6 / 42.2, 1024 x 1 113.0 / 53.3; of 1024 64 x 2 23.0 / 9.0, 256 x 1 22.7 / 12.3).
+// The first is 302 MB at 5.0 TB/s.
 template <bool NORM, bool XF32, int RES>
 hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
   const int V = a.H / 8;
   if (V <= 64) return launch_rows_t<NORM, XF32, RES, 64, 1>(a, s);
+  if (a.rows <= 1024) {
+    if (V <= 256) return launch_rows_t<NORM, XF32, RES, 256, 1>(a, s);
+    if (V <= 512) return launch_rows_t<NORM, XF32, RES, 512, 1>(a, s);
+    if (V <= 1024) return launch_rows_t<NORM, XF32, RES, 1024, 1>(a, s);
+    if (V <= 2048) return launch_rows_t<NORM, XF32, RES, 1024, 2>(a, s);
+    if (V <= 3072) return launch_rows_t<NORM, XF32, RES, 1024, 3>(a, s);
+    return launch_rows_t<NORM, XF32, RES, 512, 8>(a, s);
+  }
+  if (V <= 128) return launch_rows_t<NORM, XF32, RES, 64, 2>(a, s);
   if (V <= 256) return launch_rows_t<NORM, XF32, RES, 256, 1>(a, s);
   if (V <= 512) return launch_rows_t<NORM, XF32, RES, 256, 2>(a, s);
   if (V <= 1024) return launch_rows_t<NORM, XF32, RES, 256, 4>(a, s);
-  if (V <= 2048) return launch_rows_t<NORM, XF32, RES, 1024, 2>(a, s);
-  return launch_rows_t<NORM, XF32, RES, 1024, 4>(a, s);
+  if (V <= 2560) return launch_rows_t<NORM, XF32, RES, 512, 5>(a, s);
+  return launch_rows_t<NORM, XF32, RES, 512, 8>(a, s);
 }
 
 }  // namespace

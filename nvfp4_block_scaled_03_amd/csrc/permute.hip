@@ -8,6 +8,7 @@
 // atomics: a row belongs to one pair.  Sums run in FP32 in the order of j, the
 // shared row last.  Bound: bytes.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "permute.h"
@@ -46,38 +47,66 @@ struct Piece {
 
 struct KernelArgs {
   int T, topk, shared, P;
-  int64_t V;                // pieces of a row
+  int V;                    // pieces of a row
+  int bpt;                  // workgroups of a token
   const int32_t* kept;      // offsets[slots]
   const int32_t* inv_pos;
   const float* w;
 };
 
-// Row of pair j of token t, or -1 (also for a value outside the rows).
-__device__ __forceinline__ int row_of(const KernelArgs& p, int64_t t, int j) {
-  const int r = p.inv_pos[j < p.topk ? t * p.topk + j : (int64_t)p.T * p.topk + t];
+// Row of pair j of token t, or -1 (also for a value outside the rows).  The
+// same for the whole workgroup or wavefront: read through the scalar cache.
+__device__ __forceinline__ int row_of(const KernelArgs& p, int t, int j) {
+  const int r = ld_uniform(p.inv_pos + (j < p.topk ? (int64_t)t * p.topk + j : (int64_t)p.T * p.topk + t));
   return (unsigned)r < (unsigned)p.P ? r : -1;
 }
 
 // Workgroups from `first` on clear the rows behind the last kept one.
-__device__ __forceinline__ void clear_tail(const KernelArgs& p, u32x4* rows, int64_t first) {
-  const int64_t from = min(max(*p.kept, 0), p.P) * p.V, to = (int64_t)p.P * p.V;
-  const int64_t step = ((int64_t)gridDim.x - first) * blockDim.x;
-  for (int64_t i = from + ((int64_t)blockIdx.x - first) * blockDim.x + threadIdx.x; i < to; i += step)
+__device__ __forceinline__ void clear_tail(const KernelArgs& p, u32x4* rows, unsigned first) {
+  const int64_t from = (int64_t)min(max(*p.kept, 0), p.P) * p.V, to = (int64_t)p.P * p.V;
+  const int64_t step = (int64_t)(gridDim.x - first) * blockDim.x;
+  for (int64_t i = from + (int64_t)(blockIdx.x - first) * blockDim.x + threadIdx.x; i < to; i += step)
     rows[i] = u32x4{0, 0, 0, 0};
 }
 
+// Rows and weights of up to 64 pairs of a token, one a lane, read at once (a
+// chain of scalar loads, one waiting for the other, had cost more than the rows).
+struct Pairs {
+  int row;
+  float w;
+  __device__ __forceinline__ Pairs(const KernelArgs& p, int t, int j, int n) {
+    const bool on = j < n, routed = j < p.topk;
+    const int64_t f = on ? (routed ? (int64_t)t * p.topk + j : (int64_t)p.T * p.topk + t) : 0;
+    const int r = p.inv_pos[f];
+    row = on && (unsigned)r < (unsigned)p.P ? r : -1;
+    w = 1.0f;
+    if (p.w) {
+      const float v = p.w[routed ? f : 0];
+      w = routed ? v : 1.0f;
+    }
+  }
+  __device__ __forceinline__ int row_at(int j) const { return __builtin_amdgcn_readlane(row, j); }
+  __device__ __forceinline__ float w_at(int j) const {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), j));
+  }
+};
+
 // A thread moves one piece of a token's row to all its places.
 __global__ __launch_bounds__(256) void permute_kernel(KernelArgs p, const uint8_t* __restrict__ x, int64_t ld_bytes,
-                                                      u32x4* __restrict__ rows, int64_t blocks) {
+                                                      u32x4* __restrict__ rows, unsigned blocks) {
   if (blockIdx.x >= blocks) return clear_tail(p, rows, blocks);
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, t = i / p.V, v = i - t * p.V;
-  if (t >= p.T) return;
-  const u32x4 d = *reinterpret_cast<const u32x4*>(x + t * ld_bytes + v * 16);
+  const int t = (int)(blockIdx.x / (unsigned)p.bpt);
+  const int v = ((int)blockIdx.x - t * p.bpt) * (int)blockDim.x + (int)threadIdx.x;
+  const u32x4 d = v < p.V ? *reinterpret_cast<const u32x4*>(x + t * ld_bytes + (int64_t)v * 16) : u32x4{0, 0, 0, 0};
   const int n = p.topk + p.shared;
+  for (int j0 = 0; j0 < n; j0 += 64) {
+    const Pairs pairs(p, t, j0 + (int)(threadIdx.x & 63), n);
+    const int m = min(64, n - j0);
 #pragma unroll 4
-  for (int j = 0; j < n; ++j) {
-    const int r = row_of(p, t, j);
-    if (r >= 0) rows[r * p.V + v] = d;
+    for (int j = 0; j < m; ++j) {
+      const int r = pairs.row_at(j);
+      if (r >= 0 && v < p.V) rows[(int64_t)r * p.V + v] = d;
+    }
   }
 }
 
@@ -86,20 +115,45 @@ template <bool F32, bool OUT_F32>
 __global__ __launch_bounds__(256) void unpermute_kernel(KernelArgs p, const u32x4* __restrict__ rows,
                                                         void* __restrict__ out) {
   constexpr int N = Piece<F32>::N;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, t = i / p.V, v = i - t * p.V;
-  if (t >= p.T) return;
+  const int t = (int)(blockIdx.x / (unsigned)p.bpt);
+  const int v = ((int)blockIdx.x - t * p.bpt) * (int)blockDim.x + (int)threadIdx.x;
   float acc[N] = {};
   const int n = p.topk + p.shared;
-#pragma unroll 4
-  for (int j = 0; j < n; ++j) {
-    const int r = row_of(p, t, j);
-    if (r < 0) continue;
-    const float w = p.w && j < p.topk ? p.w[t * p.topk + j] : 1.0f;
-    float d[N];
-    Piece<F32>::unpack(rows[r * p.V + v], d);
+  for (int j0 = 0; j0 < n; j0 += 64) {
+    const Pairs pairs(p, t, j0 + (int)(threadIdx.x & 63), n);
+    // The pairs that have a row, in their order.  Their pieces are requested
+    // together (places past the last one: it once more), without branches
+    // between the loads, each of which would wait for the load before.
+    uint64_t left = __ballot(pairs.row >= 0);
+    auto batch = [&](auto size) {
+      constexpr int B = decltype(size)::value;
+      const int count = __popcll(left);
+      int j = 0, at[B];
+      u32x4 d[B];
 #pragma unroll
-    for (int k = 0; k < N; ++k) acc[k] = __builtin_fmaf(w, d[k], acc[k]);
+      for (int k = 0; k < B; ++k) {
+        if (left) j = __builtin_ctzll(left);
+        left &= left - 1;
+        at[k] = j;
+        d[k] = rows[(int64_t)pairs.row_at(j) * p.V + min(v, p.V - 1)];
+      }
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        if (k >= count) break;
+        const float w = pairs.w_at(at[k]);
+        float e[N];
+        Piece<F32>::unpack(d[k], e);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = __builtin_fmaf(w, e[i], acc[i]);
+      }
+    };
+    while (left) {
+      if (__popcll(left) > 4) batch(std::integral_constant<int, 8>());
+      else batch(std::integral_constant<int, 4>());
+    }
   }
+  if (v >= p.V) return;
+  const int64_t i = (int64_t)t * p.V + v;
   if constexpr (F32 == OUT_F32) {
     static_cast<u32x4*>(out)[i] = Piece<F32>::pack(acc);
   } else if constexpr (OUT_F32) {   // bf16 rows, float32 sums
@@ -118,25 +172,27 @@ template <bool F32, bool OUT_F32>
 __global__ __launch_bounds__(256) void unpermute_backward_kernel(KernelArgs p, const void* __restrict__ d_out,
                                                                  const u32x4* __restrict__ rows,
                                                                  u32x4* __restrict__ d_rows, float* __restrict__ d_w,
-                                                                 int groups, int64_t blocks) {
+                                                                 int groups, unsigned blocks) {
   if (blockIdx.x >= blocks) return clear_tail(p, d_rows, blocks);
   constexpr int N = Piece<F32>::N;
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)(blockIdx.x / (8 * groups)) * 8 + blockIdx.x % 8;
-  const int j = blockIdx.x / 8 % groups * 4 + (threadIdx.x >> 6), n = p.topk + p.shared;
+  const int t = (int)(blockIdx.x / (8u * groups)) * 8 + (int)(blockIdx.x % 8);
+  const int j = __builtin_amdgcn_readfirstlane((int)(blockIdx.x / 8 % groups * 4 + (threadIdx.x >> 6)));
+  const int n = p.topk + p.shared;
   if (t >= p.T || j >= n) return;
   const int r = row_of(p, t, j);
   const bool weighted = p.w && j < p.topk;
   float dot = 0.0f;
   if (r >= 0) {
-    const float w = weighted ? p.w[t * p.topk + j] : 1.0f;
+    const float w = weighted ? ld_uniform(p.w + (int64_t)t * p.topk + j) : 1.0f;
+    const int64_t at_r = (int64_t)r * p.V, at_d = (int64_t)t * p.V;
 #pragma unroll 4
-    for (int64_t v = lane; v < p.V; v += 64) {
+    for (int v = lane; v < p.V; v += 64) {
       float d[N], x[N];
       if constexpr (F32 == OUT_F32) {
-        Piece<F32>::unpack(static_cast<const u32x4*>(d_out)[t * p.V + v], d);
+        Piece<F32>::unpack(static_cast<const u32x4*>(d_out)[at_d + v], d);
       } else if constexpr (OUT_F32) {
-        const f32x4* at = static_cast<const f32x4*>(d_out) + 2 * (t * p.V + v);
+        const f32x4* at = static_cast<const f32x4*>(d_out) + 2 * (at_d + v);
         const f32x4 a = at[0], b = at[1];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -144,7 +200,7 @@ __global__ __launch_bounds__(256) void unpermute_backward_kernel(KernelArgs p, c
           d[4 + k] = b[k];
         }
       } else {
-        const u32x2 a = static_cast<const u32x2*>(d_out)[t * p.V + v];
+        const u32x2 a = static_cast<const u32x2*>(d_out)[at_d + v];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           d[2 * k] = bf16_bits_to_f32(a[k] & 0xFFFFu);
@@ -152,48 +208,54 @@ __global__ __launch_bounds__(256) void unpermute_backward_kernel(KernelArgs p, c
         }
       }
       if (d_w) {
-        Piece<F32>::unpack(rows[r * p.V + v], x);
+        Piece<F32>::unpack(rows[at_r + v], x);
 #pragma unroll
         for (int k = 0; k < N; ++k) dot = __builtin_fmaf(d[k], x[k], dot);
       }
 #pragma unroll
       for (int k = 0; k < N; ++k) d[k] *= w;
-      if (d_rows) d_rows[r * p.V + v] = Piece<F32>::pack(d);
+      if (d_rows) d_rows[at_r + v] = Piece<F32>::pack(d);
     }
   }
   if (d_w && j < p.topk) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off);
-    if (lane == 0) d_w[t * p.topk + j] = dot;
+    if (lane == 0) d_w[(int64_t)t * p.topk + j] = dot;
   }
 }
 
 KernelArgs kernel_args(const PermuteArgs& a, bool f32) {
-  return KernelArgs{a.T, a.topk, a.shared, a.T * (a.topk + a.shared), a.W / (f32 ? 4 : 8), a.offsets + a.slots,
-                    a.inv_pos, a.w};
+  return KernelArgs{a.T, a.topk, a.shared, a.T * (a.topk + a.shared), (int)(a.W / (f32 ? 4 : 8)), 1,
+                    a.offsets + a.slots, a.inv_pos, a.w};
 }
+// Threads of a workgroup that takes pieces of one token.
+int threads_for(int V) { return std::min(256, (V + 63) / 64 * 64); }
 // Workgroups that clear the tail: they leave at once where no pair was dropped.
-int64_t tail_blocks(const KernelArgs& k) { return std::min<int64_t>(1024, (k.P * k.V + 255) / 256); }
+int64_t tail_blocks(const KernelArgs& k) { return std::min<int64_t>(1024, ((int64_t)k.P * k.V + 255) / 256); }
 
 }  // namespace
 
 hipError_t launch_permute(const PermuteArgs& a, const void* x, bool f32, int64_t ldx, void* rows, bool zero_tail,
                           hipStream_t s) {
-  const KernelArgs k = kernel_args(a, f32);
-  const int64_t blocks = (k.T * k.V + 255) / 256;
-  permute_kernel<<<(unsigned)(blocks + (zero_tail ? tail_blocks(k) : 0)), 256, 0, s>>>(
-      k, static_cast<const uint8_t*>(x), ldx * (f32 ? 4 : 2), static_cast<u32x4*>(rows), blocks);
+  KernelArgs k = kernel_args(a, f32);
+  const int threads = threads_for(k.V);
+  k.bpt = (k.V + threads - 1) / threads;
+  const int64_t blocks = (int64_t)k.T * k.bpt;
+  permute_kernel<<<(unsigned)(blocks + (zero_tail ? tail_blocks(k) : 0)), threads, 0, s>>>(
+      k, static_cast<const uint8_t*>(x), ldx * (f32 ? 4 : 2), static_cast<u32x4*>(rows), (unsigned)blocks);
   return hipGetLastError();
 }
 
 hipError_t launch_unpermute(const PermuteArgs& a, const void* rows, bool f32, void* out, bool out_f32, hipStream_t s) {
-  const KernelArgs k = kernel_args(a, f32);
-  const unsigned blocks = (unsigned)((k.T * k.V + 255) / 256);
+  KernelArgs k = kernel_args(a, f32);
+  const int threads = threads_for(k.V);
+  k.bpt = (k.V + threads - 1) / threads;
+  const unsigned blocks = (unsigned)((int64_t)k.T * k.bpt);
   const u32x4* r = static_cast<const u32x4*>(rows);
-  if (f32 && out_f32) unpermute_kernel<true, true><<<blocks, 256, 0, s>>>(k, r, out);
-  else if (f32) unpermute_kernel<true, false><<<blocks, 256, 0, s>>>(k, r, out);
-  else if (out_f32) unpermute_kernel<false, true><<<blocks, 256, 0, s>>>(k, r, out);
-  else unpermute_kernel<false, false><<<blocks, 256, 0, s>>>(k, r, out);
+  if (f32 && out_f32) unpermute_kernel<true, true><<<blocks, threads, 0, s>>>(k, r, out);
+  else if (f32) unpermute_kernel<true, false><<<blocks, threads, 0, s>>>(k, r, out);
+  else if (out_f32) unpermute_kernel<false, true><<<blocks, threads, 0, s>>>(k, r, out);
+  else unpermute_kernel<false, false><<<blocks, threads, 0, s>>>(k, r, out);
   return hipGetLastError();
 }
 
@@ -205,10 +267,10 @@ hipError_t launch_unpermute_backward(const PermuteArgs& a, const void* d_out, bo
   const unsigned grid = (unsigned)(blocks + (zero_tail && d_rows ? tail_blocks(k) : 0));
   const u32x4* r = static_cast<const u32x4*>(rows);
   u32x4* d = static_cast<u32x4*>(d_rows);
-  if (f32 && out_f32) unpermute_backward_kernel<true, true><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, blocks);
-  else if (f32) unpermute_backward_kernel<true, false><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, blocks);
-  else if (out_f32) unpermute_backward_kernel<false, true><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, blocks);
-  else unpermute_backward_kernel<false, false><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, blocks);
+  if (f32 && out_f32) unpermute_backward_kernel<true, true><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, (unsigned)blocks);
+  else if (f32) unpermute_backward_kernel<true, false><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, (unsigned)blocks);
+  else if (out_f32) unpermute_backward_kernel<false, true><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, (unsigned)blocks);
+  else unpermute_backward_kernel<false, false><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, (unsigned)blocks);
   return hipGetLastError();
 }
 

@@ -62,7 +62,8 @@ def _check(n, h, w, eps, rows=slice(None)):
 
 
 SIZES = [(1, 8), (1, 64), (5, 512), (5, 520), (2, 2048), (7, 2056), (3, 4096), (2, 4104), (3, 8192), (2, 8200),
-         (2, 16384), (1, 16392), (2, 32768), (300, 1032)]
+         (2, 16384), (1, 16392), (2, 24584), (2, 32768), (300, 1032),
+         (1500, 64), (1501, 1032), (1100, 2056), (1030, 4104), (1025, 8200), (1027, 20488)]
 
 
 @pytest.mark.parametrize("T,H", SIZES)
