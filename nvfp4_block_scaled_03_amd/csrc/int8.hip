@@ -52,7 +52,8 @@ __global__ __launch_bounds__(256) void int8_prep_kernel(int64_t N, int64_t K, bo
 // A handful of rows: 16 MT rows x 16 NT columns a workgroup, whose KW wavefronts
 // split K.  Both operands come straight from memory into registers, the next
 // chunk's while the present one is multiplied; the partial sums meet in LDS and
-// leave in whole rows.
+// leave in whole rows.  The weights, read once, pass the caches by (34816 x 5120, M =
+// 1: 32.7 -> 30.1 us, 5.9 TB/s).
 // ---------------------------------------------------------------------------
 template <bool GATED, int MT, int NT, int KW>
 __global__ __launch_bounds__(KW * 64) void int8_few_kernel(Int8Args p) {
@@ -77,7 +78,8 @@ __global__ __launch_bounds__(KW * 64) void int8_few_kernel(Int8Args p) {
   };
   auto load = [&](int c, Chunk& d) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) d.w[j] = *reinterpret_cast<const i32x4*>(wq + ((int64_t)j * KC + c) * 1024);
+    for (int j = 0; j < NT; ++j)
+      d.w[j] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wq + ((int64_t)j * KC + c) * 1024));
     // (past K the weights are zeros: any 16 bytes of the row will do)
     const int k = min(c * 64 + lg * 16, p.K - 16);
 #pragma unroll
@@ -159,7 +161,7 @@ hipError_t launch_few_t(const Int8Args& p, hipStream_t s) {
 // into distinct banks.  A stage's weights are whole operands as they lie.
 // ---------------------------------------------------------------------------
 constexpr int kMaxParts = 4;                          // of K
-constexpr int64_t kPartBytes = int64_t(16) << 20;     // their sums, at most
+constexpr int64_t kPartBytes = int64_t(64) << 20;     // their sums, at most
 
 // s_waitcnt immediate: at most n vector memory operations outstanding.
 constexpr int wait_loads(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
@@ -226,10 +228,17 @@ void int8_tile_kernel(Int8Args p, int nb0, int TNB, int S) {
     for (int q = 0; q < PA; ++q)
       asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(ra[q] + min(ua[q], last)), "s"(as),
                    "{m0}"(base + (wv * PA + q) * 1024) : "memory");
+    if (TMB == 1) {   // weights that are read once pass the caches by
 #pragma unroll
-    for (int q = 0; q < PB; ++q)
-      asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(vb[q]), "s"(ws),
-                   "{m0}"(base + LA * 1024 + (wv * PB + q) * 1024) : "memory");
+      for (int q = 0; q < PB; ++q)
+        asm volatile("global_load_lds_dwordx4 %0, %1 nt" : : "v"(vb[q]), "s"(ws),
+                     "{m0}"(base + LA * 1024 + (wv * PB + q) * 1024) : "memory");
+    } else {
+#pragma unroll
+      for (int q = 0; q < PB; ++q)
+        asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(vb[q]), "s"(ws),
+                     "{m0}"(base + LA * 1024 + (wv * PB + q) * 1024) : "memory");
+    }
   };
 
   i32x4 acc[TM][TN];
@@ -286,9 +295,9 @@ void int8_tile_kernel(Int8Args p, int nb0, int TNB, int S) {
 
   const int64_t m0 = (int64_t)mb * BM + wr * 16 * TM;
   if constexpr (SPLIT) {
-    // The part's sums, in streaming columns.
-    const int64_t NP = (int64_t)tiles * 16;
-    int* const at = p.part + (int64_t)part * p.M * NP + (int64_t)(nb * (BN / 16) + wc * TN) * 16 + ln;
+    // The part's sums, in the launch's streaming columns.
+    const int64_t NP = min((int64_t)(tiles - nb0 * (BN / 16)) * 16, (int64_t)TNB * BN);
+    int* const at = p.part + (int64_t)part * p.M * NP + (int64_t)((nb - nb0) * (BN / 16) + wc * TN) * 16 + ln;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       if (nb * (BN / 16) + wc * TN + j >= tiles) break;
@@ -331,13 +340,13 @@ void int8_tile_kernel(Int8Args p, int nb0, int TNB, int S) {
   }
 }
 
-// Adds the S parts of four output columns and finishes them.
+// Adds the S parts of four output columns and finishes them; the parts hold
+// the NP streaming columns from col0 on.
 template <bool GATED>
-__global__ __launch_bounds__(256) void int8_join_kernel(Int8Args p, int S) {
-  const int64_t n_out = GATED ? p.N / 2 : p.N, NP = int8_tiles(p.N, GATED) * 16;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = n_out / 4;
-  const int64_t row[1] = {i / quads}, col = (i - row[0] * quads) * 4;
-  if (row[0] >= p.M) return;
+__global__ __launch_bounds__(256) void int8_join_kernel(Int8Args p, int S, int64_t col0, int64_t NP) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = (GATED ? NP / 2 : NP) / 4;
+  const int64_t row[1] = {i / quads}, c = (i - row[0] * quads) * 4, col = (GATED ? col0 / 2 : col0) + c;
+  if (row[0] >= p.M || col >= (GATED ? p.N / 2 : p.N)) return;
   EpiIn<1> in;
   epi_request<GATED>(p.ep, row[0], col, in);
   const float sx = p.sx[row[0]];
@@ -347,14 +356,13 @@ __global__ __launch_bounds__(256) void int8_join_kernel(Int8Args p, int S) {
     return f32x4{(float)v[0] * (sx * sw[0]), (float)v[1] * (sx * sw[1]), (float)v[2] * (sx * sw[2]),
                  (float)v[3] * (sx * sw[3])};
   };
-  const int64_t src = GATED ? (col >> 4) * 32 + (col & 15) : col;
+  const int64_t src = GATED ? (c >> 4) * 32 + (c & 15) : c;
   const f32x4 v = sum(src, p.sw + col), up[1] = {GATED ? sum(src + 16, p.sw + p.ep.half + col) : v};
   float z[4] = {v[0], v[1], v[2], v[3]};
   epi_finish<GATED, 1>(p.ep, z, up, in, row, col);
 }
 
-// Column blocks nb0 .. nb0 + nbs - 1 of 16 TN WC columns; K in S parts (SPLIT:
-// of all columns).
+// Column blocks nb0 .. nb0 + nbs - 1 of 16 TN WC columns; K in S parts (SPLIT).
 template <bool GATED, bool SPLIT, int WR, int WC, int TM, int TN, int D, int OCC>
 hipError_t launch_tile_t(const Int8Args& p, int nb0, int nbs, int S, hipStream_t s) {
   S = std::min(S, (int)int8_chunks(p.K) / 2);   // (a stage or more in every part)
@@ -363,8 +371,10 @@ hipError_t launch_tile_t(const Int8Args& p, int nb0, int nbs, int S, hipStream_t
       <<<(unsigned)((rb * nbs * S + 7) / 8 * 8), WR * WC * 64, 0, s>>>(p, nb0, nbs, S);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !SPLIT) return e;
-  const int64_t quads = (int64_t)p.M * (GATED ? p.N / 2 : p.N) / 4;
-  int8_join_kernel<GATED><<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(p, S);
+  const int64_t col0 = (int64_t)nb0 * 16 * TN * WC;
+  const int64_t NP = std::min(int8_tiles(p.N, GATED) * 16 - col0, (int64_t)nbs * 16 * TN * WC);
+  const int64_t quads = p.M * ((GATED ? NP / 2 : NP) / 4);
+  int8_join_kernel<GATED><<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(p, S, col0, NP);
   return hipGetLastError();
 }
 
@@ -374,22 +384,23 @@ hipError_t launch_tile_t(const Int8Args& p, int nb0, int nbs, int S, hipStream_t
 //   a + (u / 2) (f2 + b2 stages) + (u % 2) (f1 + b1 stages)     (occ 1: u (f1 + b1 stages))
 // with stages of 128 k; a K in S parts divides the stages, multiplies the tiles
 // and costs a launch and the sums' way through memory, 2.4 + 4 S M N / 2.2e6.  No
-// kernel is faster than its weights come: 3 + N K / 5.0e6.  Fitted to 1600
-// timings in graphs of 11 weights from 2048 x 512 to 34816 x 5120 with M = 16 ..
-// 4096; the choice by it is 1 % slower than the best one on average, 15 % at most.
+// kernel is faster than its weights come: 3 + N K / 5.0e6, a quarter more for
+// every further row block that reads them again.  Fitted to 2400 timings in
+// graphs of 12 weights from 2048 x 512 to 34816 x 5120 with M = 16 .. 4096; the
+// choice by it is 1 % slower than the best one on average, 18 % at most.
 // E.g. (us, 16 / 32 / 64 / 128 x 64, 256 x 128, 256 x 256): 4096 x 4096 M = 32
 // 9.3 / 10.6 / 11.4 / 15.5 / - / -, M = 512 42 / 26.5 / 18.9 / 17.7 / 30.5 / 54,
 // M = 4096 - / - / - / 102 / 76 / 65; K in 1 / 2 / 4 parts: 5120 x 17408 M = 16
 // 30.2 / 22.3 / 25.8 (16 x 64), M = 128 60.6 / 37.5 / 40.1 (128 x 64).
 // ---------------------------------------------------------------------------
 struct TileCost {
-  int bm, bn, occ, max_parts;
+  int bm, bn, occ;
   float a, f1, b1, f2, b2;
 };
 constexpr TileCost kTiles[] = {
-    {16, 64, 2, kMaxParts, 2.4f, 0.90f, 0.175f, 1.38f, 0.277f}, {32, 64, 2, kMaxParts, 2.6f, 0.64f, 0.217f, 1.33f, 0.318f},
-    {64, 64, 2, kMaxParts, 2.8f, 1.07f, 0.240f, 2.33f, 0.415f}, {128, 64, 2, kMaxParts, 3.0f, 1.70f, 0.367f, 3.25f, 0.657f},
-    {256, 128, 1, 1, 1.5f, 6.93f, 0.722f, 0.0f, 0.0f},          {256, 256, 1, 1, 1.5f, 11.7f, 1.283f, 0.0f, 0.0f},
+    {16, 64, 2, 2.4f, 0.90f, 0.175f, 1.38f, 0.277f}, {32, 64, 2, 2.6f, 0.64f, 0.217f, 1.33f, 0.318f},
+    {64, 64, 2, 2.8f, 1.07f, 0.240f, 2.33f, 0.415f}, {128, 64, 2, 3.0f, 1.70f, 0.367f, 3.25f, 0.657f},
+    {256, 128, 1, 1.5f, 6.93f, 0.722f, 0.0f, 0.0f},          {256, 256, 1, 1.5f, 11.7f, 1.283f, 0.0f, 0.0f},
 };
 constexpr int kTileKinds = sizeof(kTiles) / sizeof(kTiles[0]);
 
@@ -398,7 +409,7 @@ float tile_cost(const TileCost& t, int64_t M, int64_t columns, int64_t K, int S)
   const float st = (float)(((K + 127) / 128 + S - 1) / S), n2 = (float)(u / t.occ), n1 = (float)(u % t.occ);
   float c = t.a + (t.occ == 1 ? n2 * (t.f1 + t.b1 * st) : n2 * (t.f2 + t.b2 * st) + n1 * (t.f1 + t.b1 * st));
   if (S > 1) c += 2.4f + 4.0f * S * M * columns / 2.2e6f;
-  return std::max(c, 3.0f + (float)columns * K / 5.0e6f);
+  return std::max(c, 3.0f + (float)columns * K / 5.0e6f * (0.75f + 0.25f * ((M + t.bm - 1) / t.bm)));
 }
 
 struct Choice {
@@ -406,10 +417,10 @@ struct Choice {
   float cost;
 };
 // The fastest kind for `columns` streaming columns.
-Choice choose(int64_t M, int64_t columns, int64_t K, int max_parts) {
+Choice choose(int64_t M, int64_t columns, int64_t K) {
   Choice best = {0, 1, 3.0e38f};
   for (int kind = 0; kind < kTileKinds; ++kind)
-    for (int S = 1; S <= std::min(max_parts, kTiles[kind].max_parts); S *= 2) {
+    for (int S = 1; S <= kMaxParts; ++S) {
       if (S > 1 && (S > (K + 127) / 128 || (int64_t)S * M * columns * 4 > kPartBytes)) break;
       const float c = tile_cost(kTiles[kind], M, columns, K, S);
       if (c < best.cost) best = {kind, S, c};
@@ -433,8 +444,12 @@ hipError_t launch_kind(const Int8Args& p, int kind, int parts, int64_t col0, int
     case 3:
       return parts > 1 ? launch_tile_t<GATED, true, 2, 2, 4, 2, 3, 2>(p, nb0, nbs, parts, s)
                        : launch_tile_t<GATED, false, 2, 2, 4, 2, 3, 2>(p, nb0, nbs, 1, s);
-    case 4: return launch_tile_t<GATED, false, 4, 2, 4, 4, 3, 1>(p, nb0, nbs, 1, s);
-    default: return launch_tile_t<GATED, false, 2, 4, 8, 4, 2, 1>(p, nb0, nbs, 1, s);
+    case 4:
+      return parts > 1 ? launch_tile_t<GATED, true, 4, 2, 4, 4, 3, 1>(p, nb0, nbs, parts, s)
+                       : launch_tile_t<GATED, false, 4, 2, 4, 4, 3, 1>(p, nb0, nbs, 1, s);
+    default:
+      return parts > 1 ? launch_tile_t<GATED, true, 2, 4, 8, 4, 2, 1>(p, nb0, nbs, parts, s)
+                       : launch_tile_t<GATED, false, 2, 4, 8, 4, 2, 1>(p, nb0, nbs, 1, s);
   }
 }
 
@@ -445,16 +460,16 @@ hipError_t launch_chosen(const Int8Args& p, hipStream_t s) {
   // 5120 8.7 / 10.3, 8.7 / 10.9, 10.1 / 11.5; 16384 x 2048 10.3 / 9.0, 10.8 / 8.8).
   if (p.M <= 8) return launch_few_t<GATED, 1, 2, 8>(p, s);
   const int64_t columns = int8_tiles(p.N, GATED) * 16;
-  const Choice one = choose(p.M, columns, p.K, kMaxParts);
+  const Choice one = choose(p.M, columns, p.K);
   // Whole rounds of 256 x 256 tiles, and the columns left over by another kernel
   // (4096 x 5120 x 17408: 393 us in 256 x 256 tiles, 347 in 256 x 128).
   const int64_t rb = (p.M + 255) / 256, cb = (columns + 255) / 256, whole = rb * cb / 256 * 256 / rb;
   if (whole > 0 && whole < cb) {
     const int64_t rest = columns - whole * 256;
-    const Choice two = choose(p.M, rest, p.K, 1);
+    const Choice two = choose(p.M, rest, p.K);
     if (tile_cost(kTiles[kTileKinds - 1], p.M, whole * 256, p.K, 1) + two.cost < one.cost) {
       const hipError_t e = launch_kind<GATED>(p, kTileKinds - 1, 1, 0, whole * 256, s);
-      return e != hipSuccess ? e : launch_kind<GATED>(p, two.kind, 1, whole * 256, rest, s);
+      return e != hipSuccess ? e : launch_kind<GATED>(p, two.kind, two.parts, whole * 256, rest, s);
     }
   }
   return launch_kind<GATED>(p, one.kind, one.parts, 0, columns, s);

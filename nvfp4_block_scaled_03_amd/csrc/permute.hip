@@ -45,6 +45,28 @@ struct Piece {
   }
 };
 
+// Rows that the last-level cache (256 MB) cannot hold pass it by (NT): nothing of
+// them would be left for their reader, and the lines that writes leave dirty
+// delay the reads behind them (8192 x 8 rows of 4 KiB there and back 138 -> 105 us;
+// rows that fit are read again from the cache: 4095 x 8 rows of 8 KiB, an eighth
+// of them kept, 13.7 us, 20.9 past it).
+constexpr int64_t kCacheBytes = int64_t(256) << 20;
+template <class Body>
+__device__ __forceinline__ void by_size(int kept, int V, const Body& body) {
+  if ((int64_t)kept * V * 16 >= kCacheBytes) body(std::true_type());
+  else body(std::false_type());
+}
+template <bool NT>
+__device__ __forceinline__ u32x4 load_row(const u32x4* at) {
+  if constexpr (NT) return __builtin_nontemporal_load(at);
+  else return *at;
+}
+template <bool NT>
+__device__ __forceinline__ void store_row(u32x4* at, const u32x4& v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, at);
+  else *at = v;
+}
+
 struct KernelArgs {
   int T, topk, shared, P;
   int V;                    // pieces of a row
@@ -61,9 +83,12 @@ __device__ __forceinline__ int row_of(const KernelArgs& p, int t, int j) {
   return (unsigned)r < (unsigned)p.P ? r : -1;
 }
 
+// Rows of pairs.
+__device__ __forceinline__ int kept_rows(const KernelArgs& p) { return min(max(ld_uniform(p.kept), 0), p.P); }
+
 // Workgroups from `first` on clear the rows behind the last kept one.
 __device__ __forceinline__ void clear_tail(const KernelArgs& p, u32x4* rows, unsigned first) {
-  const int64_t from = (int64_t)min(max(*p.kept, 0), p.P) * p.V, to = (int64_t)p.P * p.V;
+  const int64_t from = (int64_t)kept_rows(p) * p.V, to = (int64_t)p.P * p.V;
   const int64_t step = (int64_t)(gridDim.x - first) * blockDim.x;
   for (int64_t i = from + (int64_t)(blockIdx.x - first) * blockDim.x + threadIdx.x; i < to; i += step)
     rows[i] = u32x4{0, 0, 0, 0};
@@ -99,15 +124,17 @@ __global__ __launch_bounds__(256) void permute_kernel(KernelArgs p, const uint8_
   const int v = ((int)blockIdx.x - t * p.bpt) * (int)blockDim.x + (int)threadIdx.x;
   const u32x4 d = v < p.V ? *reinterpret_cast<const u32x4*>(x + t * ld_bytes + (int64_t)v * 16) : u32x4{0, 0, 0, 0};
   const int n = p.topk + p.shared;
-  for (int j0 = 0; j0 < n; j0 += 64) {
-    const Pairs pairs(p, t, j0 + (int)(threadIdx.x & 63), n);
-    const int m = min(64, n - j0);
+  by_size(kept_rows(p), p.V, [&](auto nt) {
+    for (int j0 = 0; j0 < n; j0 += 64) {
+      const Pairs pairs(p, t, j0 + (int)(threadIdx.x & 63), n);
+      const int m = min(64, n - j0);
 #pragma unroll 4
-    for (int j = 0; j < m; ++j) {
-      const int r = pairs.row_at(j);
-      if (r >= 0 && v < p.V) rows[(int64_t)r * p.V + v] = d;
+      for (int j = 0; j < m; ++j) {
+        const int r = pairs.row_at(j);
+        if (r >= 0 && v < p.V) store_row<decltype(nt)::value>(rows + (int64_t)r * p.V + v, d);
+      }
     }
-  }
+  });
 }
 
 // A thread sums one piece over a token's rows.
@@ -119,39 +146,41 @@ __global__ __launch_bounds__(256) void unpermute_kernel(KernelArgs p, const u32x
   const int v = ((int)blockIdx.x - t * p.bpt) * (int)blockDim.x + (int)threadIdx.x;
   float acc[N] = {};
   const int n = p.topk + p.shared;
-  for (int j0 = 0; j0 < n; j0 += 64) {
-    const Pairs pairs(p, t, j0 + (int)(threadIdx.x & 63), n);
-    // The pairs that have a row, in their order.  Their pieces are requested
-    // together (places past the last one: it once more), without branches
-    // between the loads, each of which would wait for the load before.
-    uint64_t left = __ballot(pairs.row >= 0);
-    auto batch = [&](auto size) {
-      constexpr int B = decltype(size)::value;
-      const int count = __popcll(left);
-      int j = 0, at[B];
-      u32x4 d[B];
+  by_size(kept_rows(p), p.V, [&](auto nt) {
+    for (int j0 = 0; j0 < n; j0 += 64) {
+      const Pairs pairs(p, t, j0 + (int)(threadIdx.x & 63), n);
+      // The pairs that have a row, in their order.  Their pieces are requested
+      // together (places past the last one: it once more), without branches
+      // between the loads, each of which would wait for the load before.
+      uint64_t left = __ballot(pairs.row >= 0);
+      auto batch = [&](auto size) {
+        constexpr int B = decltype(size)::value;
+        const int count = __popcll(left);
+        int j = 0, at[B];
+        u32x4 d[B];
 #pragma unroll
-      for (int k = 0; k < B; ++k) {
-        if (left) j = __builtin_ctzll(left);
-        left &= left - 1;
-        at[k] = j;
-        d[k] = rows[(int64_t)pairs.row_at(j) * p.V + min(v, p.V - 1)];
+        for (int k = 0; k < B; ++k) {
+          if (left) j = __builtin_ctzll(left);
+          left &= left - 1;
+          at[k] = j;
+          d[k] = load_row<decltype(nt)::value>(rows + (int64_t)pairs.row_at(j) * p.V + min(v, p.V - 1));
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+          if (k >= count) break;
+          const float w = pairs.w_at(at[k]);
+          float e[N];
+          Piece<F32>::unpack(d[k], e);
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[i] = __builtin_fmaf(w, e[i], acc[i]);
+        }
+      };
+      while (left) {
+        if (__popcll(left) > 4) batch(std::integral_constant<int, 8>());
+        else batch(std::integral_constant<int, 4>());
       }
-#pragma unroll
-      for (int k = 0; k < B; ++k) {
-        if (k >= count) break;
-        const float w = pairs.w_at(at[k]);
-        float e[N];
-        Piece<F32>::unpack(d[k], e);
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = __builtin_fmaf(w, e[i], acc[i]);
-      }
-    };
-    while (left) {
-      if (__popcll(left) > 4) batch(std::integral_constant<int, 8>());
-      else batch(std::integral_constant<int, 4>());
     }
-  }
+  });
   if (v >= p.V) return;
   const int64_t i = (int64_t)t * p.V + v;
   if constexpr (F32 == OUT_F32) {
@@ -186,36 +215,38 @@ __global__ __launch_bounds__(256) void unpermute_backward_kernel(KernelArgs p, c
   if (r >= 0) {
     const float w = weighted ? ld_uniform(p.w + (int64_t)t * p.topk + j) : 1.0f;
     const int64_t at_r = (int64_t)r * p.V, at_d = (int64_t)t * p.V;
+    by_size(kept_rows(p), p.V, [&](auto nt) {
 #pragma unroll 4
-    for (int v = lane; v < p.V; v += 64) {
-      float d[N], x[N];
-      if constexpr (F32 == OUT_F32) {
-        Piece<F32>::unpack(static_cast<const u32x4*>(d_out)[at_d + v], d);
-      } else if constexpr (OUT_F32) {
-        const f32x4* at = static_cast<const f32x4*>(d_out) + 2 * (at_d + v);
-        const f32x4 a = at[0], b = at[1];
+      for (int v = lane; v < p.V; v += 64) {
+        float d[N], x[N];
+        if constexpr (F32 == OUT_F32) {
+          Piece<F32>::unpack(static_cast<const u32x4*>(d_out)[at_d + v], d);
+        } else if constexpr (OUT_F32) {
+          const f32x4* at = static_cast<const f32x4*>(d_out) + 2 * (at_d + v);
+          const f32x4 a = at[0], b = at[1];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          d[k] = a[k];
-          d[4 + k] = b[k];
+          for (int k = 0; k < 4; ++k) {
+            d[k] = a[k];
+            d[4 + k] = b[k];
+          }
+        } else {
+          const u32x2 a = static_cast<const u32x2*>(d_out)[at_d + v];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            d[2 * k] = bf16_bits_to_f32(a[k] & 0xFFFFu);
+            d[2 * k + 1] = __int_as_float((int)(a[k] & 0xFFFF0000u));
+          }
         }
-      } else {
-        const u32x2 a = static_cast<const u32x2*>(d_out)[at_d + v];
+        if (d_w) {
+          Piece<F32>::unpack(load_row<decltype(nt)::value>(rows + at_r + v), x);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          d[2 * k] = bf16_bits_to_f32(a[k] & 0xFFFFu);
-          d[2 * k + 1] = __int_as_float((int)(a[k] & 0xFFFF0000u));
+          for (int k = 0; k < N; ++k) dot = __builtin_fmaf(d[k], x[k], dot);
         }
-      }
-      if (d_w) {
-        Piece<F32>::unpack(rows[at_r + v], x);
 #pragma unroll
-        for (int k = 0; k < N; ++k) dot = __builtin_fmaf(d[k], x[k], dot);
+        for (int k = 0; k < N; ++k) d[k] *= w;
+        if (d_rows) store_row<decltype(nt)::value>(d_rows + at_r + v, Piece<F32>::pack(d));
       }
-#pragma unroll
-      for (int k = 0; k < N; ++k) d[k] *= w;
-      if (d_rows) d_rows[at_r + v] = Piece<F32>::pack(d);
-    }
+    });
   }
   if (d_w && j < p.topk) {
 #pragma unroll
@@ -241,8 +272,11 @@ hipError_t launch_permute(const PermuteArgs& a, const void* x, bool f32, int64_t
   const int threads = threads_for(k.V);
   k.bpt = (k.V + threads - 1) / threads;
   const int64_t blocks = (int64_t)k.T * k.bpt;
-  permute_kernel<<<(unsigned)(blocks + (zero_tail ? tail_blocks(k) : 0)), threads, 0, s>>>(
-      k, static_cast<const uint8_t*>(x), ldx * (f32 ? 4 : 2), static_cast<u32x4*>(rows), (unsigned)blocks);
+  const unsigned grid = (unsigned)(blocks + (zero_tail ? tail_blocks(k) : 0));
+  const uint8_t* src = static_cast<const uint8_t*>(x);
+  const int64_t ld = ldx * (f32 ? 4 : 2);
+  u32x4* r = static_cast<u32x4*>(rows);
+  permute_kernel<<<grid, threads, 0, s>>>(k, src, ld, r, (unsigned)blocks);
   return hipGetLastError();
 }
 
@@ -267,10 +301,11 @@ hipError_t launch_unpermute_backward(const PermuteArgs& a, const void* d_out, bo
   const unsigned grid = (unsigned)(blocks + (zero_tail && d_rows ? tail_blocks(k) : 0));
   const u32x4* r = static_cast<const u32x4*>(rows);
   u32x4* d = static_cast<u32x4*>(d_rows);
-  if (f32 && out_f32) unpermute_backward_kernel<true, true><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, (unsigned)blocks);
-  else if (f32) unpermute_backward_kernel<true, false><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, (unsigned)blocks);
-  else if (out_f32) unpermute_backward_kernel<false, true><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, (unsigned)blocks);
-  else unpermute_backward_kernel<false, false><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, (unsigned)blocks);
+  const unsigned n = (unsigned)blocks;
+  if (f32 && out_f32) unpermute_backward_kernel<true, true><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, n);
+  else if (f32) unpermute_backward_kernel<true, false><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, n);
+  else if (out_f32) unpermute_backward_kernel<false, true><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, n);
+  else unpermute_backward_kernel<false, false><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, n);
   return hipGetLastError();
 }
 
