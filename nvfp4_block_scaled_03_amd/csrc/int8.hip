@@ -383,24 +383,28 @@ hipError_t launch_tile_t(const Int8Args& p, int nb0, int nbs, int S, hipStream_t
 // u = ceil(tiles / 256) of them, `occ` at a time,
 //   a + (u / 2) (f2 + b2 stages) + (u % 2) (f1 + b1 stages)     (occ 1: u (f1 + b1 stages))
 // with stages of 128 k; a K in S parts divides the stages, multiplies the tiles
-// and costs a launch and the sums' way through memory, 2.4 + 4 S M N / 2.2e6.  No
-// kernel is faster than its weights come: 3 + N K / 5.0e6, a quarter more for
-// every further row block that reads them again.  Fitted to 2400 timings in
-// graphs of 12 weights from 2048 x 512 to 34816 x 5120 with M = 16 .. 4096; the
-// choice by it is 1 % slower than the best one on average, 18 % at most.
-// E.g. (us, 16 / 32 / 64 / 128 x 64, 256 x 128, 256 x 256): 4096 x 4096 M = 32
-// 9.3 / 10.6 / 11.4 / 15.5 / - / -, M = 512 42 / 26.5 / 18.9 / 17.7 / 30.5 / 54,
-// M = 4096 - / - / - / 102 / 76 / 65; K in 1 / 2 / 4 parts: 5120 x 17408 M = 16
-// 30.2 / 22.3 / 25.8 (16 x 64), M = 128 60.6 / 37.5 / 40.1 (128 x 64).
+// and costs a launch and the sums' way through memory, 2.4 + 4 S M N / 2.2e6.  The
+// weights come from memory meanwhile, N K / 6.0e6, 15 % more for every further row
+// block that reads them again: the longer of the two, and a fifth of the shorter.
+// Fitted to 3600 timings in graphs of 12 weights from 2048 x 512 to 65536 x 8192
+// with M = 16 .. 4096; the choice by it is 1 % slower than the best one on average,
+// 21 % at most.  E.g. (us, 16 / 32 / 64 / 128 x 64, 256 x 128, 256 x 256): 4096 x
+// 4096 M = 32 9.3 / 10.6 / 11.4 / 15.5 / - / -, M = 512 42 / 26.5 / 18.9 / 17.7 /
+// 30.5 / 54, M = 4096 - / - / - / 102 / 76 / 65; 128 x 64 or 64 x 64 against 128 x 256
+// or 64 x 256: 34816 x 5120 M = 64 44.6 / 40.9, M = 128 59.9 / 48.2, M = 384 92.8 /
+// 87.5; K in 1 / 2 / 4 parts: 5120 x 17408 M = 16 30.2 / 22.3 / 25.8 (16 x 64), M =
+// 128 60.6 / 37.5 / 40.1 (128 x 64), and M = 384 62.6 in 256 x 128 tiles, 46.3 in 128
+// x 256 with 4 parts.
 // ---------------------------------------------------------------------------
 struct TileCost {
   int bm, bn, occ;
   float a, f1, b1, f2, b2;
 };
 constexpr TileCost kTiles[] = {
-    {16, 64, 2, 2.4f, 0.90f, 0.175f, 1.38f, 0.277f}, {32, 64, 2, 2.6f, 0.64f, 0.217f, 1.33f, 0.318f},
-    {64, 64, 2, 2.8f, 1.07f, 0.240f, 2.33f, 0.415f}, {128, 64, 2, 3.0f, 1.70f, 0.367f, 3.25f, 0.657f},
-    {256, 128, 1, 1.5f, 6.93f, 0.722f, 0.0f, 0.0f},          {256, 256, 1, 1.5f, 11.7f, 1.283f, 0.0f, 0.0f},
+    {16, 64, 2, 2.7f, 0.65f, 0.165f, 1.45f, 0.247f},  {32, 64, 2, 3.26f, 0.0f, 0.204f, 0.87f, 0.296f},
+    {64, 64, 2, 3.5f, 0.25f, 0.233f, 1.21f, 0.398f},  {128, 64, 2, 3.5f, 0.82f, 0.349f, 1.09f, 0.632f},
+    {64, 256, 1, 3.5f, 0.80f, 0.615f, 0.0f, 0.0f},    {128, 256, 1, 1.44f, 3.67f, 0.729f, 0.0f, 0.0f},
+    {256, 128, 1, 1.0f, 6.79f, 0.697f, 0.0f, 0.0f},   {256, 256, 1, 1.0f, 10.8f, 1.248f, 0.0f, 0.0f},
 };
 constexpr int kTileKinds = sizeof(kTiles) / sizeof(kTiles[0]);
 
@@ -409,7 +413,8 @@ float tile_cost(const TileCost& t, int64_t M, int64_t columns, int64_t K, int S)
   const float st = (float)(((K + 127) / 128 + S - 1) / S), n2 = (float)(u / t.occ), n1 = (float)(u % t.occ);
   float c = t.a + (t.occ == 1 ? n2 * (t.f1 + t.b1 * st) : n2 * (t.f2 + t.b2 * st) + n1 * (t.f1 + t.b1 * st));
   if (S > 1) c += 2.4f + 4.0f * S * M * columns / 2.2e6f;
-  return std::max(c, 3.0f + (float)columns * K / 5.0e6f * (0.75f + 0.25f * ((M + t.bm - 1) / t.bm)));
+  const float m = (float)columns * K / 6.0e6f * (0.85f + 0.15f * ((M + t.bm - 1) / t.bm));
+  return std::max(c, 3.0f + m) + 0.2f * std::min(c, m);
 }
 
 struct Choice {
@@ -445,6 +450,12 @@ hipError_t launch_kind(const Int8Args& p, int kind, int parts, int64_t col0, int
       return parts > 1 ? launch_tile_t<GATED, true, 2, 2, 4, 2, 3, 2>(p, nb0, nbs, parts, s)
                        : launch_tile_t<GATED, false, 2, 2, 4, 2, 3, 2>(p, nb0, nbs, 1, s);
     case 4:
+      return parts > 1 ? launch_tile_t<GATED, true, 2, 4, 2, 4, 3, 1>(p, nb0, nbs, parts, s)
+                       : launch_tile_t<GATED, false, 2, 4, 2, 4, 3, 1>(p, nb0, nbs, 1, s);
+    case 5:
+      return parts > 1 ? launch_tile_t<GATED, true, 2, 4, 4, 4, 3, 1>(p, nb0, nbs, parts, s)
+                       : launch_tile_t<GATED, false, 2, 4, 4, 4, 3, 1>(p, nb0, nbs, 1, s);
+    case 6:
       return parts > 1 ? launch_tile_t<GATED, true, 4, 2, 4, 4, 3, 1>(p, nb0, nbs, parts, s)
                        : launch_tile_t<GATED, false, 4, 2, 4, 4, 3, 1>(p, nb0, nbs, 1, s);
     default:

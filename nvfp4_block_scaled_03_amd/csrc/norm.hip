@@ -318,7 +318,7 @@ hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
     if (V <= 512) return launch_rows_t<NORM, XF32, RES, 512, 1>(a, s);
     if (V <= 1024) return launch_rows_t<NORM, XF32, RES, 1024, 1>(a, s);
     if (V <= 2048) return launch_rows_t<NORM, XF32, RES, 1024, 2>(a, s);
-    if (V <= 3072) return launch_rows_t<NORM, XF32, RES, 1024, 3>(a, s);
+    if (V <= 3 * 1024) return launch_rows_t<NORM, XF32, RES, 1024, 3>(a, s);
     return launch_rows_t<NORM, XF32, RES, 512, 8>(a, s);
   }
   if (V <= 128) return launch_rows_t<NORM, XF32, RES, 64, 2>(a, s);

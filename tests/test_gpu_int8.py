@@ -156,6 +156,17 @@ def test_larger_layers(dev, M, N, K, cfg):
     assert got.shape == (M, N // 2 if gated else N)
 
 
+# every tile size, in one part and with K in parts
+@pytest.mark.parametrize("M,N,K", [(42, 104, 400), (16, 72, 2576), (61, 136, 128), (17, 2120, 4352), (51, 8648, 128),
+                                   (65, 1960, 4624), (65, 16168, 144), (72, 2952, 7440), (36, 34304, 144),
+                                   (40, 34824, 272), (17, 16616, 8064), (100, 34824, 272), (66, 18280, 4368),
+                                   (1240, 6472, 1536), (5780, 360, 6416), (964, 8552, 1680), (140, 17832, 14336)])
+@pytest.mark.parametrize("cfg", [CONFIGS[1], CONFIGS[5]], ids=["plain", "gated"])
+def test_tile_sizes(dev, M, N, K, cfg):
+    got = _rows_of_large(dev, M, N, K, cfg)
+    assert got.shape == (M, N // 2 if cfg[1] else N)
+
+
 def _rows_of_large(dev, M, N, K, cfg):
     """As _case, with the reference's product on the GPU in FP64 (exact)."""
     act, gated, with_bias, rt, ot = cfg
