@@ -607,11 +607,15 @@ def _no_gradient(name: str, *tensors):
                 raise ValueError(f"{name} has no gradient: call it under torch.no_grad()")
 
 
-def _rows8(t: torch.Tensor) -> bool:
-    """Whether the rows of t [rows, n] lie apart and can be read and written
-    eight elements at a time."""
-    return (t.stride(1) == 1 and t.data_ptr() % 16 == 0
-            and (t.shape[0] <= 1 or (t.stride(0) >= t.shape[1] and t.stride(0) % 8 == 0)))
+def _rows_at(t: torch.Tensor, unit: int = 8):
+    """(address, row stride) of t [rows, n] if its rows lie apart and can be read
+    and written ``unit`` elements at a time, else None."""
+    rows, n = t.shape
+    ld, step = t.stride()
+    at = t.data_ptr()
+    if rows <= 1:
+        ld = n
+    return None if step != 1 or at % 16 or ld < n or ld % unit else (at, ld)
 
 
 class NormOut(NamedTuple):
@@ -646,43 +650,50 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
         raise ValueError("x must be [T, H] and weight [H]")
     T, H = x.shape
     want_y, want_q = NORM_OUTPUTS[outputs]
-    a = RmsNormArgs(eps=eps, x_dtype=_dtype_code(x), w_dtype=_dtype_code(weight))
+    at_r = at_h = at_y = (None, 0)
+    r_type = y_type = 0
     if residual is not None:
         if residual.shape != (T, H):
             raise ValueError(f"residual must be [{T}, {H}]")
+        r_type = _dtype_code(residual)
         if h is None:
             h = torch.empty(T, H, dtype=residual.dtype, device=x.device)
-        elif h.shape != (T, H) or h.dtype != residual.dtype or not _rows8(h):
+            at_h = h.data_ptr(), H
+        elif h.shape != (T, H) or h.dtype != residual.dtype or (at_h := _rows_at(h)) is None:
             raise ValueError(f"h must be [{T}, {H}] in the residual's type, with rows of consecutive elements, 16-byte "
                              "aligned, strides multiples of 8")
-        a.residual_dtype = _dtype_code(residual)
-        if not _rows8(residual):
+        at_r = _rows_at(residual)
+        if at_r is None:
             residual = residual.clone(memory_format=torch.contiguous_format)
-        a.residual, a.ld_residual = residual.data_ptr(), _row_stride(residual)
-        a.h, a.ld_h = h.data_ptr(), _row_stride(h)
+            at_r = residual.data_ptr(), H
     elif h is not None:
         raise ValueError("h is made only with a residual")
-    if not _rows8(x):
+    at_x = _rows_at(x)
+    if at_x is None:
         x = x.clone(memory_format=torch.contiguous_format)
-    a.x, a.ldx = x.data_ptr(), _row_stride(x)
-    weight = weight.contiguous()
-    if weight.data_ptr() % 16:
-        weight = weight.clone()
-    a.weight = weight.data_ptr()
+        at_x = x.data_ptr(), H
+    at_w = weight.data_ptr()
+    if at_w % 16 or not weight.is_contiguous():
+        weight = weight.clone(memory_format=torch.contiguous_format)
+        at_w = weight.data_ptr()
     if want_y:
         if y is None:
             y = torch.empty(T, H, dtype=out_dtype, device=x.device)
-        elif y.shape != (T, H) or not _rows8(y):
+            at_y = y.data_ptr(), H
+        elif y.shape != (T, H) or (at_y := _rows_at(y)) is None:
             raise ValueError(f"y must be [{T}, {H}] with rows of consecutive elements, 16-byte aligned, strides multiples "
                              "of 8")
-        a.y, a.ld_y, a.y_dtype = y.data_ptr(), _row_stride(y), _dtype_code(y)
+        y_type = _dtype_code(y)
     elif y is not None:
         raise ValueError(f"y is not made with outputs={outputs!r}")
+    at_q = at_s = None
     if want_q:
         q, s = _int8_rows(T, H, x.device, q, s)
-        a.q, a.s = q.data_ptr(), s.data_ptr()
+        at_q, at_s = q.data_ptr(), s.data_ptr()
     elif q is not None or s is not None:
         raise ValueError(f"q and s are not made with outputs={outputs!r}")
+    a = RmsNormArgs(*at_x, *at_r, at_w, *at_h, *at_y, at_q, at_s, _dtype_code(x), r_type, _dtype_code(weight), y_type,
+                    eps)
     call("rms_norm", a, T, H, _raw_stream(dev))
     return NormOut(y, h, q, s)
 
@@ -710,11 +721,12 @@ def int8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional
     if x.dim() != 2:
         raise ValueError("x must be [rows, K]")
     rows, K = x.shape
-    if not _rows8(x):
+    at = _rows_at(x)
+    if at is None:
         x = x.clone(memory_format=torch.contiguous_format)
+        at = x.data_ptr(), K
     q, s = _int8_rows(rows, K, x.device, q, s)
-    call("int8_quantize", x.data_ptr(), _dtype_code(x), rows, K, _row_stride(x), q.data_ptr(), s.data_ptr(),
-         _raw_stream(dev))
+    call("int8_quantize", at[0], _dtype_code(x), rows, K, at[1], q.data_ptr(), s.data_ptr(), _raw_stream(dev))
     return q, s
 
 
@@ -781,9 +793,10 @@ def int8_linear(x: torch.Tensor, w: Int8LinearWeight, s: Optional[torch.Tensor] 
         s = s.contiguous()
     elif s is not None:
         raise ValueError("scales belong to int8 x")
-    unit = 16 if codes else 8
-    if x.stride(1) != 1 or x.data_ptr() % 16 or (M > 1 and (x.stride(0) < K or x.stride(0) % unit or x.stride(0) > 1 << 22)):
+    at_x = _rows_at(x, 16 if codes else 8)
+    if at_x is None or at_x[1] > 1 << 22:
         x = x.clone(memory_format=torch.contiguous_format)
+        at_x = x.data_ptr(), K
     if out is None:
         out = torch.empty(M, n_out, dtype=out_dtype, device=x.device)
     elif out.shape != (M, n_out) or not _rows4(out):
@@ -806,7 +819,7 @@ def int8_linear(x: torch.Tensor, w: Int8LinearWeight, s: Optional[torch.Tensor] 
     if ws is None:
         n = _lib.load().int8_linear_workspace_size(M, N, K, x_dtype)
         ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
-    call("int8_linear", x.data_ptr(), x_dtype, _row_stride(x), _ptr(s), M, N, K, w.prep.data_ptr(), w.s.data_ptr(), epi,
+    call("int8_linear", at_x[0], x_dtype, at_x[1], _ptr(s), M, N, K, w.prep.data_ptr(), w.s.data_ptr(), epi,
          out.data_ptr(), _dtype_code(out), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
          _raw_stream(dev))
     return out
@@ -822,9 +835,11 @@ def _permute(d: Dims, x, offsets, inv_pos, out):
     fresh = out is None
     if fresh:
         out = torch.empty(_pairs(d), W, dtype=x.dtype, device=x.device)
-    if not _rows8(x):
+    at = _rows_at(x)
+    if at is None:
         x = x.clone(memory_format=torch.contiguous_format)
-    call("moe_permute", d, x.data_ptr(), _dtype_code(x), W, _row_stride(x), offsets.data_ptr(), inv_pos.data_ptr(),
+        at = x.data_ptr(), W
+    call("moe_permute", d, at[0], _dtype_code(x), W, at[1], offsets.data_ptr(), inv_pos.data_ptr(),
          out.data_ptr(), int(fresh), _raw_stream(x.get_device()))
     return out
 
