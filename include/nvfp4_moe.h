@@ -477,8 +477,8 @@ int int8_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ldx
  *   epi: as for nvfp4_linear_fused (its gated is the weight's), or NULL: the
  *     product alone into contiguous out.
  * N a multiple of 4 (gated: of 8), at most 2^20; K a multiple of 16 below 131072
- * (so that no sum passes 31 bits), bfloat16 x at most 32768; ldx at most 2^22;
- * M <= 2^24, M N <= 2^40.  A row or column whose scale is NaN gives NaN.
+ * (so that no sum passes 31 bits), bfloat16 x at most 32768; N K <= 2^35; ldx at
+ * most 2^22; M <= 2^24, M N <= 2^40.  A row or column whose scale is NaN gives NaN.
  * ws: int8_linear_workspace_size(M, N, K, x_dtype) bytes, 256-byte aligned, no
  * initial contents; it serves every call of fewer rows, and bfloat16's serves
  * int8 codes too. */
@@ -508,7 +508,8 @@ int int8_linear(const void* x, int x_dtype, int64_t ldx, const float* sx, int64_
  * topk_w NULL.  x [T][ldx], rows and d_rows [P][width], out and d_out [T][width],
  * bfloat16 or float32 (rows, d_rows in dtype; out, d_out in out_dtype), 16-byte
  * aligned; width a multiple of 8, at most 2^20, ldx >= width a multiple of 8,
- * T width <= 2^40.  Rows behind the last kept one (expert_offsets[E + shared]) are
+ * T width <= 2^40 and T rows, each in whole KiB (past 4 KiB: in whole 4 KiB), below
+ * 64 GiB - 4 MiB.  Rows behind the last kept one (expert_offsets[E + shared]) are
  * cleared with zero_tail and left as they were without.  No output may overlap an input. */
 int moe_permute(const nvfp4_moe_dims* dims, const void* x, int dtype, int64_t width, int64_t ldx,
                 const int32_t* expert_offsets, const int32_t* inv_pos, void* rows, int zero_tail, void* stream);

@@ -1079,7 +1079,7 @@ namespace {
 // |sum| <= 128 * 128 K < 2^31; rows of codes in whole 16-byte units.
 bool int8_weight_ok(int64_t N, int64_t K, int gated) {
   return (gated == 0 || gated == 1) && N >= 1 && N <= (int64_t(1) << 20) && N % (gated ? 8 : 4) == 0 && K >= 16 &&
-         K % 16 == 0 && K < 131072;
+         K % 16 == 0 && K < 131072 && N * K <= (int64_t(1) << 35);
 }
 bool int8_shape_ok(int64_t M, int64_t N, int64_t K, int x_dtype, int gated) {
   return int8_weight_ok(N, K, gated) && M >= 0 && M <= (int64_t(1) << 24) && M * N <= (int64_t(1) << 40) &&
@@ -1097,7 +1097,7 @@ int int8_prep_weights(int64_t N, int64_t K, int gated, const int8_t* q, uint8_t*
   const char* W = "int8_prep_weights";
   if (!int8_weight_ok(N, K, gated))
     return fail(NVFP4_ESHAPE, "%s: ESHAPE N=%lld K=%lld gated=%d (N a multiple of 4, gated of 8, at most 2^20; K a multiple "
-                "of 16 below 131072)", W, (long long)N, (long long)K, gated);
+                "of 16 below 131072; N K <= 2^35)", W, (long long)N, (long long)K, gated);
   if (!q || !prep) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
   if (!aligned(q, 16) || !aligned(prep, 16))
     return fail(NVFP4_EINVAL, "%s: EINVAL q and prep must be 16-byte aligned", W);
@@ -1122,7 +1122,7 @@ int int8_linear(const void* x, int x_dtype, int64_t ldx, const float* sx, int64_
   if (!int8_shape_ok(M, N, K, x_dtype, e->gated) || ldx < K || ldx % unit ||
       ldx > (int64_t(1) << 22))
     return fail(NVFP4_ESHAPE, "%s: ESHAPE M=%lld N=%lld K=%lld ldx=%lld gated=%d (N a multiple of 4, gated of 8, at most "
-                "2^20; K a multiple of 16 below 131072, bfloat16 x: at most %d; M <= 2^24, M N <= 2^40; ldx >= K a multiple "
+                "2^20; K a multiple of 16 below 131072, bfloat16 x: at most %d; N K <= 2^35; M <= 2^24, M N <= 2^40; ldx >= K a multiple "
                 "of %d, at most 2^22)", W, (long long)M, (long long)N, (long long)K, (long long)ldx, e->gated, nvfp4::kNormMaxH, (int)unit);
   nvfp4::Int8Args a{};
   if (int r = check_epilogue(W, e, M, N, K, out, out_dtype, &a.ep, 8)) return r;
@@ -1160,13 +1160,18 @@ int int8_linear(const void* x, int x_dtype, int64_t ldx, const float* sx, int64_
 // ------------------------------------------------------------------ rows by expert
 namespace {
 // Dimensions of the permutation, and rows of W elements.
-int check_permute(const char* W, const nvfp4_moe_dims* d, int64_t width, nvfp4::PermuteArgs* k) {
+int check_permute(const char* W, const nvfp4_moe_dims* d, int64_t width, int dtype, nvfp4::PermuteArgs* k) {
   if (!d) return fail(NVFP4_EINVAL, "%s: EINVAL dims is NULL", W);
   nvfp4_moe_dims any = *d;   // H and I play no part: rows have a width of their own
   any.H = any.I = 128;
   if (int r = check_dims(&any, W)) return r;
   if (width < 8 || width % 8 || width > (int64_t(1) << 20) || d->T * (width / 4) > (int64_t(1) << 38))
     return fail(NVFP4_ESHAPE, "%s: ESHAPE width=%lld (a multiple of 8, at most 2^20; T width <= 2^40)", W, (long long)width);
+  // A thread per 16-byte piece of a token's row, in whole wavefronts up to four,
+  // in whole fours beyond; a launch has fewer than 2^32.
+  const int64_t pieces = width / (dtype == NVFP4_F32 ? 4 : 8), unit = pieces <= 256 ? 64 : 256;
+  if (d->T * ((pieces + unit - 1) / unit * unit) >= (int64_t(1) << 32) - (1 << 18))
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE T=%d width=%lld (T rows must stay below 64 GiB)", W, d->T, (long long)width);
   k->T = d->T;
   k->topk = d->topk;
   k->shared = d->shared;
@@ -1180,7 +1185,7 @@ int moe_permute(const nvfp4_moe_dims* d, const void* x, int dtype, int64_t width
                 const int32_t* expert_offsets, const int32_t* inv_pos, void* rows, int zero_tail, void* stream) {
   const char* W = "moe_permute";
   nvfp4::PermuteArgs k{};
-  if (int r = check_permute(W, d, width, &k)) return r;
+  if (int r = check_permute(W, d, width, dtype, &k)) return r;
   if (dtype != NVFP4_BF16 && dtype != NVFP4_F32) return fail(NVFP4_EINVAL, "%s: EINVAL dtype=%d", W, dtype);
   if (ldx < width || ldx % 8)
     return fail(NVFP4_ESHAPE, "%s: ESHAPE width=%lld ldx=%lld (ldx at least the width, a multiple of 8)", W,
@@ -1198,7 +1203,7 @@ int moe_unpermute(const nvfp4_moe_dims* d, const void* rows, int dtype, int64_t 
                   const int32_t* inv_pos, const float* topk_w, void* out, int out_dtype, void* stream) {
   const char* W = "moe_unpermute";
   nvfp4::PermuteArgs k{};
-  if (int r = check_permute(W, d, width, &k)) return r;
+  if (int r = check_permute(W, d, width, dtype, &k)) return r;
   if ((dtype != NVFP4_BF16 && dtype != NVFP4_F32) || (out_dtype != NVFP4_BF16 && out_dtype != NVFP4_F32))
     return fail(NVFP4_EINVAL, "%s: EINVAL dtype=%d out_dtype=%d", W, dtype, out_dtype);
   if (d->T == 0) return ok();
@@ -1217,7 +1222,7 @@ int moe_unpermute_backward(const nvfp4_moe_dims* d, const void* d_out, int out_d
                            void* d_rows, float* d_w, int zero_tail, void* stream) {
   const char* W = "moe_unpermute_backward";
   nvfp4::PermuteArgs k{};
-  if (int r = check_permute(W, d, width, &k)) return r;
+  if (int r = check_permute(W, d, width, dtype, &k)) return r;
   if ((dtype != NVFP4_BF16 && dtype != NVFP4_F32) || (out_dtype != NVFP4_BF16 && out_dtype != NVFP4_F32))
     return fail(NVFP4_EINVAL, "%s: EINVAL dtype=%d out_dtype=%d", W, dtype, out_dtype);
   if (d->T == 0) return ok();

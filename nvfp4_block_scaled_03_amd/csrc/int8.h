@@ -35,8 +35,8 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
 // Codes and scales of the rows of x itself (x, x_f32, ldx, rows, H, q, s).
 hipError_t launch_int8_quantize(const NormArgs& a, hipStream_t s);
 
-// Weight W [N][K] int8 in the streaming layout (half > 0: gate rows [0, half)
-// and up rows [half, 2 half) in alternate tiles).
+// Weight W [N][K] int8 in the streaming layout (gated: gate rows [0, N / 2) and
+// up rows [N / 2, N) in alternate tiles).
 size_t int8_prep_bytes(int64_t N, int64_t K, bool gated);
 hipError_t launch_int8_prep(int64_t N, int64_t K, bool gated, const int8_t* q, uint8_t* prep, hipStream_t s);
 

@@ -1,4 +1,4 @@
-// Dense int8 layers (int8_linear, int8_linear_fused) for gfx950:
+// Dense int8 layers (int8_linear) for gfx950:
 //   y[m][n] = sx[m] sw[n] sum_k xq[m][k] wq[n][k]   (then the epilogue)
 // on the 16x16x64 int8 matrix instruction.  The sums are int32 and exact
 // (|sum| <= 2^14 K < 2^31), in whatever order they are made.
@@ -49,53 +49,38 @@ __global__ __launch_bounds__(256) void int8_prep_kernel(int64_t N, int64_t K, bo
 }
 
 // ---------------------------------------------------------------------------
-// A handful of rows: 16 MT rows x 16 NT columns a workgroup, whose KW wavefronts
+// A handful of rows (up to 16): 16 NT columns a workgroup, whose KW wavefronts
 // split K.  Both operands come straight from memory into registers, the next
 // chunk's while the present one is multiplied; the partial sums meet in LDS and
-// leave in whole rows.  The weights, read once, pass the caches by (34816 x 5120, M =
-// 1: 32.7 -> 30.1 us, 5.9 TB/s).
+// leave in whole rows.  Bound: the weights' bytes.  Read once, they pass the caches
+// by (34816 x 5120, M = 1: 32.7 -> 30.1 us, 5.9 TB/s).
 // ---------------------------------------------------------------------------
-template <bool GATED, int MT, int NT, int KW>
+template <bool GATED, int NT, int KW>
 __global__ __launch_bounds__(KW * 64) void int8_few_kernel(Int8Args p) {
-  constexpr int BM = 16 * MT, BN = 16 * NT, SW = BN + 4;
-  __shared__ __attribute__((aligned(16))) int sh[KW * BM * SW];
+  constexpr int BN = 16 * NT, SW = BN + 4;
+  __shared__ __attribute__((aligned(16))) int sh[KW * 16 * SW];
   const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
   const int kw = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int KC = (int)int8_chunks(p.K);
-  const int64_t tiles = int8_tiles(p.N, GATED);
-  // Row blocks are the faster index, eight workgroups apart in launch order,
-  // so that those of one column block share an XCD's L2.
-  const int rb = (p.M + BM - 1) / BM;
-  const int grp = blockIdx.x / (8 * rb), rem = blockIdx.x - grp * 8 * rb, nb = grp * 8 + (rem & 7), mb = rem >> 3;
-  if ((int64_t)nb * NT >= tiles) return;
+  const int KC = (int)int8_chunks(p.K), nb = blockIdx.x;
   const int c_lo = KC * kw / KW, c_hi = KC * (kw + 1) / KW;
-  const uint8_t* wq = p.w + ((int64_t)nb * NT * KC * 64 + lane) * 16;
-  const int8_t* aq[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) aq[i] = p.a + (int64_t)min(mb * BM + 16 * i + ln, p.M - 1) * p.lda;
+  const uint8_t* const wq = p.w + ((int64_t)nb * NT * KC * 64 + lane) * 16;
+  const int8_t* const aq = p.a + (int64_t)min(ln, p.M - 1) * p.lda;
   struct Chunk {
-    i32x4 w[NT], a[MT];
+    i32x4 w[NT], a;
   };
   auto load = [&](int c, Chunk& d) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       d.w[j] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wq + ((int64_t)j * KC + c) * 1024));
     // (past K the weights are zeros: any 16 bytes of the row will do)
-    const int k = min(c * 64 + lg * 16, p.K - 16);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) d.a[i] = *reinterpret_cast<const i32x4*>(aq[i] + k);
+    d.a = *reinterpret_cast<const i32x4*>(aq + min(c * 64 + lg * 16, p.K - 16));
   };
-  i32x4 acc[MT][NT];
+  i32x4 acc[NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  for (int j = 0; j < NT; ++j) acc[j] = i32x4{0, 0, 0, 0};
   auto compute = [&](const Chunk& d) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(d.a[i], d.w[j], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < NT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(d.a, d.w[j], acc[j], 0, 0, 0);
   };
   if (c_lo < c_hi) {
     Chunk d0, d1;   // (past the end: the last chunk, not used)
@@ -113,27 +98,25 @@ __global__ __launch_bounds__(KW * 64) void int8_few_kernel(Int8Args p) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) sh[(kw * BM + i * 16 + lg * 4 + r) * SW + 16 * j + ln] = acc[i][j][r];
+    for (int r = 0; r < 4; ++r) sh[(kw * 16 + lg * 4 + r) * SW + 16 * j + ln] = acc[j][r];
   __syncthreads();
-  constexpr int OUTC = GATED ? BN / 2 : BN, TOTAL = BM * (OUTC / 4);
+  constexpr int OUTC = GATED ? BN / 2 : BN, TOTAL = 16 * (OUTC / 4);
   const int64_t n_out = GATED ? p.N / 2 : p.N;
 #pragma unroll 1
   for (int at = threadIdx.x; at < TOTAL; at += KW * 64) {
     const int r = at / (OUTC / 4), c4 = at % (OUTC / 4) * 4;
-    const int64_t row[1] = {(int64_t)mb * BM + r}, col = (int64_t)nb * OUTC + c4;
-    if (row[0] >= p.M) break;   // (rows ascend)
+    const int64_t row[1] = {r}, col = (int64_t)nb * OUTC + c4;
+    if (r >= p.M) break;   // (rows ascend)
     if (col >= n_out) continue;
     EpiIn<1> in;
     epi_request<GATED>(p.ep, row[0], col, in);
-    const float sx = p.sx[row[0]];
+    const float sx = p.sx[r];
     auto sum = [&](int cc, const float* sw) {
       i32x4 v = *reinterpret_cast<const i32x4*>(sh + r * SW + cc);
 #pragma unroll
-      for (int k = 1; k < KW; ++k) v += *reinterpret_cast<const i32x4*>(sh + (k * BM + r) * SW + cc);
+      for (int k = 1; k < KW; ++k) v += *reinterpret_cast<const i32x4*>(sh + (k * 16 + r) * SW + cc);
       return f32x4{(float)v[0] * (sx * sw[0]), (float)v[1] * (sx * sw[1]), (float)v[2] * (sx * sw[2]),
                    (float)v[3] * (sx * sw[3])};
     };
@@ -144,12 +127,12 @@ __global__ __launch_bounds__(KW * 64) void int8_few_kernel(Int8Args p) {
   }
 }
 
-template <bool GATED, int MT, int NT, int KW>
+template <bool GATED, int NT, int KW>
 hipError_t launch_few_t(const Int8Args& p, hipStream_t s) {
-  const int64_t rb = (p.M + 16 * MT - 1) / (16 * MT), groups = (int8_tiles(p.N, GATED) / NT + 7) / 8;
-  int8_few_kernel<GATED, MT, NT, KW><<<(unsigned)(groups * 8 * rb), KW * 64, 0, s>>>(p);
+  int8_few_kernel<GATED, NT, KW><<<(unsigned)(int8_tiles(p.N, GATED) / NT), KW * 64, 0, s>>>(p);
   return hipGetLastError();
 }
+
 // ---------------------------------------------------------------------------
 // Tiles of BM = 16 TM WR rows x BN = 16 TN WC columns for many rows: WR x WC
 // wavefronts of 16 TM x 16 TN each.  Both operands travel from memory straight
@@ -469,7 +452,7 @@ hipError_t launch_chosen(const Int8Args& p, hipStream_t s) {
   // A handful of rows: x straight from the caches (us, against 16 x 64 tiles:
   // 34816 x 5120 M = 1 33 to 37 / 38.1, M = 8 35.8 / 38.6, M = 16 43.0 / 39.5; 5120 x
   // 5120 8.7 / 10.3, 8.7 / 10.9, 10.1 / 11.5; 16384 x 2048 10.3 / 9.0, 10.8 / 8.8).
-  if (p.M <= 8) return launch_few_t<GATED, 1, 2, 8>(p, s);
+  if (p.M <= 8) return launch_few_t<GATED, 2, 8>(p, s);
   const int64_t columns = int8_tiles(p.N, GATED) * 16;
   const Choice one = choose(p.M, columns, p.K);
   // Whole rounds of 256 x 256 tiles, and the columns left over by another kernel

@@ -16,6 +16,8 @@
 //
 // A row stays in registers between its two uses: one read, one write.  Bound:
 // bytes.
+#include <algorithm>
+
 #include "common.h"
 #include "int8.h"
 
@@ -298,9 +300,25 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(NormArgs p) 
 template <bool NORM, bool XF32, int RES, int TPR, int VPT>
 hipError_t launch_rows_t(const NormArgs& a, hipStream_t s) {
   constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
-  const int64_t grid = (a.rows + ROWS - 1) / ROWS;
-  row_kernel<NORM, XF32, RES, TPR, VPT><<<(unsigned)grid, TPR < 256 ? 256 : TPR, 0, s>>>(a);
-  return hipGetLastError();
+  // (a launch has fewer than 2^32 threads)
+  constexpr int64_t STEP = (int64_t(1) << 31) / TPR;
+  NormArgs p = a;
+  auto past = [](const void* at, int64_t bytes) {
+    return at ? const_cast<char*>(static_cast<const char*>(at)) + bytes : nullptr;
+  };
+  for (int64_t r = 0; r < a.rows; r += STEP) {
+    p.rows = std::min(a.rows - r, STEP);
+    row_kernel<NORM, XF32, RES, TPR, VPT>
+        <<<(unsigned)((p.rows + ROWS - 1) / ROWS), TPR < 256 ? 256 : TPR, 0, s>>>(p);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    p.x = past(p.x, STEP * p.ldx * (XF32 ? 4 : 2));
+    p.res = past(p.res, STEP * p.ldr * (RES == 2 ? 4 : 2));
+    p.h = past(p.h, STEP * p.ldh * (RES == 2 ? 4 : 2));
+    p.y = past(p.y, STEP * p.ldy * (p.y_f32 ? 4 : 2));
+    p.q = reinterpret_cast<int8_t*>(past(p.q, STEP * p.H));
+    p.s = reinterpret_cast<float*>(past(p.s, STEP * 4));
+  }
+  return hipSuccess;
 }
 // Threads and pieces a thread.  Few rows: as many threads as there are pieces,
 // for the latency (H = 5120, both outputs, us: 1 row 256 x 3 6.4, 512 x 2 4.7, 1024 x

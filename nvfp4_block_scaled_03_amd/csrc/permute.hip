@@ -195,8 +195,8 @@ __global__ __launch_bounds__(256) void unpermute_kernel(KernelArgs p, const u32x
   }
 }
 
-// A wavefront per pair: its row's gradient and its weight's.  The workgroups
-// of a token are eight apart, on one XCD, whose L2 holds the token's d_out.
+// A wavefront per pair (up to four a workgroup): its row's gradient and its
+// weight's.  The workgroups of a token are eight apart, on one XCD, whose L2 holds the token's d_out.
 template <bool F32, bool OUT_F32>
 __global__ __launch_bounds__(256) void unpermute_backward_kernel(KernelArgs p, const void* __restrict__ d_out,
                                                                  const u32x4* __restrict__ rows,
@@ -302,10 +302,11 @@ hipError_t launch_unpermute_backward(const PermuteArgs& a, const void* d_out, bo
   const u32x4* r = static_cast<const u32x4*>(rows);
   u32x4* d = static_cast<u32x4*>(d_rows);
   const unsigned n = (unsigned)blocks;
-  if (f32 && out_f32) unpermute_backward_kernel<true, true><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, n);
-  else if (f32) unpermute_backward_kernel<true, false><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, n);
-  else if (out_f32) unpermute_backward_kernel<false, true><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, n);
-  else unpermute_backward_kernel<false, false><<<grid, 256, 0, s>>>(k, d_out, r, d, d_w, groups, n);
+  const int threads = 64 * std::min(4, k.topk + k.shared);
+  if (f32 && out_f32) unpermute_backward_kernel<true, true><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, n);
+  else if (f32) unpermute_backward_kernel<true, false><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, n);
+  else if (out_f32) unpermute_backward_kernel<false, true><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, n);
+  else unpermute_backward_kernel<false, false><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, n);
   return hipGetLastError();
 }
 

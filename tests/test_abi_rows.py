@@ -84,7 +84,8 @@ def test_int8_sizes(lib):
     assert lib.int8_prep_weights_size(64, 128, 0) == 64 * 128
     assert lib.int8_prep_weights_size(4, 16, 0) == 64 * 128          # whole fours of tiles, pairs of chunks
     assert lib.int8_prep_weights_size(72, 144, 1) == 128 * 256       # 36 gate columns: 3 pairs of tiles, in fours
-    for bad in ((6, 128, 0), (4, 128, 1), (64, 24, 0), (64, 131072, 0), (0, 128, 0), (64, 128, 2), (1 << 21, 128, 0)):
+    for bad in ((6, 128, 0), (4, 128, 1), (64, 24, 0), (64, 131072, 0), (0, 128, 0), (64, 128, 2), (1 << 21, 128, 0),
+                (1 << 20, (1 << 15) + 16, 0)):
         assert lib.int8_prep_weights_size(*bad) == 0, bad
     assert lib.int8_linear_workspace_size(3, 64, 128, 0) >= 3 * 128 + 3 * 4
     assert lib.int8_linear_workspace_size(3, 64, 128, 1) == 0
@@ -113,6 +114,8 @@ def _linear(lib, x=P, x_dtype=2, ldx=128, sx=2 * P, M=4, N=64, K=128, w=3 * P, s
     (dict(K=32784, ldx=32784, x_dtype=0), _lib.NVFP4_ESHAPE, "at most 32768"),
     (dict(ldx=112), _lib.NVFP4_ESHAPE, "ldx=112"),
     (dict(ldx=136), _lib.NVFP4_ESHAPE, "ldx=136"),
+    (dict(ldx=(1 << 22) + 16), _lib.NVFP4_ESHAPE, "at most 2^22"),
+    (dict(N=1 << 20, K=(1 << 15) + 16, ldx=(1 << 15) + 16), _lib.NVFP4_ESHAPE, "N K <= 2^35"),
     (dict(out_dtype=2), _lib.NVFP4_EINVAL, "out_dtype=2"),
     (dict(epi=dict(act=5)), _lib.NVFP4_EINVAL, "act=5"),
     (dict(epi=dict(gated=2)), _lib.NVFP4_ESHAPE, "gated=2"),
@@ -168,6 +171,8 @@ def _backward(lib, d=None, d_out=P, out_dtype=0, rows=2 * P, dtype=0, width=64, 
     (_permute, dict(width=60), _lib.NVFP4_ESHAPE, "width=60"),
     (_permute, dict(width=(1 << 20) + 8), _lib.NVFP4_ESHAPE, "width"),
     (_permute, dict(d=_d(T=1 << 22, topk=2), width=1 << 20, ldx=1 << 20), _lib.NVFP4_ESHAPE, "2^40"),
+    (_permute, dict(d=_d(T=1 << 22, topk=1), width=8192, ldx=8192), _lib.NVFP4_ESHAPE, "64 GiB"),
+    (_unpermute, dict(d=_d(T=1 << 22, topk=1), width=4096, dtype=1), _lib.NVFP4_ESHAPE, "64 GiB"),
     (_permute, dict(ldx=56), _lib.NVFP4_ESHAPE, "ldx=56"),
     (_permute, dict(dtype=2), _lib.NVFP4_EINVAL, "dtype=2"),
     (_permute, dict(x=None), _lib.NVFP4_EINVAL, "null"),

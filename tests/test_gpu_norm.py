@@ -212,6 +212,22 @@ def test_more_than_two_gigabytes_of_rows(dev):
     assert not n.q[:4].any() and not n.y[65535:65540].any()
 
 
+def test_more_rows_than_a_launch_has_threads_for(dev):
+    T, H = (1 << 26) + 3, 8
+    x = torch.zeros(T, H, dtype=BF, device=dev)
+    w = torch.ones(H, dtype=BF, device=dev)
+    ends = torch.tensor([0, (1 << 25) - 1, 1 << 25, (1 << 26) - 1, 1 << 26, T - 1], device=dev)
+    some, _, _ = _inputs(dev, len(ends), H, BF, None, BF)
+    x[ends] = some
+    n = ops.rms_norm(x, w, residual=x, outputs="both")
+    assert torch.equal(n.h[ends], 2 * some)
+    _check(ops.NormOut(n.y[ends], None, n.q[ends], n.s[ends]), 2 * some, w, 1e-6)
+    assert int((n.s != 0).sum()) == len(ends) and int(n.y.any(1).sum()) == len(ends)
+    q, s = ops.int8_quantize(x)
+    qe, se = ops.int8_quantize(some)
+    assert torch.equal(q[ends], qe) and torch.equal(s[ends], se) and int((s != 0).sum()) == len(ends)
+
+
 def test_empty_refused_and_other_streams(dev):
     w = torch.ones(64, dtype=BF, device=dev)
     n = ops.rms_norm(torch.empty(0, 64, dtype=BF, device=dev), w, outputs="both")

@@ -190,6 +190,36 @@ def test_rows_past_two_gigaelements(dev):
     assert (gw[-100:].double() - dots).abs().max() <= (W / 64 + 8) * HALF * float(dots.max())
 
 
+def test_as_many_tokens_as_there_can_be(dev):
+    T, W = 1 << 24, 8
+    d = ops.dims(T, 1, 2, 128, 128)
+    al = ops.moe_align(d, torch.arange(T, device=dev, dtype=torch.int32).view(T, 1) % 2)
+    x = torch.randn(T, W, generator=torch.Generator(device=dev).manual_seed(1), device=dev).to(BF)
+    rows = ops.moe_permute(d, x, al)
+    assert torch.equal(rows, x.view(T // 2, 2, W).transpose(0, 1).reshape(T, W))
+    w = torch.full((T, 1), 0.5, device=dev, requires_grad=True)
+    rows.requires_grad_()
+    out = ops.moe_unpermute(d, rows, al, w)
+    gr, gw = torch.autograd.grad(out, (rows, w), x)
+    assert torch.equal(out, (0.5 * x.float()).to(BF)) and torch.equal(gr, (0.5 * rows.detach().float()).to(BF))
+    dots = (x.double() ** 2).sum(1, keepdim=True)
+    assert ((gw.double() - dots).abs() <= 8 * HALF * dots).all()
+
+
+def test_second_derivatives_are_refused(dev):
+    g, d, al, w, inv = _setup(dev, 5, 2, 4, 0)
+    x = _rand(g, dev, F32, 5, 16).requires_grad_()
+    w = w.requires_grad_()
+    out = ops.moe_unpermute(d, ops.moe_permute(d, x, al), al, w)
+    gx, gw = torch.autograd.grad((out * out).sum(), (x, w), create_graph=True)
+    ref = torch.autograd.grad(ops.moe_unpermute(d, ops.moe_permute(d, x, al), al, w), (x, w), 2 * out.detach())
+    assert torch.equal(gx, ref[0]) and torch.equal(gw, ref[1])
+    with pytest.raises(RuntimeError):                    # (torch finds no way from the gradients to x)
+        torch.autograd.grad(gx.sum() + gw.sum(), x, retain_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (gx.sum() + gw.sum()).backward()
+
+
 def test_other_stream_and_graph_with_gradients(dev):
     T, k, E, W = 50, 4, 8, 264
     g, d, al, w, inv = _setup(dev, T, k, E, 1, 3, 0.2)
