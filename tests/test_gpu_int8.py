@@ -226,6 +226,31 @@ def test_bf16_input_equals_its_codes(dev):
         assert torch.equal(ops.int8_linear(q, w, s, ws=ws), ref)
 
 
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 64), (1, 528), (1, 4112), (1, 32752), (2, 272), (2, 16368), (3, 1040), (4, 8176),
+                                 (5, 144), (6, 5440), (7, 4656), (8, 80), (8, 4080), (8, 4096), (3, 16384), (1, 32768)])
+def test_few_bf16_rows_equal_their_codes(dev, M, K):
+    """Zeros, the ends of the range, infinities and NaN among them, strided or not."""
+    wq, sw = _codes(dev, 72, K, 9)
+    g = _gen(dev, M + K)
+    wide = torch.randn(M, K + 24, generator=g, device=dev).to(BF)
+    for x in (wide[:, 8:K + 8], wide[:, :K].contiguous()):
+        x[0, K // 2] = 90.0                                    # codes of small parts of the maximum
+        for i, what in enumerate((0.0, 2.0 ** -120, 2.0 ** 110, float("inf"), float("nan"))):
+            if M > i + 1:
+                x[i + 1] = x[i + 1] * what if 0 < what < 2.0 ** 120 else x[i + 1]
+                if what == 0.0:
+                    x[i + 1] = 0.0
+                elif not what < 2.0 ** 120:
+                    x[i + 1, K - 1] = what
+        for gated in (False, True):
+            w = ops.prepare_int8_weight(wq, sw, gated)
+            q, s = ops.int8_quantize(x)
+            ref = ops.int8_linear(q, w, s, out_dtype=F32)
+            got = ops.int8_linear(x, w, out_dtype=F32)
+            assert torch.equal(torch.isnan(got), torch.isnan(ref))
+            assert torch.equal(got.nan_to_num(), ref.nan_to_num())
+
+
 def test_quantised_weight(dev):
     w = 0.02 * torch.randn(136, 272, generator=_gen(dev, 1), device=dev)
     x = torch.randn(9, 272, generator=_gen(dev, 2), device=dev).to(BF)
