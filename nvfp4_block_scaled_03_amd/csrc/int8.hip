@@ -49,12 +49,13 @@ __global__ __launch_bounds__(256) void int8_prep_kernel(int64_t N, int64_t K, bo
 }
 
 // ---------------------------------------------------------------------------
-// A handful of rows (up to 16): 16 NT columns a workgroup, whose KW wavefronts
+// A handful of rows (kFewRows at most): 16 NT columns a workgroup, whose KW wavefronts
 // split K.  Both operands come straight from memory into registers, the next
 // chunk's while the present one is multiplied; the partial sums meet in LDS and
 // leave in whole rows.  Bound: the weights' bytes.  Read once, they pass the caches
 // by (34816 x 5120, M = 1: 32.7 -> 30.1 us, 5.9 TB/s).
 // ---------------------------------------------------------------------------
+constexpr int kFewRows = 16;
 template <bool GATED, int NT, int KW>
 __global__ __launch_bounds__(KW * 64) void int8_few_kernel(Int8Args p) {
   constexpr int BN = 16 * NT, SW = BN + 4;
@@ -400,6 +401,17 @@ float tile_cost(const TileCost& t, int64_t M, int64_t columns, int64_t K, int S)
   return std::max(c, 3.0f + m) + 0.2f * std::min(c, m);
 }
 
+// The same for the few-rows kernel, of whose workgroups three run at once on a CU;
+// fitted to 95 timings (1 and 16 rows, us, against the best of the tiles': 34816 x
+// 5120 33.2, 41.1 / 34.9, 35.9; 5120 x 5120 7.6, 9.4 / 9.3, 10.6; 16384 x 2048 10.2,
+// 11.4 / 8.1, 8.3; 16384 x 16384 56.9, 54.4 / 41.0, 41.9).
+float few_cost(int64_t M, int64_t columns, int64_t K) {
+  const float rounds = std::max(1.0f, (float)columns / (32.0f * 768.0f));
+  const float c = 3.5f + rounds * (float)(((K + 127) / 128 * 2 + 7) / 8) * (0.227f + 0.011f * M);
+  const float m = (float)columns * K / 5.5e6f;
+  return std::max(c, 3.0f + m) + 0.2f * std::min(c, m);
+}
+
 struct Choice {
   int kind, parts;
   float cost;
@@ -449,12 +461,9 @@ hipError_t launch_kind(const Int8Args& p, int kind, int parts, int64_t col0, int
 
 template <bool GATED>
 hipError_t launch_chosen(const Int8Args& p, hipStream_t s) {
-  // A handful of rows: x straight from the caches (us, against 16 x 64 tiles:
-  // 34816 x 5120 M = 1 33 to 37 / 38.1, M = 8 35.8 / 38.6, M = 16 43.0 / 39.5; 5120 x
-  // 5120 8.7 / 10.3, 8.7 / 10.9, 10.1 / 11.5; 16384 x 2048 10.3 / 9.0, 10.8 / 8.8).
-  if (p.M <= 8) return launch_few_t<GATED, 2, 8>(p, s);
   const int64_t columns = int8_tiles(p.N, GATED) * 16;
   const Choice one = choose(p.M, columns, p.K);
+  if (p.M <= kFewRows && few_cost(p.M, columns, p.K) < one.cost) return launch_few_t<GATED, 2, 8>(p, s);
   // Whole rounds of 256 x 256 tiles, and the columns left over by another kernel
   // (4096 x 5120 x 17408: 393 us in 256 x 256 tiles, 347 in 256 x 128).
   const int64_t rb = (p.M + 255) / 256, cb = (columns + 255) / 256, whole = rb * cb / 256 * 256 / rb;

@@ -156,6 +156,16 @@ def test_larger_layers(dev, M, N, K, cfg):
     assert got.shape == (M, N // 2 if gated else N)
 
 
+# a handful of rows, on their own kernel and on the tiles'
+@pytest.mark.parametrize("M", [1, 4, 9, 16, 17])
+@pytest.mark.parametrize("N,K", [(264, 4112), (5128, 1040), (16392, 272), (16392, 2064), (34824, 528), (520, 16400),
+                                 (8200, 8208)])
+@pytest.mark.parametrize("cfg", [CONFIGS[1], CONFIGS[5]], ids=["plain", "gated"])
+def test_a_handful_of_rows(dev, M, N, K, cfg):
+    got = _rows_of_large(dev, M, N, K, cfg)
+    assert got.shape == (M, N // 2 if cfg[1] else N)
+
+
 # every tile size, in one part and with K in parts
 @pytest.mark.parametrize("M,N,K", [(42, 104, 400), (16, 72, 2576), (61, 136, 128), (17, 2120, 4352), (51, 8648, 128),
                                    (65, 1960, 4624), (65, 16168, 144), (72, 2952, 7440), (36, 34304, 144),
