@@ -143,6 +143,14 @@ hipError_t launch_few_t(const Int8Args& p, hipStream_t s) {
 // bytes of a row, a whole cache line, and a row's eight 16-byte units are
 // swizzled by the row, so that the 16 rows of a fragment (one unit each) fall
 // into distinct banks.  A stage's weights are whole operands as they lie.
+//
+// What bounds it: few row blocks, the weights' bytes (34816 x 5120, M = 64 in 64 x
+// 256 tiles: 40 us, 4.5 TB/s from 136 CUs).  Many rows, the matrix units' power: 4096
+// x 4096 x 17408 in 256 x 256 tiles takes 225 us (2.6 PFLOP/s), 176 us with operands of
+// zeros; the loads alone (25-30 B a cycle and CU from L2 into LDS) take 167-175,
+// the products alone 160.  A deeper ring, products of 32 x 32 x 32 (more registers
+// than there are), 4 wavefronts of 128 x 128, stages begun at different places and
+// rows of x padded apart were no faster.
 // ---------------------------------------------------------------------------
 constexpr int kMaxParts = 4;                          // of K
 constexpr int64_t kPartBytes = int64_t(64) << 20;     // their sums, at most
@@ -465,7 +473,8 @@ hipError_t launch_chosen(const Int8Args& p, hipStream_t s) {
   const Choice one = choose(p.M, columns, p.K);
   if (p.M <= kFewRows && few_cost(p.M, columns, p.K) < one.cost) return launch_few_t<GATED, 2, 8>(p, s);
   // Whole rounds of 256 x 256 tiles, and the columns left over by another kernel
-  // (4096 x 5120 x 17408: 393 us in 256 x 256 tiles, 347 in 256 x 128).
+  // (4096 x 5120 x 17408: 393 us in 256 x 256 tiles, 347 in 256 x 128, 312 so: 231 for
+  // 4096 columns and 81 for 1024, in 256 x 128 tiles with K in two parts).
   const int64_t rb = (p.M + 255) / 256, cb = (columns + 255) / 256, whole = rb * cb / 256 * 256 / rb;
   if (whole > 0 && whole < cb) {
     const int64_t rest = columns - whole * 256;
