@@ -320,29 +320,38 @@ hipError_t launch_rows_t(const NormArgs& a, hipStream_t s) {
   }
   return hipSuccess;
 }
-// Threads and pieces a thread.  Few rows: as many threads as there are pieces,
-// for the latency (H = 5120, both outputs, us: 1 row 256 x 3 6.4, 512 x 2 4.7, 1024 x
-// 1 4.2; 256 rows 8.3, 6.6, 6.0; 17408 1024 x 3 7.7, 256 x 9 14.9).  Many rows: more
-// pieces a thread, for fewer reductions and barriers a byte (8192 rows of 4096,
-// both outputs / codes alone: 256 x 2 60.5 / 24.0, 1024 x 1 66.1 / 35.4; of 8192 256 x
-// 4 121.6 / 42.2, 1024 x 1 113.0 / 53.3; of 1024 64 x 2 23.0 / 9.0, 256 x 1 22.7 / 12.3).
-// The first is 302 MB at 5.0 TB/s.
+// Threads and pieces a thread.  A piece a thread for the latency (H = 5120, both
+// outputs, us: 1 row 256 x 3 6.4, 512 x 2 4.7, 1024 x 1 4.2) as long as the workgroups
+// take turns in loading and reducing (both outputs / codes alone: 1024 rows of 8192
+// 256 x 4 23.7 / 9.5, 1024 x 1 20.1 / 9.5; 4096 rows of 4096 256 x 2 35.6 / 13.9, 512 x
+// 1 32.2 / 14.8; 16384 rows of 2048 64 x 4 68.7 / 21.6, 256 x 1 59.4 / 27.0).  Fewer
+// reductions and barriers a byte for many rows that are short or leave threads idle,
+// and for the codes alone, whose rows have a third of the bytes (16384 rows of 1024 64
+// x 2 35.5 / 13.2, 256 x 1 39.1 / 20.8; of 5120 256 x 3 151.6 / 47.7, 1024 x 1 155.6 /
+// 77.7), and for long ones, which do not fit a piece a thread (4096 rows of 16384 512 x
+// 4 125.8 / 36.2, 1024 x 2 137.4 / 43.1).  151.6 us are 755 MB at 5.0 TB/s.
 template <bool NORM, bool XF32, int RES>
 hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
   const int V = a.H / 8;
+  const bool many = a.rows > (NORM ? 4096 : 1024);
   if (V <= 64) return launch_rows_t<NORM, XF32, RES, 64, 1>(a, s);
-  if (a.rows <= 1024) {
-    if (V <= 256) return launch_rows_t<NORM, XF32, RES, 256, 1>(a, s);
-    if (V <= 512) return launch_rows_t<NORM, XF32, RES, 512, 1>(a, s);
-    if (V <= 1024) return launch_rows_t<NORM, XF32, RES, 1024, 1>(a, s);
+  if (many) {
+    if (V <= 128) return launch_rows_t<NORM, XF32, RES, 64, 2>(a, s);
+    if constexpr (!NORM) {
+      if (V <= 256) return launch_rows_t<NORM, XF32, RES, 64, 4>(a, s);
+      if (V <= 512) return launch_rows_t<NORM, XF32, RES, 256, 2>(a, s);
+      if (V > 768 && V <= 1024) return launch_rows_t<NORM, XF32, RES, 256, 4>(a, s);
+    }
+    if (V > 512 && V <= 768) return launch_rows_t<NORM, XF32, RES, 256, 3>(a, s);
+  }
+  if (V <= 256) return launch_rows_t<NORM, XF32, RES, 256, 1>(a, s);
+  if (V <= 512) return launch_rows_t<NORM, XF32, RES, 512, 1>(a, s);
+  if (V <= 1024) return launch_rows_t<NORM, XF32, RES, 1024, 1>(a, s);
+  if (a.rows <= 256) {   // (17408, 1 row: 1024 x 3 7.7, 256 x 9 14.9)
     if (V <= 2048) return launch_rows_t<NORM, XF32, RES, 1024, 2>(a, s);
     if (V <= 3 * 1024) return launch_rows_t<NORM, XF32, RES, 1024, 3>(a, s);
-    return launch_rows_t<NORM, XF32, RES, 512, 8>(a, s);
   }
-  if (V <= 128) return launch_rows_t<NORM, XF32, RES, 64, 2>(a, s);
-  if (V <= 256) return launch_rows_t<NORM, XF32, RES, 256, 1>(a, s);
-  if (V <= 512) return launch_rows_t<NORM, XF32, RES, 256, 2>(a, s);
-  if (V <= 1024) return launch_rows_t<NORM, XF32, RES, 256, 4>(a, s);
+  if (V <= 2048) return launch_rows_t<NORM, XF32, RES, 512, 4>(a, s);
   if (V <= 2560) return launch_rows_t<NORM, XF32, RES, 512, 5>(a, s);
   return launch_rows_t<NORM, XF32, RES, 512, 8>(a, s);
 }

@@ -63,7 +63,8 @@ def _check(n, h, w, eps, rows=slice(None)):
 
 SIZES = [(1, 8), (1, 64), (5, 512), (5, 520), (2, 2048), (7, 2056), (3, 4096), (2, 4104), (3, 8192), (2, 8200),
          (2, 16384), (1, 16392), (2, 24584), (2, 32768), (300, 1032),
-         (1500, 64), (1501, 1032), (1100, 2056), (1030, 4104), (1025, 8200), (1027, 20488)]
+         (1500, 64), (1501, 1032), (1100, 2056), (1030, 4104), (1025, 8200), (1027, 20488),
+         (4099, 1000), (4097, 4112), (300, 16376), (257, 24584)]
 
 
 @pytest.mark.parametrize("T,H", SIZES)
@@ -153,7 +154,9 @@ def test_rows_without_a_value_and_rows_with_nan_or_infinity(dev):
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
-@pytest.mark.parametrize("T,K", [(1, 8), (3, 16), (17, 528), (4, 4096), (2, 17408), (1, 32768), (513, 1040)])
+@pytest.mark.parametrize("T,K", [(1, 8), (3, 16), (17, 528), (4, 4096), (2, 17408), (1, 32768), (513, 1040), (1030, 1000),
+                                 (1027, 2048), (1026, 4088), (1025, 6136), (1029, 8192), (300, 16376), (257, 20480),
+                                 (258, 24584)])
 def test_int8_quantize(dev, T, K, dt):
     x, _, _ = _inputs(dev, T, K, dt, None, dt, seed=3)
     q, s = ops.int8_quantize(x)
