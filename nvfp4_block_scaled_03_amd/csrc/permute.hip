@@ -195,18 +195,20 @@ __global__ __launch_bounds__(256) void unpermute_kernel(KernelArgs p, const u32x
   }
 }
 
-// A wavefront per pair (up to four a workgroup): its row's gradient and its
-// weight's.  The workgroups of a token are eight apart, on one XCD, whose L2 holds the token's d_out.
-template <bool F32, bool OUT_F32>
+// WPP wavefronts per pair (one: up to four pairs a workgroup): its row's
+// gradient and its weight's.  The workgroups of a token are eight apart, on one
+// XCD, whose L2 holds the token's d_out.
+template <bool F32, bool OUT_F32, int WPP>
 __global__ __launch_bounds__(256) void unpermute_backward_kernel(KernelArgs p, const void* __restrict__ d_out,
                                                                  const u32x4* __restrict__ rows,
                                                                  u32x4* __restrict__ d_rows, float* __restrict__ d_w,
                                                                  int groups, unsigned blocks) {
   if (blockIdx.x >= blocks) return clear_tail(p, d_rows, blocks);
   constexpr int N = Piece<F32>::N;
-  const int lane = threadIdx.x & 63;
+  __shared__ float dots[WPP];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int t = (int)(blockIdx.x / (8u * groups)) * 8 + (int)(blockIdx.x % 8);
-  const int j = __builtin_amdgcn_readfirstlane((int)(blockIdx.x / 8 % groups * 4 + (threadIdx.x >> 6)));
+  const int j = (int)(blockIdx.x / 8 % groups) * (4 / WPP) + wave / WPP, part = wave % WPP;
   const int n = p.topk + p.shared;
   if (t >= p.T || j >= n) return;
   const int r = row_of(p, t, j);
@@ -217,7 +219,7 @@ __global__ __launch_bounds__(256) void unpermute_backward_kernel(KernelArgs p, c
     const int64_t at_r = (int64_t)r * p.V, at_d = (int64_t)t * p.V;
     by_size(kept_rows(p), p.V, [&](auto nt) {
 #pragma unroll 4
-      for (int v = lane; v < p.V; v += 64) {
+      for (int v = part * 64 + lane; v < p.V; v += WPP * 64) {
         float d[N], x[N];
         if constexpr (F32 == OUT_F32) {
           Piece<F32>::unpack(static_cast<const u32x4*>(d_out)[at_d + v], d);
@@ -251,7 +253,14 @@ __global__ __launch_bounds__(256) void unpermute_backward_kernel(KernelArgs p, c
   if (d_w && j < p.topk) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off);
-    if (lane == 0) d_w[(int64_t)t * p.topk + j] = dot;
+    if constexpr (WPP > 1) {   // (the same pair for the whole workgroup)
+      if (lane == 0) dots[part] = dot;
+      __syncthreads();
+      dot = dots[0];
+#pragma unroll
+      for (int w = 1; w < WPP; ++w) dot += dots[w];
+    }
+    if (lane == 0 && part == 0) d_w[(int64_t)t * p.topk + j] = dot;
   }
 }
 
@@ -293,21 +302,32 @@ hipError_t launch_unpermute(const PermuteArgs& a, const void* rows, bool f32, vo
   return hipGetLastError();
 }
 
+template <int WPP>
+hipError_t launch_backward_t(const KernelArgs& k, const void* d_out, bool out_f32, const u32x4* r, bool f32, u32x4* d,
+                             float* d_w, bool zero_tail, hipStream_t s) {
+  const int n = k.topk + k.shared, groups = (n * WPP + 3) / 4, threads = 64 * std::min(4, n * WPP);
+  const int64_t blocks = (int64_t)((k.T + 7) / 8) * 8 * groups;
+  const unsigned grid = (unsigned)(blocks + (zero_tail && d ? tail_blocks(k) : 0)), b = (unsigned)blocks;
+  if (f32 && out_f32) unpermute_backward_kernel<true, true, WPP><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, b);
+  else if (f32) unpermute_backward_kernel<true, false, WPP><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, b);
+  else if (out_f32)
+    unpermute_backward_kernel<false, true, WPP><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, b);
+  else unpermute_backward_kernel<false, false, WPP><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, b);
+  return hipGetLastError();
+}
+
 hipError_t launch_unpermute_backward(const PermuteArgs& a, const void* d_out, bool out_f32, const void* rows, bool f32,
                                      void* d_rows, float* d_w, bool zero_tail, hipStream_t s) {
   const KernelArgs k = kernel_args(a, f32);
-  const int groups = (k.topk + k.shared + 3) / 4;
-  const int64_t blocks = (int64_t)((k.T + 7) / 8) * 8 * groups;
-  const unsigned grid = (unsigned)(blocks + (zero_tail && d_rows ? tail_blocks(k) : 0));
   const u32x4* r = static_cast<const u32x4*>(rows);
   u32x4* d = static_cast<u32x4*>(d_rows);
-  const unsigned n = (unsigned)blocks;
-  const int threads = 64 * std::min(4, k.topk + k.shared);
-  if (f32 && out_f32) unpermute_backward_kernel<true, true><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, n);
-  else if (f32) unpermute_backward_kernel<true, false><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, n);
-  else if (out_f32) unpermute_backward_kernel<false, true><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, n);
-  else unpermute_backward_kernel<false, false><<<grid, threads, 0, s>>>(k, d_out, r, d, d_w, groups, n);
-  return hipGetLastError();
+  // Four wavefronts a pair for long rows, and for shorter ones while there are few
+  // pairs (us, bfloat16 of width W, one / four: 8192 x 8 pairs W = 8192 510 / 433, 4096
+  // 235 / 202, 2880 150 / 164; 256 x 8 W = 2880 11.6 / 8.8; 512 x 8 W = 1024 6.7 / 8.9;
+  // 128 x 2 W = 7168 11.7 / 5.9).  A launch has fewer than 2^32 threads.
+  if (k.P < 1 << 23 && (k.V >= 512 || (k.V > 64 && k.P <= 8 * k.V)))
+    return launch_backward_t<4>(k, d_out, out_f32, r, f32, d, d_w, zero_tail, s);
+  return launch_backward_t<1>(k, d_out, out_f32, r, f32, d, d_w, zero_tail, s);
 }
 
 }  // namespace nvfp4

@@ -101,6 +101,14 @@ def test_gradients(dev, T, k, E, shared, dropped, W, dt, ot):
     assert np.array_equal(_f64(one), wr) if dt == F32 or ot == BF else (np.abs(_f64(one) - wr) <= HALF_BF * np.abs(wr)).all()
 
 
+@pytest.mark.parametrize("W", [1032, 3584, 4112])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_gradients_of_more_pairs(dev, dt, W):
+    """On both sides of the pairs from which one wavefront takes a row."""
+    test_gradients(dev, 60, 8, 20, 1, 0.1, W, dt, BF)
+    test_gradients(dev, 500, 8, 20, 1, 0.1, W, dt, BF)
+
+
 def test_gradients_against_differences(dev):
     """The whole way, x -> rows -> (row by row) -> sum, in float32: linear in x
     and in the weights, so that a difference is exact but for its roundings."""
