@@ -907,7 +907,8 @@ def moe_permute(d: Dims, x: torch.Tensor, al: Alignment, out: Optional[torch.Ten
     p is that of the token of ``al.sorted_pair[p]``.  ``al``: moe_align's for the
     T, topk, E and shared of ``d`` (whose H plays no part).  Rows behind the last
     kept pair are zeros, in ``out`` [P, width] left as they were.  Differentiable
-    in x (without ``out``)."""
+    in x (without ``out``), once; a backward pass that is captured into a graph
+    needs leaves that no other autograd graph alive has used."""
     dev = x.get_device()
     if not _same_device(dev, al.offsets, al.inv_pos, out):
         with torch.cuda.device(dev):
@@ -931,7 +932,7 @@ def moe_unpermute(d: Dims, rows: torch.Tensor, al: Alignment, topk_w: Optional[t
     pair (t, j), plus the shared expert's row (FP32, rounded once to
     ``out_dtype``, the rows' type by default).  ``rows`` [P, width] in moe_permute's
     order; without ``topk_w`` (float32 [T, topk]) every weight is 1.  Differentiable
-    in rows and topk_w (without ``out``); a saved tensor that a call of this
+    in rows and topk_w (without ``out``), as moe_permute; a saved tensor that a call of this
     module writes through ``out`` before the backward pass is not noticed."""
     dev = rows.get_device()
     if not _same_device(dev, al.offsets, al.inv_pos, topk_w, out):
