@@ -151,7 +151,8 @@ __global__ __launch_bounds__(256) void unpermute_kernel(KernelArgs p, const u32x
       const Pairs pairs(p, t, j0 + (int)(threadIdx.x & 63), n);
       // The pairs that have a row, in their order.  Their pieces are requested
       // together (places past the last one: it once more), without branches
-      // between the loads, each of which would wait for the load before.
+      // between the loads, each of which would wait for the load before (256 x 11
+      // rows of 8 KiB: up to 8 at a time 8.6 us, up to 12 7.2).
       uint64_t left = __ballot(pairs.row >= 0);
       auto batch = [&](auto size) {
         constexpr int B = decltype(size)::value;
@@ -167,17 +168,20 @@ __global__ __launch_bounds__(256) void unpermute_kernel(KernelArgs p, const u32x
         }
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-          if (k >= count) break;
-          const float w = pairs.w_at(at[k]);
-          float e[N];
-          Piece<F32>::unpack(d[k], e);
+          if (k < count) {
+            const float w = pairs.w_at(at[k]);
+            float e[N];
+            Piece<F32>::unpack(d[k], e);
 #pragma unroll
-          for (int i = 0; i < N; ++i) acc[i] = __builtin_fmaf(w, e[i], acc[i]);
+            for (int i = 0; i < N; ++i) acc[i] = __builtin_fmaf(w, e[i], acc[i]);
+          }
         }
       };
       while (left) {
-        if (__popcll(left) > 4) batch(std::integral_constant<int, 8>());
-        else batch(std::integral_constant<int, 4>());
+        if (__popcll(left) > 8) batch(std::integral_constant<int, 12>());
+        else if (__popcll(left) > 4) batch(std::integral_constant<int, 8>());
+        else if (__popcll(left) > 2) batch(std::integral_constant<int, 4>());
+        else batch(std::integral_constant<int, 2>());
       }
     }
   });

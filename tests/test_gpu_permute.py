@@ -41,7 +41,8 @@ def _rand(g, dev, dt, *shape):
 
 
 CASES = [(1, 1, 1, 0, 0.0), (1, 8, 16, 1, 0.0), (3, 2, 4, 0, 0.5), (5, 10, 12, 1, 0.3), (17, 3, 5, 1, 0.0),
-         (40, 8, 64, 0, 0.9), (6, 4, 4, 0, 1.0), (6, 4, 4, 1, 1.0), (130, 5, 9, 1, 0.2)]
+         (40, 8, 64, 0, 0.9), (6, 4, 4, 0, 1.0), (6, 4, 4, 1, 1.0), (130, 5, 9, 1, 0.2),
+         (4, 26, 30, 1, 0.1), (9, 80, 90, 0, 0.5)]
 
 
 @pytest.mark.parametrize("dt,ot", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
