@@ -12,7 +12,8 @@
 // of 254 |v| - (2 k + 1) max |v|; near a whole number the candidate may be one
 // off, which the comparison sets right.  With bfloat16 h and w all of it is exact
 // in FP32 (v has 16 bits, 254 v 23, (2 k + 1) max |v| 24); with float32 ones v is
-// exact in FP64.  FP64 too where a row's magnitudes come near the ends of FP32.
+// exact in FP64 (48 bits) and the comparison takes in what FP64 rounds off 254 |v|
+// (55).  FP64 too where a row's magnitudes come near the ends of FP32.
 //
 // A row stays in registers between its two uses: one read, one write.  Bound:
 // bytes.
@@ -137,9 +138,11 @@ __device__ __forceinline__ int code_f32(float a, float top, float inv) {
   const int c = (int)k;
   return c + (d > 0.0f || (d == 0.0f && (c & 1)));
 }
+// (254 a is p + e.  Where p - (2 k + 1) top comes near e it is exact: a whole
+// multiple of the last places of p and top, and far below either.)
 __device__ __forceinline__ int code_f64(double a, double top, double inv) {
-  const double k = floor(a * inv);
-  const double d = __builtin_fma(-(2.0 * k + 1.0), top, 254.0 * a);
+  const double k = floor(a * inv), p = 254.0 * a, e = __builtin_fma(254.0, a, -p);
+  const double d = __builtin_fma(-(2.0 * k + 1.0), top, p) + e;
   const int c = (int)k;
   return min(c + (d > 0.0 || (d == 0.0 && (c & 1))), 127);
 }

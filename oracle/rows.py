@@ -5,6 +5,8 @@ Test infrastructure only: imported by tests/, never by the product path.
 """
 from __future__ import annotations
 
+from fractions import Fraction
+
 import numpy as np
 
 
@@ -14,8 +16,14 @@ def quantize(v):
     v = np.asarray(v, dtype=np.float64)
     top = np.abs(v).max(axis=1)
     safe = np.where(top > 0, top, 1.0)[:, None]
-    # (127 v is exact for v of up to 46 bits and so is a tie of the quotient)
-    return np.rint(127.0 * v / safe).astype(np.int64), top
+    with np.errstate(invalid="ignore"):
+        t = 127.0 * v / safe
+        q = np.rint(t).astype(np.int64)
+        # (t is off by 2^-45 at most: next to a half the rational quotient decides)
+        near = np.argwhere(np.abs(np.abs(t - np.trunc(t)) - 0.5) < 2.0 ** -40)
+    for r, c in near:
+        q[r, c] = round(127 * Fraction(v[r, c]) / Fraction(top[r]))
+    return q, top
 
 
 def int8_quantize(x):
