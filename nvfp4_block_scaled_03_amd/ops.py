@@ -645,7 +645,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     if not _same_device(dev, weight, residual, y, h, q, s):
         with torch.cuda.device(dev):
             return rms_norm(x, weight, eps, residual, outputs, out_dtype, y, h, q, s)
-    _no_gradient("rms_norm", x, weight, residual)
+    _no_gradient("rms_norm", x, weight, residual, y, h, s)
     if x.dim() != 2 or weight.shape != x.shape[1:]:
         raise ValueError("x must be [T, H] and weight [H]")
     T, H = x.shape
@@ -717,7 +717,7 @@ def int8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional
     if not _same_device(dev, q, s):
         with torch.cuda.device(dev):
             return int8_quantize(x, q, s)
-    _no_gradient("int8_quantize", x)
+    _no_gradient("int8_quantize", x, s)
     if x.dim() != 2:
         raise ValueError("x must be [rows, K]")
     rows, K = x.shape
@@ -779,7 +779,7 @@ def int8_linear(x: torch.Tensor, w: Int8LinearWeight, s: Optional[torch.Tensor] 
     if not _same_device(dev, w.prep, w.s, s, bias, residual, out, ws):
         with torch.cuda.device(dev):
             return int8_linear(x, w, s, out_dtype, out, ws, bias, act, residual)
-    _no_gradient("int8_linear", x, bias, residual)
+    _no_gradient("int8_linear", x, s, w.s, bias, residual, out)
     N, K = w.N, w.K
     if x.dim() != 2 or x.shape[1] != K or x.dtype not in (torch.bfloat16, torch.int8):
         raise ValueError(f"x must be int8 or bfloat16 [M, {K}]")

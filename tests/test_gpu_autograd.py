@@ -1,0 +1,76 @@
+"""What autograd may take for differentiable in the norm, the int8 layers and
+the movement of rows by expert: refused."""
+import pytest
+import torch
+
+from nvfp4_block_scaled_03_amd import ops
+
+from parity import device
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def dev():
+    return device()
+
+
+class _Calls:
+    """Arguments of every operator, and calls with one of them put in."""
+
+    def __init__(self, dev):
+        g = torch.Generator(device=dev).manual_seed(1)
+        r = lambda *s: torch.randn(*s, generator=g, device=dev)
+        T, H, k, E = 6, 64, 2, 4
+        ids = torch.randint(0, E, (T, k), generator=g, device=dev, dtype=torch.int32)
+        d = ops.dims(T, k, E, 128, 128)
+        al = ops.moe_align(d, ids)
+        x, weight, res, w8 = r(T, H).to(BF), r(H), r(T, H), r(32, H)
+        wq, ws = ops.int8_quantize(w8)
+        xq, xs = ops.int8_quantize(x)
+        self.tensors = dict(x=x, weight=weight, residual=res, s=xs, w_s=ws, bias=r(32), added=r(T, 32), rows=r(T * k, H),
+                            topk_w=r(T, k))
+        t = self.tensors
+        get = lambda new, name: new.get(name, t[name])
+        layer = lambda **n: ops.int8_linear(xq, ops.prepare_int8_weight(wq, get(n, "w_s")), get(n, "s"),
+                                            bias=get(n, "bias"), residual=get(n, "added"), out_dtype=F32)
+        self.calls = {
+            "rms_norm": (lambda **n: ops.rms_norm(get(n, "x"), get(n, "weight"), residual=get(n, "residual")).y,
+                         ("x", "weight", "residual")),
+            "int8_quantize": (lambda **n: ops.int8_quantize(get(n, "x"))[1], ("x",)),
+            "int8_linear": (layer, ("s", "w_s", "bias", "added")),
+            "int8_linear of bf16": (lambda **n: ops.int8_linear(get(n, "x"), ops.prepare_int8_weight(wq, ws)), ("x",)),
+            "moe_permute": (lambda **n: ops.moe_permute(d, get(n, "x"), al), ("x",)),
+            "moe_unpermute": (lambda **n: ops.moe_unpermute(d, get(n, "rows"), al, get(n, "topk_w")), ("rows", "topk_w")),
+        }
+
+
+OPERATORS = ["rms_norm", "int8_quantize", "int8_linear", "int8_linear of bf16", "moe_permute", "moe_unpermute"]
+
+
+@pytest.mark.parametrize("name", OPERATORS[:4])
+def test_gradients_that_do_not_exist_are_refused(dev, name):
+    c = _Calls(dev)
+    call, names = c.calls[name]
+    for arg in names:
+        leaf = c.tensors[arg].clone().requires_grad_()
+        with pytest.raises(ValueError, match="no gradient"):
+            call(**{arg: leaf})
+        with torch.no_grad():
+            call(**{arg: leaf})
+
+
+def test_results_into_tensors_that_take_gradients_are_refused(dev):
+    x, w = torch.randn(4, 64, device=dev), torch.ones(64, device=dev)
+    leaf = lambda *s: torch.zeros(*s, device=dev, requires_grad=True)
+    q = torch.empty(4, 64, dtype=torch.int8, device=dev)
+    w8 = ops.quantize_int8_weight(torch.randn(32, 64, device=dev))
+    for bad in (lambda: ops.rms_norm(x, w, y=leaf(4, 64)),
+                lambda: ops.rms_norm(x, w, residual=x, h=leaf(4, 64)),
+                lambda: ops.rms_norm(x, w, outputs="int8", q=q, s=leaf(4)),
+                lambda: ops.int8_quantize(x, s=leaf(4)),
+                lambda: ops.int8_linear(x.to(BF), w8, out=leaf(4, 32))):
+        with pytest.raises(ValueError, match="no gradient"):
+            bad()
