@@ -11,6 +11,7 @@ import functools
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from ._lib import NVFP4_BF16, NVFP4_F32, NVFP4_I8, Dims, Epilogue, RmsNormArgs, RouteParams, call
@@ -599,12 +600,21 @@ def mx_linear(x: torch.Tensor, w: MxLinearWeight, out_dtype=torch.bfloat16, out:
 
 
 # ---------------------------------------------------------------- norm and int8 layers
+def _no_tangent(name: str, *tensors):
+    """Refuses tensors that carry a forward-mode tangent: the result would have none."""
+    if forward_ad._current_level >= 0 and torch._C._is_fwd_grad_enabled():
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError(f"{name} has no forward-mode derivative: call it with the primal tensors")
+
+
 def _no_gradient(name: str, *tensors):
     """Refuses a call that autograd would take for a differentiable one."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 raise ValueError(f"{name} has no gradient: call it under torch.no_grad()")
+    _no_tangent(name, *tensors)
 
 
 def _rows_at(t: torch.Tensor, unit: int = 8):
@@ -907,8 +917,8 @@ def moe_permute(d: Dims, x: torch.Tensor, al: Alignment, out: Optional[torch.Ten
     p is that of the token of ``al.sorted_pair[p]``.  ``al``: moe_align's for the
     T, topk, E and shared of ``d`` (whose H plays no part).  Rows behind the last
     kept pair are zeros, in ``out`` [P, width] left as they were.  Differentiable
-    in x (without ``out``), once; a backward pass that is captured into a graph
-    needs leaves that no other autograd graph alive has used."""
+    in x (without ``out``), once and in reverse mode; a backward pass that is
+    captured into a graph needs leaves that no other autograd graph alive has used."""
     dev = x.get_device()
     if not _same_device(dev, al.offsets, al.inv_pos, out):
         with torch.cuda.device(dev):
@@ -916,6 +926,7 @@ def moe_permute(d: Dims, x: torch.Tensor, al: Alignment, out: Optional[torch.Ten
     if x.dim() != 2 or x.shape[0] != d.T:
         raise ValueError(f"x must be [{d.T}, width]")
     _check_alignment(d, al)
+    _no_tangent("moe_permute", x)
     if out is not None:
         _no_gradient("moe_permute with out", x, out)
         if out.shape != (_pairs(d), x.shape[1]) or out.dtype != x.dtype or not out.is_contiguous() \
@@ -941,6 +952,7 @@ def moe_unpermute(d: Dims, rows: torch.Tensor, al: Alignment, topk_w: Optional[t
     if rows.dim() != 2 or rows.shape[0] != _pairs(d):
         raise ValueError(f"rows must be [{_pairs(d)}, width]")
     _check_alignment(d, al)
+    _no_tangent("moe_unpermute", rows, topk_w)
     if topk_w is not None:
         if topk_w.shape != (d.T, d.topk) or topk_w.dtype != torch.float32:
             raise ValueError(f"topk_w must be float32 [{d.T}, {d.topk}]")

@@ -2,6 +2,7 @@
 the movement of rows by expert: refused."""
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 from nvfp4_block_scaled_03_amd import ops
 
@@ -48,6 +49,31 @@ class _Calls:
 
 
 OPERATORS = ["rms_norm", "int8_quantize", "int8_linear", "int8_linear of bf16", "moe_permute", "moe_unpermute"]
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_forward_mode_derivatives_are_refused(dev, name):
+    """A tensor with a tangent: the result would come without one, a derivative of zero."""
+    c = _Calls(dev)
+    call, names = c.calls[name]
+    ref = call()
+    with forward_ad.dual_level():
+        for arg in names:
+            dual = forward_ad.make_dual(c.tensors[arg], torch.ones_like(c.tensors[arg]))
+            with pytest.raises(ValueError, match="forward-mode"):
+                call(**{arg: dual})
+            with torch.no_grad(), pytest.raises(ValueError, match="forward-mode"):    # (tangents live on there)
+                call(**{arg: dual})
+            assert torch.equal(call(**{arg: forward_ad.unpack_dual(dual).primal}), ref)
+        assert torch.equal(call(), ref)
+
+
+def test_a_jacobian_in_forward_mode_is_refused(dev):
+    c = _Calls(dev)
+    call, _ = c.calls["moe_permute"]
+    with pytest.raises(ValueError, match="forward-mode"):
+        torch.autograd.functional.jacobian(lambda x: call(x=x), c.tensors["x"].float(), strategy="forward-mode",
+                                           vectorize=True)
 
 
 @pytest.mark.parametrize("name", OPERATORS[:4])
