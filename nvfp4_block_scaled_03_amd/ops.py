@@ -662,6 +662,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     want_y, want_q = NORM_OUTPUTS[outputs]
     at_r = at_h = at_y = (None, 0)
     r_type = y_type = 0
+    given = []                 # the caller's tensors that are written
     if residual is not None:
         if residual.shape != (T, H):
             raise ValueError(f"residual must be [{T}, {H}]")
@@ -672,6 +673,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
         elif h.shape != (T, H) or h.dtype != residual.dtype or (at_h := _rows_at(h)) is None:
             raise ValueError(f"h must be [{T}, {H}] in the residual's type, with rows of consecutive elements, 16-byte "
                              "aligned, strides multiples of 8")
+        else:
+            given.append(h)
         at_r = _rows_at(residual)
         if at_r is None:
             residual = residual.clone(memory_format=torch.contiguous_format)
@@ -693,30 +696,39 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
         elif y.shape != (T, H) or (at_y := _rows_at(y)) is None:
             raise ValueError(f"y must be [{T}, {H}] with rows of consecutive elements, 16-byte aligned, strides multiples "
                              "of 8")
+        else:
+            given.append(y)
         y_type = _dtype_code(y)
     elif y is not None:
         raise ValueError(f"y is not made with outputs={outputs!r}")
     at_q = at_s = None
     if want_q:
-        q, s = _int8_rows(T, H, x.device, q, s)
+        q, s = _int8_rows(T, H, x.device, q, s, given)
         at_q, at_s = q.data_ptr(), s.data_ptr()
     elif q is not None or s is not None:
         raise ValueError(f"q and s are not made with outputs={outputs!r}")
     a = RmsNormArgs(*at_x, *at_r, at_w, *at_h, *at_y, at_q, at_s, _dtype_code(x), r_type, _dtype_code(weight), y_type,
                     eps)
     call("rms_norm", a, T, H, _raw_stream(dev))
+    if given:
+        _written(*given)
     return NormOut(y, h, q, s)
 
 
-def _int8_rows(T: int, H: int, device, q, s):
+def _int8_rows(T: int, H: int, device, q, s, given: list):
+    """q and s, checked or fresh; those of the caller join ``given``."""
     if q is None:
         q = torch.empty(T, H, dtype=torch.int8, device=device)
     elif q.shape != (T, H) or q.dtype != torch.int8 or not q.is_contiguous():
         raise ValueError(f"q must be contiguous int8 [{T}, {H}]")
+    else:
+        given.append(q)
     if s is None:
         s = torch.empty(T, dtype=torch.float32, device=device)
     elif s.shape != (T,) or s.dtype != torch.float32 or not s.is_contiguous():
         raise ValueError(f"s must be contiguous float32 [{T}]")
+    else:
+        given.append(s)
     return q, s
 
 
@@ -735,8 +747,11 @@ def int8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional
     if at is None:
         x = x.clone(memory_format=torch.contiguous_format)
         at = x.data_ptr(), K
-    q, s = _int8_rows(rows, K, x.device, q, s)
+    given = []
+    q, s = _int8_rows(rows, K, x.device, q, s, given)
     call("int8_quantize", at[0], _dtype_code(x), rows, K, at[1], q.data_ptr(), s.data_ptr(), _raw_stream(dev))
+    if given:
+        _written(*given)
     return q, s
 
 
@@ -807,7 +822,8 @@ def int8_linear(x: torch.Tensor, w: Int8LinearWeight, s: Optional[torch.Tensor] 
     if at_x is None or at_x[1] > 1 << 22:
         x = x.clone(memory_format=torch.contiguous_format)
         at_x = x.data_ptr(), K
-    if out is None:
+    fresh = out is None
+    if fresh:
         out = torch.empty(M, n_out, dtype=out_dtype, device=x.device)
     elif out.shape != (M, n_out) or not _rows4(out):
         raise ValueError(f"out must be [{M}, {n_out}] with rows of consecutive elements, starts and strides "
@@ -832,6 +848,8 @@ def int8_linear(x: torch.Tensor, w: Int8LinearWeight, s: Optional[torch.Tensor] 
     call("int8_linear", at_x[0], x_dtype, at_x[1], _ptr(s), M, N, K, w.prep.data_ptr(), w.s.data_ptr(), epi,
          out.data_ptr(), _dtype_code(out), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
          _raw_stream(dev))
+    if not fresh:
+        _written(out)
     return out
 
 
@@ -851,15 +869,20 @@ def _permute(d: Dims, x, offsets, inv_pos, out):
         at = x.data_ptr(), W
     call("moe_permute", d, at[0], _dtype_code(x), W, at[1], offsets.data_ptr(), inv_pos.data_ptr(),
          out.data_ptr(), int(fresh), _raw_stream(x.get_device()))
+    if not fresh:
+        _written(out)
     return out
 
 
 def _unpermute(d: Dims, rows, offsets, inv_pos, topk_w, out, out_dtype):
     W = rows.shape[1]
-    if out is None:
+    fresh = out is None
+    if fresh:
         out = torch.empty(d.T, W, dtype=out_dtype or rows.dtype, device=rows.device)
     call("moe_unpermute", d, rows.data_ptr(), _dtype_code(rows), W, offsets.data_ptr(), inv_pos.data_ptr(),
          _ptr(topk_w), out.data_ptr(), _dtype_code(out), _raw_stream(rows.get_device()))
+    if not fresh:
+        _written(out)
     return out
 
 
@@ -943,8 +966,7 @@ def moe_unpermute(d: Dims, rows: torch.Tensor, al: Alignment, topk_w: Optional[t
     pair (t, j), plus the shared expert's row (FP32, rounded once to
     ``out_dtype``, the rows' type by default).  ``rows`` [P, width] in moe_permute's
     order; without ``topk_w`` (float32 [T, topk]) every weight is 1.  Differentiable
-    in rows and topk_w (without ``out``), as moe_permute; a saved tensor that a call of this
-    module writes through ``out`` before the backward pass is not noticed."""
+    in rows and topk_w (without ``out``), as moe_permute."""
     dev = rows.get_device()
     if not _same_device(dev, al.offsets, al.inv_pos, topk_w, out):
         with torch.cuda.device(dev):

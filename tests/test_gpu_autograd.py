@@ -1,5 +1,5 @@
 """What autograd may take for differentiable in the norm, the int8 layers and
-the movement of rows by expert: refused."""
+the movement of rows by expert: refused, or noticed."""
 import pytest
 import torch
 from torch.autograd import forward_ad
@@ -100,3 +100,75 @@ def test_results_into_tensors_that_take_gradients_are_refused(dev):
                 lambda: ops.int8_linear(x.to(BF), w8, out=leaf(4, 32))):
         with pytest.raises(ValueError, match="no gradient"):
             bad()
+
+
+def _written_by(dev):
+    """(tensors, call that writes into them) for every operator with results of the caller's."""
+    g = torch.Generator(device=dev).manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=g, device=dev)
+    e = lambda *s, dt=F32: torch.zeros(*s, dtype=dt, device=dev)
+    x, w = r(4, 128), r(128)
+    xb = x.to(BF)
+    al_d = ops.dims(4, 2, 4, 128, 128)
+    al = ops.moe_align(al_d, torch.randint(0, 4, (4, 2), generator=g, device=dev, dtype=torch.int32))
+    w8, w8g = ops.quantize_int8_weight(r(64, 128)), ops.quantize_int8_weight(r(64, 128), gated=True)
+    cases = {}
+    y, h, q, s = e(4, 128), e(4, 128), e(4, 128, dt=torch.int8), e(4)
+    cases["rms_norm"] = ((y, h, q, s), lambda: ops.rms_norm(x, w, residual=x, outputs="both", y=y, h=h, q=q, s=s))
+    x2, r2 = x.clone(), x.clone()
+    cases["rms_norm in place"] = ((x2, r2), lambda: ops.rms_norm(x2, w, residual=r2, y=x2, h=r2))
+    q2, s2 = e(4, 128, dt=torch.int8), e(4)
+    cases["int8_quantize"] = ((q2, s2), lambda: ops.int8_quantize(x, q2, s2))
+    o1, o2, o3 = e(4, 64), e(4, 32, dt=BF), e(8, 64)
+    cases["int8_linear"] = ((o1,), lambda: ops.int8_linear(xb, w8, out=o1))
+    cases["int8_linear gated"] = ((o2,), lambda: ops.int8_linear(xb, w8g, act="silu", out=o2))
+    cases["int8_linear, some rows"] = ((o3,), lambda: ops.int8_linear(xb, w8, out=o3[2:6]))
+    p1, p2 = e(8, 128), e(4, 128)
+    cases["moe_permute"] = ((p1,), lambda: ops.moe_permute(al_d, x, al, out=p1))
+    rows = r(8, 128)
+    cases["moe_unpermute"] = ((p2,), lambda: ops.moe_unpermute(al_d, rows, al, out=p2))
+    return cases
+
+
+WRITERS = ["rms_norm", "rms_norm in place", "int8_quantize", "int8_linear", "int8_linear gated", "int8_linear, some rows",
+           "moe_permute", "moe_unpermute"]
+
+
+@pytest.mark.parametrize("name", WRITERS)
+def test_a_saved_tensor_written_over_is_noticed(dev, name):
+    """A product saves a tensor, a call writes into it: no gradient from the new values."""
+    tensors, call = _written_by(dev)[name]
+    for t in tensors:
+        if not t.is_floating_point():
+            before = t._version
+            call()
+            assert t._version > before
+            continue
+        leaf = torch.ones_like(t, requires_grad=True)
+        y = leaf * t
+        call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+        y = leaf * t                 # (written before it is saved: as ever)
+        y.sum().backward()
+        assert torch.equal(leaf.grad, t)
+
+
+def test_rows_saved_by_the_weighted_sum_and_written_over(dev):
+    d = ops.dims(5, 2, 4, 128, 128)
+    g = torch.Generator(device=dev).manual_seed(3)
+    al = ops.moe_align(d, torch.randint(0, 4, (5, 2), generator=g, device=dev, dtype=torch.int32))
+    rows, x = torch.randn(10, 64, generator=g, device=dev), torch.randn(5, 64, generator=g, device=dev)
+    w = torch.rand(5, 2, generator=g, device=dev, requires_grad=True)
+    out = ops.moe_unpermute(d, rows, al, w)
+    ops.moe_permute(d, x, al, out=rows)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+
+
+def test_inference_tensors_are_written(dev):
+    """Tensors made under inference_mode have no versions; a call outside writes them as before."""
+    with torch.inference_mode():
+        x, w, y = torch.randn(4, 64, device=dev), torch.ones(64, device=dev), torch.empty(4, 64, device=dev)
+    with torch.no_grad():
+        assert torch.equal(ops.rms_norm(x, w, y=y, out_dtype=F32).y, ops.rms_norm(x.clone(), w.clone(), out_dtype=F32).y)
