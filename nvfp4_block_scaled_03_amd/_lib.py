@@ -185,8 +185,7 @@ def last_error() -> str:
 
 def call(name: str, *args) -> int:
     """Call a status-returning entry point; raise Nvfp4Error on failure."""
-    lib = load()
-    rc = getattr(lib, name)(*args)
+    rc = getattr(_lib or load(), name)(*args)
     if rc != NVFP4_OK:
         raise Nvfp4Error(name, rc, last_error())
     return rc

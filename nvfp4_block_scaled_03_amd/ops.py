@@ -25,12 +25,14 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+_DTYPE_CODES = {torch.bfloat16: NVFP4_BF16, torch.float32: NVFP4_F32}
+
+
 def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
-        return NVFP4_BF16
-    if t.dtype == torch.float32:
-        return NVFP4_F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _need_cuda(*ts):
@@ -39,10 +41,9 @@ def _need_cuda(*ts):
             raise ValueError("tensors must live on the GPU")
 
 
-def _raw_stream(device: int) -> int:
-    """Handle of the device's current stream (torch.cuda.current_stream, whose
-    Python object alone takes 2.8 us, most of a short call)."""
-    return torch._C._cuda_getCurrentRawStream(device)
+# Handle of a device's current stream (torch.cuda.current_stream, whose Python
+# object alone takes 2.8 us, most of a short call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _same_device(device: int, *tensors) -> bool:
@@ -195,7 +196,7 @@ def route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias: Opt
     elif weights.shape != (T, k) or weights.dtype != torch.float32 or not weights.is_contiguous():
         raise ValueError("weights must be contiguous float32 [T, k]")
     else:
-        _written(weights)
+        _written((weights,))
     call("moe_route", params, logits.data_ptr(), _dtype_code(logits), ld, _ptr(bias), T, E, k, ids.data_ptr(),
          weights.data_ptr(), _raw_stream(dev))
     return ids, weights
@@ -210,17 +211,16 @@ class Alignment:
     workspace: torch.Tensor
 
 
-def _written(*ts):
-    """Tells autograd that the library wrote into tensors of the caller, which a
-    graph may have saved."""
-    torch._C._increment_version(ts)
+# Tells autograd that the library wrote into tensors of the caller (a sequence
+# of them), which a graph may have saved.
+_written = torch._C._increment_version
 
 
 def _alignment(d: Dims, al: Optional[Alignment], device) -> Alignment:
     """``al`` to be written anew, or a fresh one."""
     if al is None:
         return alloc_alignment(d, device)
-    _written(al.offsets, al.inv_pos)
+    _written((al.offsets, al.inv_pos))
     return al
 
 
@@ -601,8 +601,9 @@ def mx_linear(x: torch.Tensor, w: MxLinearWeight, out_dtype=torch.bfloat16, out:
 
 # ---------------------------------------------------------------- norm and int8 layers
 def _no_tangent(name: str, *tensors):
-    """Refuses tensors that carry a forward-mode tangent: the result would have none."""
-    if forward_ad._current_level >= 0 and torch._C._is_fwd_grad_enabled():
+    """Refuses tensors that carry a tangent of the forward-mode level there is
+    (callers look whether there is one): the result would have none."""
+    if torch._C._is_fwd_grad_enabled():
         for t in tensors:
             if t is not None and forward_ad.unpack_dual(t).tangent is not None:
                 raise ValueError(f"{name} has no forward-mode derivative: call it with the primal tensors")
@@ -614,7 +615,8 @@ def _no_gradient(name: str, *tensors):
         for t in tensors:
             if t is not None and t.requires_grad:
                 raise ValueError(f"{name} has no gradient: call it under torch.no_grad()")
-    _no_tangent(name, *tensors)
+    if forward_ad._current_level >= 0:
+        _no_tangent(name, *tensors)
 
 
 def _rows_at(t: torch.Tensor, unit: int = 8):
@@ -711,7 +713,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
                     eps)
     call("rms_norm", a, T, H, _raw_stream(dev))
     if given:
-        _written(*given)
+        _written(given)
     return NormOut(y, h, q, s)
 
 
@@ -751,7 +753,7 @@ def int8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional
     q, s = _int8_rows(rows, K, x.device, q, s, given)
     call("int8_quantize", at[0], _dtype_code(x), rows, K, at[1], q.data_ptr(), s.data_ptr(), _raw_stream(dev))
     if given:
-        _written(*given)
+        _written(given)
     return q, s
 
 
@@ -849,7 +851,7 @@ def int8_linear(x: torch.Tensor, w: Int8LinearWeight, s: Optional[torch.Tensor] 
          out.data_ptr(), _dtype_code(out), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
          _raw_stream(dev))
     if not fresh:
-        _written(out)
+        _written((out,))
     return out
 
 
@@ -870,7 +872,7 @@ def _permute(d: Dims, x, offsets, inv_pos, out):
     call("moe_permute", d, at[0], _dtype_code(x), W, at[1], offsets.data_ptr(), inv_pos.data_ptr(),
          out.data_ptr(), int(fresh), _raw_stream(x.get_device()))
     if not fresh:
-        _written(out)
+        _written((out,))
     return out
 
 
@@ -882,7 +884,7 @@ def _unpermute(d: Dims, rows, offsets, inv_pos, topk_w, out, out_dtype):
     call("moe_unpermute", d, rows.data_ptr(), _dtype_code(rows), W, offsets.data_ptr(), inv_pos.data_ptr(),
          _ptr(topk_w), out.data_ptr(), _dtype_code(out), _raw_stream(rows.get_device()))
     if not fresh:
-        _written(out)
+        _written((out,))
     return out
 
 
@@ -949,7 +951,8 @@ def moe_permute(d: Dims, x: torch.Tensor, al: Alignment, out: Optional[torch.Ten
     if x.dim() != 2 or x.shape[0] != d.T:
         raise ValueError(f"x must be [{d.T}, width]")
     _check_alignment(d, al)
-    _no_tangent("moe_permute", x)
+    if forward_ad._current_level >= 0:
+        _no_tangent("moe_permute", x)
     if out is not None:
         _no_gradient("moe_permute with out", x, out)
         if out.shape != (_pairs(d), x.shape[1]) or out.dtype != x.dtype or not out.is_contiguous() \
@@ -974,7 +977,8 @@ def moe_unpermute(d: Dims, rows: torch.Tensor, al: Alignment, topk_w: Optional[t
     if rows.dim() != 2 or rows.shape[0] != _pairs(d):
         raise ValueError(f"rows must be [{_pairs(d)}, width]")
     _check_alignment(d, al)
-    _no_tangent("moe_unpermute", rows, topk_w)
+    if forward_ad._current_level >= 0:
+        _no_tangent("moe_unpermute", rows, topk_w)
     if topk_w is not None:
         if topk_w.shape != (d.T, d.topk) or topk_w.dtype != torch.float32:
             raise ValueError(f"topk_w must be float32 [{d.T}, {d.topk}]")
@@ -1083,7 +1087,7 @@ class MxMoELayer:
 
     def forward(self, x, topk_ids, topk_w, out=None, out_dtype=torch.bfloat16, weights=None, marks=None):
         d, w, s = self.d, weights or self.w, _stream()
-        _written(self.al.offsets, self.al.inv_pos)
+        _written((self.al.offsets, self.al.inv_pos))
         if out is None:
             out = torch.empty(d.T, d.H, dtype=out_dtype, device=x.device)
         call("moe_mxfp4_quantize_and_align", ctypes.byref(d), _p(x), _p(self.a1_q), _p(self.a1_e), _p(topk_ids),
@@ -1195,7 +1199,7 @@ class MoELayer:
         GEMM1, between the GEMMs and after GEMM2 + combine."""
         d, w = self.d, weights or self.w
         self.x_last, self.tw_last = x, topk_w
-        _written(self.al.offsets, self.al.inv_pos)
+        _written((self.al.offsets, self.al.inv_pos))
         if out is None:
             out = torch.empty(d.T, d.H, dtype=out_dtype, device=x.device)
         s = _stream()
