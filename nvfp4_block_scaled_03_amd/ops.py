@@ -81,6 +81,8 @@ def global_scale(x: torch.Tensor, batches: int = 1, out: Optional[torch.Tensor] 
     wsb = lib.nvfp4_global_scale_workspace_size(batches, n)
     ws = torch.zeros(max(wsb, 16), dtype=torch.uint8, device=x.device)
     call("nvfp4_global_scale", _p(x), _dtype_code(x), batches, n, _p(g), _p(ws), wsb, _stream())
+    if out is not None:
+        _written((out,))
     return g
 
 
@@ -95,12 +97,15 @@ def quantize(x: torch.Tensor, g: torch.Tensor, rows_per_g: Optional[int] = None,
     if x2.stride(-1) != 1:
         x2 = x2.contiguous()
     rows = x2.shape[0]
+    given = [t for t in (q, sf, deq) if t is not None]
     if q is None:
         q = torch.empty(rows, K // 2, dtype=torch.uint8, device=x.device)
     if sf is None:
         sf = torch.empty(rows, K // 16, dtype=torch.uint8, device=x.device)
     call("nvfp4_quantize", _p(x2), _dtype_code(x2), rows, K, x2.stride(0), _p(g),
          rows if rows_per_g is None else rows_per_g, _p(q), _p(sf), _p(deq), _stream())
+    if given:
+        _written(given)
     return q, sf
 
 
@@ -136,13 +141,16 @@ def gate_logits(x: torch.Tensor, wg: torch.Tensor, bias: Optional[torch.Tensor] 
         if bias.shape != (E,) or bias.dtype != torch.float32:
             raise ValueError("bias must be float32 [E]")
         bias = bias.contiguous()
-    if out is None:
+    fresh = out is None
+    if fresh:
         out = torch.empty(T, E, dtype=torch.float32, device=x.device)
     elif out.shape != (T, E) or out.dtype != torch.float32 or not out.is_contiguous():
         raise ValueError("out must be contiguous float32 [T, E]")
     wg = wg.contiguous()
     call("moe_gate", at, ld, wg.data_ptr(), _dtype_code(wg), _ptr(bias), T, E, H, out.data_ptr(),
          _raw_stream(dev))
+    if not fresh:
+        _written((out,))
     return out
 
 
@@ -191,6 +199,8 @@ def route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias: Opt
         ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
     elif ids.shape != (T, k) or ids.dtype != torch.int32 or not ids.is_contiguous():
         raise ValueError("ids must be contiguous int32 [T, k]")
+    else:
+        _written((ids,))
     if weights is None:
         weights = torch.empty(T, k, dtype=torch.float32, device=logits.device)
     elif weights.shape != (T, k) or weights.dtype != torch.float32 or not weights.is_contiguous():
@@ -220,7 +230,7 @@ def _alignment(d: Dims, al: Optional[Alignment], device) -> Alignment:
     """``al`` to be written anew, or a fresh one."""
     if al is None:
         return alloc_alignment(d, device)
-    _written((al.offsets, al.inv_pos))
+    _written((al.offsets, al.inv_pos, al.sorted_pair))
     return al
 
 
@@ -274,6 +284,8 @@ def quantize_and_align(d: Dims, x: torch.Tensor, topk_ids: torch.Tensor, al: Opt
     call("moe_quantize_and_align", ctypes.byref(d), _p(x.contiguous()), _p(g), _p(gs_ws), wsb,
          _p(q), _p(sf), _p(deq), _p(topk_ids.contiguous()), _p(al.offsets), _p(al.sorted_pair),
          _p(al.inv_pos), _p(al.plan), _p(al.workspace), al.workspace.numel(), _stream())
+    if deq is not None:
+        _written((deq,))
     return g, q, sf, al
 
 
@@ -357,19 +369,25 @@ def gemm1_w4a4(d: Dims, a1_q, a1_sf, g1, al: Alignment, w: ExpertWeights, g2, a2
     optionally receives the decoded copy of a2."""
     P = d.T * d.topk + d.shared * d.T
     dev = g1.device
+    given = [t for t in (a2_q, a2_sf, a2_deq) if t is not None]
     a2_q = a2_q if a2_q is not None else torch.empty(max(P, 1), d.I // 2, dtype=torch.uint8, device=dev)
     a2_sf = a2_sf if a2_sf is not None else torch.empty(max(P, 1), d.I // 16, dtype=torch.uint8, device=dev)
     call("grouped_gemm1_swiglu", ctypes.byref(d), _p(a1_q), _p(a1_sf), _p(a1_deq), _p(g1),
          _p(al.sorted_pair), _p(al.offsets), _p(al.plan), _p(w.prep13), _p(w.g13), _p(g2),
          _p(a2_q), _p(a2_sf), _p(a2_deq), _stream())
+    if given:
+        _written(given)
     return a2_q, a2_sf
 
 
 def gemm1_w4a16(d: Dims, x, al: Alignment, w: ExpertWeights, a2=None):
     P = d.T * d.topk + d.shared * d.T
+    fresh = a2 is None
     a2 = a2 if a2 is not None else torch.empty(max(P, 1), d.I, dtype=torch.bfloat16, device=x.device)
     call("grouped_gemm1_swiglu_w4a16", ctypes.byref(d), _p(x), _p(al.sorted_pair), _p(al.offsets),
          _p(al.plan), _p(w.prep13), _p(w.g13), _p(a2), _stream())
+    if not fresh:
+        _written((a2,))
     return a2
 
 
@@ -381,11 +399,14 @@ def gemm_workspace(d: Dims, device) -> torch.Tensor:
 def gemm2_w4a4(d: Dims, a2_q, a2_sf, g2, al: Alignment, topk_w, w: ExpertWeights,
                out_dtype=torch.bfloat16, out=None, ws=None, a2_deq=None):
     dev = g2.device
+    fresh = out is None
     out = out if out is not None else torch.empty(d.T, d.H, dtype=out_dtype, device=dev)
     ws = ws if ws is not None else gemm_workspace(d, dev)
     call("grouped_gemm2_combine", ctypes.byref(d), _p(a2_q), _p(a2_sf), _p(a2_deq), _p(g2),
          _p(al.offsets), _p(al.inv_pos), _p(al.plan), _p(topk_w), _p(w.prep2), _p(w.g2), _p(out),
          _dtype_code(out), _p(ws), ws.numel() * 4, _stream())
+    if not fresh:
+        _written((out,))
     return out
 
 
@@ -396,17 +417,21 @@ def gemm2_w4a4_noalloc(d: Dims, a2_q, a2_sf, g2, al: Alignment, topk_w, w: Exper
     call("grouped_gemm2_combine_noalloc", ctypes.byref(d), _p(a2_q), _p(a2_sf), _p(a2_deq), _p(g2),
          _p(al.offsets), _p(al.inv_pos), _p(al.plan), _p(topk_w), _p(w.prep2), _p(w.g2), _p(out),
          _dtype_code(out), _stream())
+    _written((out,))
     return out
 
 
 def gemm2_w4a16(d: Dims, a2, al: Alignment, topk_w, w: ExpertWeights, out_dtype=torch.bfloat16,
                 out=None, ws=None):
     dev = a2.device
+    fresh = out is None
     out = out if out is not None else torch.empty(d.T, d.H, dtype=out_dtype, device=dev)
     ws = ws if ws is not None else gemm_workspace(d, dev)
     call("grouped_gemm2_combine_w4a16", ctypes.byref(d), _p(a2), _p(al.offsets), _p(al.inv_pos),
          _p(al.plan), _p(topk_w), _p(w.prep2), _p(w.g2), _p(out), _dtype_code(out), _p(ws),
          ws.numel() * 4, _stream())
+    if not fresh:
+        _written((out,))
     return out
 
 
@@ -486,7 +511,8 @@ def _linear_fused(name: str, x, w, scale, bias, act, residual, out_dtype, out, w
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
     M, n_out = x.shape[0], N // 2 if w.gated else N
-    if out is None:
+    fresh = out is None
+    if fresh:
         out = torch.empty(M, n_out, dtype=out_dtype, device=x.device)
     elif out.shape != (M, n_out) or not _rows4(out):
         raise ValueError(f"out must be [{M}, {n_out}] with rows of consecutive elements, starts and strides "
@@ -508,6 +534,8 @@ def _linear_fused(name: str, x, w, scale, bias, act, residual, out_dtype, out, w
     weight = (w.prep.data_ptr(),) if scale is None else (w.prep.data_ptr(), scale.data_ptr())
     call(name, x.data_ptr(), M, N, K, *weight, epi, out.data_ptr(), _dtype_code(out), ws.data_ptr(),
          ws.numel() * ws.element_size(), _raw_stream(dev))
+    if not fresh:
+        _written((out,))
     return out
 
 
@@ -530,10 +558,14 @@ def linear(x: torch.Tensor, w: LinearWeight, variant: str = "w4a4", out_dtype=to
         ws = ws if ws is not None else _linear_call_workspace(M, w.N, w.K, w4a4, True, x.device)
         return _linear_fused("nvfp4_linear_fused" if w4a4 else "nvfp4_linear_w4a16_fused", x, w, w.g, bias, act,
                              residual, out_dtype, out, ws)
-    out = out if out is not None else torch.empty(M, w.N, dtype=out_dtype, device=x.device)
+    fresh = out is None
+    if fresh:
+        out = torch.empty(M, w.N, dtype=out_dtype, device=x.device)
     ws = ws if ws is not None else _linear_call_workspace(M, w.N, w.K, w4a4, False, x.device)
     call("nvfp4_linear" if w4a4 else "nvfp4_linear_w4a16", _p(x.contiguous()), M, w.N, w.K, _p(w.prep),
          _p(w.g), _p(out), _dtype_code(out), _p(ws), ws.numel(), _stream())
+    if not fresh:
+        _written((out,))
     return out
 
 
@@ -546,9 +578,12 @@ def mx_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None, ex: Optional[
     if x2.stride(-1) != 1:
         x2 = x2.contiguous()
     rows = x2.shape[0]
+    given = [t for t in (q, ex) if t is not None]
     q = q if q is not None else torch.empty(rows, K // 2, dtype=torch.uint8, device=x.device)
     ex = ex if ex is not None else torch.empty(rows, K // 32, dtype=torch.uint8, device=x.device)
     call("mxfp4_quantize", _p(x2), _dtype_code(x2), rows, K, x2.stride(0), _p(q), _p(ex), _stream())
+    if given:
+        _written(given)
     return q, ex
 
 
@@ -592,10 +627,14 @@ def mx_linear(x: torch.Tensor, w: MxLinearWeight, out_dtype=torch.bfloat16, out:
     if bias is not None or act != "none" or residual is not None or w.gated:
         ws = ws if ws is not None else mx_linear_workspace(M, w.N, w.K, x.device)
         return _linear_fused("mxfp4_linear_fused", x, w, None, bias, act, residual, out_dtype, out, ws)
-    out = out if out is not None else torch.empty(M, w.N, dtype=out_dtype, device=x.device)
+    fresh = out is None
+    if fresh:
+        out = torch.empty(M, w.N, dtype=out_dtype, device=x.device)
     ws = ws if ws is not None else mx_linear_workspace(M, w.N, w.K, x.device)
     call("mxfp4_linear", _p(x.contiguous()), M, w.N, w.K, _p(w.prep), _p(out), _dtype_code(out), _p(ws),
          ws.numel(), _stream())
+    if not fresh:
+        _written((out,))
     return out
 
 
@@ -1087,8 +1126,9 @@ class MxMoELayer:
 
     def forward(self, x, topk_ids, topk_w, out=None, out_dtype=torch.bfloat16, weights=None, marks=None):
         d, w, s = self.d, weights or self.w, _stream()
-        _written((self.al.offsets, self.al.inv_pos))
-        if out is None:
+        _written((self.al.offsets, self.al.inv_pos, self.al.sorted_pair))
+        fresh = out is None
+        if fresh:
             out = torch.empty(d.T, d.H, dtype=out_dtype, device=x.device)
         call("moe_mxfp4_quantize_and_align", ctypes.byref(d), _p(x), _p(self.a1_q), _p(self.a1_e), _p(topk_ids),
              _p(self.al.offsets), _p(self.al.sorted_pair), _p(self.al.inv_pos), _p(self.al.plan),
@@ -1104,6 +1144,8 @@ class MxMoELayer:
             _p(self.al.offsets), _p(self.al.inv_pos), _p(self.al.plan), _p(topk_w), _p(w.prep2),
             _p(out), _dtype_code(out), _p(self.ws), self.ws.numel() * 4, part, st)
         _run_gemms(self.side, g1, g2, marks)
+        if not fresh:
+            _written((out,))
         return out
 
     def gemm1(self, weights=None):
@@ -1117,6 +1159,7 @@ class MxMoELayer:
         call("grouped_gemm2_combine_mxfp4", ctypes.byref(d), _p(self.a2_q), _p(self.a2_e),
              _p(self.al.offsets), _p(self.al.inv_pos), _p(self.al.plan), _p(topk_w), _p(w.prep2),
              _p(out), _dtype_code(out), _p(self.ws), self.ws.numel() * 4, _stream())
+        _written((out,))
 
 
 # ---------------------------------------------------------------- the layer
@@ -1192,6 +1235,7 @@ class MoELayer:
                  _p(self.al.offsets), _p(self.al.inv_pos), _p(self.al.plan), _p(tw),
                  _p(w.prep2), _p(w.g2), _p(out), _dtype_code(out), _p(self.ws),
                  self.ws.numel() * 4, s)
+        _written((out,))
 
     def forward(self, x, topk_ids, topk_w, variant: str = "w4a4", out=None,
                 out_dtype=torch.bfloat16, weights: Optional[ExpertWeights] = None, marks=None):
@@ -1199,8 +1243,9 @@ class MoELayer:
         GEMM1, between the GEMMs and after GEMM2 + combine."""
         d, w = self.d, weights or self.w
         self.x_last, self.tw_last = x, topk_w
-        _written((self.al.offsets, self.al.inv_pos))
-        if out is None:
+        _written((self.al.offsets, self.al.inv_pos, self.al.sorted_pair))
+        fresh = out is None
+        if fresh:
             out = torch.empty(d.T, d.H, dtype=out_dtype, device=x.device)
         s = _stream()
         if variant == "w4a4":
@@ -1241,6 +1286,8 @@ class MoELayer:
         else:
             raise ValueError(variant)
         _run_gemms(side, g1, g2, marks)
+        if not fresh:
+            _written((out,))
         return out
 
 

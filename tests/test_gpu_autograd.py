@@ -112,6 +112,8 @@ def _written_by(dev):
     al_d = ops.dims(4, 2, 4, 128, 128)
     al = ops.moe_align(al_d, torch.randint(0, 4, (4, 2), generator=g, device=dev, dtype=torch.int32))
     w8, w8g = ops.quantize_int8_weight(r(64, 128)), ops.quantize_int8_weight(r(64, 128), gated=True)
+    w4, w4g = ops.quantize_linear_weight(r(128, 128)), ops.quantize_linear_weight(r(256, 128), gated=True)
+    mx, mxg = ops.quantize_mx_weight(r(128, 128)), ops.quantize_mx_weight(r(256, 128), gated=True)
     cases = {}
     y, h, q, s = e(4, 128), e(4, 128), e(4, 128, dt=torch.int8), e(4)
     cases["rms_norm"] = ((y, h, q, s), lambda: ops.rms_norm(x, w, residual=x, outputs="both", y=y, h=h, q=q, s=s))
@@ -127,11 +129,63 @@ def _written_by(dev):
     cases["moe_permute"] = ((p1,), lambda: ops.moe_permute(al_d, x, al, out=p1))
     rows = r(8, 128)
     cases["moe_unpermute"] = ((p2,), lambda: ops.moe_unpermute(al_d, rows, al, out=p2))
+    l1, l2, l3, l4, l5 = (e(4, 128, dt=BF) for _ in range(5))
+    cases["linear"] = ((l1,), lambda: ops.linear(xb, w4, out=l1))
+    cases["linear w4a16"] = ((l5,), lambda: ops.linear(xb, w4, "w4a16", out=l5))
+    cases["linear gated"] = ((l2,), lambda: ops.linear(xb, w4g, act="silu", out=l2))
+    cases["mx_linear"] = ((l3,), lambda: ops.mx_linear(xb, mx, out=l3))
+    cases["mx_linear gated"] = ((l4,), lambda: ops.mx_linear(xb, mxg, act="silu", out=l4))
+    lo = e(4, 8)
+    cases["gate_logits"] = ((lo,), lambda: ops.gate_logits(xb, w.expand(8, 128).contiguous(), out=lo))
+    ids, tw = e(4, 2, dt=torch.int32), e(4, 2)
+    logits = r(4, 8)
+    cases["route_scored"] = ((ids, tw), lambda: ops.route_scored(logits, 2, ids=ids, weights=tw))
+    gs = e(1)
+    cases["global_scale"] = ((gs,), lambda: ops.global_scale(x, out=gs))
+    one = torch.ones(1, device=dev)
+    c4, s4, d4 = e(4, 64, dt=torch.uint8), e(4, 8, dt=torch.uint8), e(4, 128, dt=torch.float16)
+    cases["quantize"] = ((c4, s4, d4), lambda: ops.quantize(xb, one, q=c4, sf=s4, deq=d4))
+    cm, em = e(4, 64, dt=torch.uint8), e(4, 4, dt=torch.uint8)
+    cases["mx_quantize"] = ((cm, em), lambda: ops.mx_quantize(xb, cm, em))
+    d4b = e(4, 128, dt=torch.float16)
+    chosen = torch.randint(0, 4, (4, 2), generator=g, device=dev, dtype=torch.int32)
+    share = torch.full((4, 2), 0.5, device=dev)
+    cases["quantize_and_align"] = ((d4b,), lambda: ops.quantize_and_align(al_d, xb, chosen, deq=d4b))
+    al2 = ops.moe_align(al_d, chosen)
+    cases["moe_align"] = ((al2.offsets, al2.inv_pos, al2.sorted_pair), lambda: ops.moe_align(al_d, chosen, al2))
+    w13, w2 = r(4, 256, 128), r(4, 128, 128)
+    we, wm = ops.quantize_expert_weights(al_d, w13, w2), ops.quantize_mx_expert_weights(al_d, w13, w2)
+    layer, mxl = ops.MoELayer(al_d, we, one), ops.MxMoELayer(al_d, wm)
+    f1, f2, f3, f4, f5, f6, f7 = (e(4, 128, dt=BF) for _ in range(7))
+    cases["MoELayer"] = ((f1,), lambda: layer.forward(xb, chosen, share, out=f1))
+    cases["MoELayer w4a16"] = ((f2,), lambda: layer.forward(xb, chosen, share, "w4a16", out=f2))
+    cases["MxMoELayer"] = ((f3,), lambda: mxl.forward(xb, chosen, share, out=f3))
+    a2 = e(8, 128, dt=BF)
+    cases["gemm1_w4a16"] = ((a2,), lambda: ops.gemm1_w4a16(al_d, xb, al2, we, a2=a2))
+    filled = ops.gemm1_w4a16(al_d, xb, al2, we)
+    cases["gemm2_w4a16"] = ((f4,), lambda: ops.gemm2_w4a16(al_d, filled, al2, share, we, out=f4))
+    g1, q1, sf1, al3 = ops.quantize_and_align(al_d, xb, chosen)
+    g2 = one
+    q2b, sf2b, deq2 = e(8, 64, dt=torch.uint8), e(8, 8, dt=torch.uint8), e(8, 128, dt=torch.float16)
+    cases["gemm1_w4a4"] = ((q2b, sf2b, deq2), lambda: ops.gemm1_w4a4(al_d, q1, sf1, g1, al3, we, g2, q2b, sf2b,
+                                                                     a2_deq=deq2))
+    q2f, sf2f = ops.gemm1_w4a4(al_d, q1, sf1, g1, al3, we, g2)
+    cases["gemm2_w4a4"] = ((f5,), lambda: ops.gemm2_w4a4(al_d, q2f, sf2f, g2, al3, share, we, out=f5))
+    cases["gemm2_w4a4_noalloc"] = ((f6,), lambda: ops.gemm2_w4a4_noalloc(al_d, q2f, sf2f, g2, al3, share, we, f6))
+
+    def second(o):
+        layer.forward(xb, chosen, share, "w4a16")
+        layer.gemm2("w4a16", o)
+
+    cases["MoELayer.gemm2"] = ((f7,), lambda: second(f7))
     return cases
 
 
 WRITERS = ["rms_norm", "rms_norm in place", "int8_quantize", "int8_linear", "int8_linear gated", "int8_linear, some rows",
-           "moe_permute", "moe_unpermute"]
+           "moe_permute", "moe_unpermute", "linear", "linear w4a16", "linear gated", "mx_linear", "mx_linear gated",
+           "gate_logits", "route_scored", "global_scale", "quantize", "mx_quantize", "quantize_and_align", "moe_align",
+           "MoELayer", "MoELayer w4a16", "MxMoELayer", "gemm1_w4a16", "gemm2_w4a16", "gemm1_w4a4", "gemm2_w4a4",
+           "gemm2_w4a4_noalloc", "MoELayer.gemm2"]
 
 
 @pytest.mark.parametrize("name", WRITERS)
