@@ -480,8 +480,8 @@ int int8_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ldx
  * (so that no sum passes 31 bits), bfloat16 x at most 32768; N K <= 2^35; ldx at
  * most 2^22; M <= 2^24, M N <= 2^40.  A row or column whose scale is NaN gives NaN.
  * ws: int8_linear_workspace_size(M, N, K, x_dtype) bytes, 256-byte aligned, no
- * initial contents; it serves every call of fewer rows, and bfloat16's serves
- * int8 codes too. */
+ * initial contents; it serves every call of fewer rows, and bfloat16's, where K
+ * admits bfloat16 rows, serves int8 codes too.  The size is 0 for what is refused. */
 size_t int8_prep_weights_size(int64_t N, int64_t K, int gated);
 int int8_prep_weights(int64_t N, int64_t K, int gated, const int8_t* q, uint8_t* prep, void* stream);
 size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int x_dtype);

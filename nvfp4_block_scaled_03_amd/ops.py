@@ -829,8 +829,12 @@ def quantize_int8_weight(w: torch.Tensor, gated: bool = False) -> Int8LinearWeig
 
 
 def int8_linear_workspace(M: int, N: int, K: int, device) -> torch.Tensor:
-    """Workspace of every ``int8_linear`` of up to M rows with a weight [N, K]."""
-    n = _lib.load().int8_linear_workspace_size(M, N, K, NVFP4_BF16)
+    """Workspace of every ``int8_linear`` of up to M rows with a weight [N, K]
+    (beyond K = 32768 of int8 codes, which alone are taken there)."""
+    lib = _lib.load()
+    n = max(lib.int8_linear_workspace_size(M, N, K, t) for t in (NVFP4_BF16, NVFP4_I8))
+    if n == 0 and (M != 0 or lib.int8_prep_weights_size(N, K, 0) == 0):
+        raise ValueError(f"int8_linear takes no M={M} N={N} K={K}")
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
