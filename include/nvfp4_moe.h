@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define NVFP4_MOE_ABI_VERSION 12
+#define NVFP4_MOE_ABI_VERSION 13
 
 /* Status codes. */
 #define NVFP4_OK 0
@@ -488,6 +488,12 @@ size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int x_dtype);
 int int8_linear(const void* x, int x_dtype, int64_t ldx, const float* sx, int64_t M, int64_t N, int64_t K,
                 const uint8_t* w_prep, const float* sw, const nvfp4_epilogue* epi, void* out, int out_dtype, void* ws,
                 size_t ws_bytes, void* stream);
+/* The launches that such a call makes, for tests and profiles (host only): plan
+ * int32 [9], their number (1 or 2), then for each the rows and columns of its
+ * tiles (0, 0: the kernel for a handful of rows), the parts of K, and the first
+ * of its columns in the weight's own layout (a gated layer's gate and up in
+ * alternate tiles of 16). */
+int int8_linear_plan(int64_t M, int64_t N, int64_t K, int gated, int32_t* plan);
 
 /* ------------------------------------------------------------------------ */
 /* Rows by expert and back, with gradients.                                  */

@@ -13,7 +13,7 @@ from ctypes import c_char_p, c_int, c_int32, c_int64, c_size_t, c_void_p
 # variant with different tile settings); the default is the in-tree build.
 LIB_PATH = os.environ.get("NVFP4_MOE_LIB") or os.path.join(
     os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
-ABI_VERSION = 12
+ABI_VERSION = 13
 
 NVFP4_OK = 0
 NVFP4_EINVAL = -1
@@ -130,6 +130,7 @@ SIGNATURES = {
     "int8_prep_weights_size": (c_size_t, [c_int64, c_int64, c_int]),
     "int8_prep_weights": (c_int, [c_int64, c_int64, c_int, c_void_p, c_void_p, c_void_p]),
     "int8_linear_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int]),
+    "int8_linear_plan": (c_int, [c_int64, c_int64, c_int64, c_int, c_void_p]),
     "int8_linear": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, _E,
                             c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
     "moe_permute": (c_int, [_P, c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_void_p]),

@@ -1111,6 +1111,25 @@ size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int x_dtype) 
   return part + (x_dtype == NVFP4_BF16 ? int8_ws_codes(M, K) + up256((size_t)M * 4) : 0);
 }
 
+int int8_linear_plan(int64_t M, int64_t N, int64_t K, int gated, int32_t* plan) {
+  const char* W = "int8_linear_plan";
+  if (!plan) return fail(NVFP4_EINVAL, "%s: EINVAL null pointer", W);
+  if (!int8_shape_ok(M, N, K, NVFP4_I8, gated) || M < 1)
+    return fail(NVFP4_ESHAPE, "%s: ESHAPE M=%lld N=%lld K=%lld gated=%d (a shape that int8_linear takes, M >= 1)", W,
+                (long long)M, (long long)N, (long long)K, gated);
+  nvfp4::Int8Step step[2];
+  const int n = nvfp4::int8_plan(M, N, K, gated != 0, step);
+  for (int i = 0; i < 9; ++i) plan[i] = 0;
+  plan[0] = n;
+  for (int i = 0; i < n; ++i) {
+    plan[1 + 4 * i] = step[i].rows;
+    plan[2 + 4 * i] = step[i].columns;
+    plan[3 + 4 * i] = step[i].parts;
+    plan[4 + 4 * i] = (int32_t)step[i].col0;
+  }
+  return ok();
+}
+
 int int8_linear(const void* x, int x_dtype, int64_t ldx, const float* sx, int64_t M, int64_t N, int64_t K,
                 const uint8_t* w_prep, const float* sw, const nvfp4_epilogue* epi, void* out, int out_dtype, void* ws,
                 size_t ws_bytes, void* stream) {

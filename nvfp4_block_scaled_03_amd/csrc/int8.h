@@ -55,4 +55,12 @@ struct Int8Args {
 size_t int8_part_bytes(int64_t M, int64_t N, bool gated);
 hipError_t launch_int8_linear(const Int8Args& a, hipStream_t s);
 
+// The launches of a call: its streaming columns [col0, col0 + cols) in tiles of
+// rows x columns, K in parts (kind -1: the kernel for a handful of rows).
+struct Int8Step {
+  int kind, rows, columns, parts;
+  int64_t col0, cols;
+};
+int int8_plan(int64_t M, int64_t N, int64_t K, bool gated, Int8Step (&step)[2]);
+
 }  // namespace nvfp4

@@ -469,25 +469,44 @@ hipError_t launch_kind(const Int8Args& p, int kind, int parts, int64_t col0, int
 
 template <bool GATED>
 hipError_t launch_chosen(const Int8Args& p, hipStream_t s) {
-  const int64_t columns = int8_tiles(p.N, GATED) * 16;
-  const Choice one = choose(p.M, columns, p.K);
-  if (p.M <= kFewRows && few_cost(p.M, columns, p.K) < one.cost) return launch_few_t<GATED, 2, 8>(p, s);
-  // Whole rounds of 256 x 256 tiles, and the columns left over by another kernel
-  // (4096 x 5120 x 17408: 393 us in 256 x 256 tiles, 347 in 256 x 128, 312 so: 231 for
-  // 4096 columns and 81 for 1024, in 256 x 128 tiles with K in two parts).
-  const int64_t rb = (p.M + 255) / 256, cb = (columns + 255) / 256, whole = rb * cb / 256 * 256 / rb;
-  if (whole > 0 && whole < cb) {
-    const int64_t rest = columns - whole * 256;
-    const Choice two = choose(p.M, rest, p.K);
-    if (tile_cost(kTiles[kTileKinds - 1], p.M, whole * 256, p.K, 1) + two.cost < one.cost) {
-      const hipError_t e = launch_kind<GATED>(p, kTileKinds - 1, 1, 0, whole * 256, s);
-      return e != hipSuccess ? e : launch_kind<GATED>(p, two.kind, two.parts, whole * 256, rest, s);
-    }
-  }
-  return launch_kind<GATED>(p, one.kind, one.parts, 0, columns, s);
+  Int8Step step[2];
+  const int n = int8_plan(p.M, p.N, p.K, GATED, step);
+  if (step[0].kind < 0) return launch_few_t<GATED, 2, 8>(p, s);
+  for (int i = 0; i < n; ++i)
+    if (const hipError_t e = launch_kind<GATED>(p, step[i].kind, step[i].parts, step[i].col0, step[i].cols, s);
+        e != hipSuccess)
+      return e;
+  return hipSuccess;
 }
 
 }  // namespace
+
+int int8_plan(int64_t M, int64_t N, int64_t K, bool gated, Int8Step (&step)[2]) {
+  auto set = [](Int8Step& s, int kind, int parts, int64_t col0, int64_t cols) {
+    s = {kind, kind < 0 ? 0 : kTiles[kind].bm, kind < 0 ? 0 : kTiles[kind].bn, parts, col0, cols};
+  };
+  const int64_t columns = int8_tiles(N, gated) * 16;
+  const Choice one = choose(M, columns, K);
+  if (M <= kFewRows && few_cost(M, columns, K) < one.cost) {
+    set(step[0], -1, 1, 0, columns);
+    return 1;
+  }
+  // Whole rounds of 256 x 256 tiles, and the columns left over by another kernel
+  // (4096 x 5120 x 17408: 393 us in 256 x 256 tiles, 347 in 256 x 128, 312 so: 231 for
+  // 4096 columns and 81 for 1024, in 256 x 128 tiles with K in two parts).
+  const int64_t rb = (M + 255) / 256, cb = (columns + 255) / 256, whole = rb * cb / 256 * 256 / rb;
+  if (whole > 0 && whole < cb) {
+    const int64_t rest = columns - whole * 256;
+    const Choice two = choose(M, rest, K);
+    if (tile_cost(kTiles[kTileKinds - 1], M, whole * 256, K, 1) + two.cost < one.cost) {
+      set(step[0], kTileKinds - 1, 1, 0, whole * 256);
+      set(step[1], two.kind, two.parts, whole * 256, rest);
+      return 2;
+    }
+  }
+  set(step[0], one.kind, one.parts, 0, columns);
+  return 1;
+}
 
 size_t int8_prep_bytes(int64_t N, int64_t K, bool gated) {
   return (size_t)int8_tiles(N, gated) * (size_t)int8_chunks(K) * 1024;
