@@ -428,7 +428,8 @@ int mxfp4_linear(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8
  * may be the residual or x itself (same type and stride), and y may be x itself;
  * outputs must not overlap inputs or each other otherwise.
  * The sum of squares, the norm's factor and the scale are FP64, decisions of
- * codes exact (v is exact in FP64).  A row of zeros has codes and scale 0.  A
+ * codes exact (v is exact in FP64).  A row of zeros has codes and scale 0; with
+ * eps = 0 its factor is infinite and its y and scale are NaN, as 0 / 0 is.  A
  * row with NaN or infinity in h or v has scale NaN (its codes mean nothing), so
  * that what is computed from it is NaN too.
  * Types bfloat16 or float32, each its own.  H a multiple of 8, at most 32768;

@@ -122,7 +122,8 @@ __device__ __forceinline__ void row_reduce(Gathered& g, Gathered* red) {
   }
 }
 
-// 1 / sqrt(x) by two Newton steps on the hardware's estimate (2^-14 or better).
+// 1 / sqrt(x) by Newton steps on the hardware's estimate (2^-14 or better): two reach
+// 2^-54 but for their own roundings, which a third takes back.
 __device__ __forceinline__ double rsqrt64(double x) {
   const double y0 = __builtin_amdgcn_rsq(x), hx = 0.5 * x;
   double y = y0 * __builtin_fma(-hx * y0, y0, 1.5);
