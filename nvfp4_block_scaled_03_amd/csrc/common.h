@@ -22,6 +22,12 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWave = 64;
 
+// Leads the assembly of a direct load into LDS.  M0 holds the LDS address; an
+// instruction has to lie between its write and the load that reads it, and the
+// compiler, which puts the write right in front of the assembly, adds that wait
+// for loads of its own only.
+#define NVFP4_M0_WAIT "s_nop 0\n\t"
+
 // ---------------------------------------------------------------------------
 // Cross-lane helpers (DPP within rows of 16 lanes).
 // ---------------------------------------------------------------------------

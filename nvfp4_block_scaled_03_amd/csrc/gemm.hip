@@ -717,7 +717,7 @@ void grouped_gemm_wide_kernel(KParams p) {
       if (4 * (wv * LOADS + q) >= 16 * decltype(mta)::value) continue;  // rows no m-tile reads
       const uint32_t lds = (uint32_t)(uintptr_t)(buf + (wv * LOADS + q) * 1024);
       const uint32_t voff = a_off[q] + (uint32_t)kc * ROW_BYTES;
-      asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(a_base), "{m0}"(lds) : "memory");
+      asm volatile(NVFP4_M0_WAIT "global_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(a_base), "{m0}"(lds) : "memory");
     }
   };
   // (builtin, not assembly: the compiler must see that every load, its own

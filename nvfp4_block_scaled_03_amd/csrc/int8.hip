@@ -218,17 +218,17 @@ void int8_tile_kernel(Int8Args p, int nb0, int TNB, int S) {
     const uint8_t* const ws = w0 + (int64_t)c * 2048;
 #pragma unroll
     for (int q = 0; q < PA; ++q)
-      asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(ra[q] + min(ua[q], last)), "s"(as),
+      asm volatile(NVFP4_M0_WAIT "global_load_lds_dwordx4 %0, %1" : : "v"(ra[q] + min(ua[q], last)), "s"(as),
                    "{m0}"(base + (wv * PA + q) * 1024) : "memory");
     if (TMB == 1) {   // weights that are read once pass the caches by
 #pragma unroll
       for (int q = 0; q < PB; ++q)
-        asm volatile("global_load_lds_dwordx4 %0, %1 nt" : : "v"(vb[q]), "s"(ws),
+        asm volatile(NVFP4_M0_WAIT "global_load_lds_dwordx4 %0, %1 nt" : : "v"(vb[q]), "s"(ws),
                      "{m0}"(base + LA * 1024 + (wv * PB + q) * 1024) : "memory");
     } else {
 #pragma unroll
       for (int q = 0; q < PB; ++q)
-        asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(vb[q]), "s"(ws),
+        asm volatile(NVFP4_M0_WAIT "global_load_lds_dwordx4 %0, %1" : : "v"(vb[q]), "s"(ws),
                      "{m0}"(base + LA * 1024 + (wv * PB + q) * 1024) : "memory");
     }
   };

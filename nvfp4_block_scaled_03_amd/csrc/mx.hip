@@ -204,17 +204,17 @@ __global__ __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(WM, WM
     const uint32_t base = ring0 + (uint32_t)slot * R::Slot;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
-      asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(va[t] + (uint32_t)kc * 1024u), "s"(a_q),
+      asm volatile(NVFP4_M0_WAIT "global_load_lds_dwordx4 %0, %1" : : "v"(va[t] + (uint32_t)kc * 1024u), "s"(a_q),
                    "{m0}"(base + R::A + (2 * wv + t) * 1024) : "memory");
 #pragma unroll
     for (int t = 0; t < NBW; ++t)
-      asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(vb[t] + (uint32_t)kc * 1024u), "s"(w_prep),
+      asm volatile(NVFP4_M0_WAIT "global_load_lds_dwordx4 %0, %1" : : "v"(vb[t] + (uint32_t)kc * 1024u), "s"(w_prep),
                    "{m0}"(base + R::B + (wv * NBW + t) * 1024) : "memory");
     if (WM == 1 || wv < 4)
-      asm volatile("global_load_lds_dword %0, %1" : : "v"(vsa + (uint32_t)kc * 256u), "s"(a_e),
+      asm volatile(NVFP4_M0_WAIT "global_load_lds_dword %0, %1" : : "v"(vsa + (uint32_t)kc * 256u), "s"(a_e),
                    "{m0}"(base + R::As + wv * 256) : "memory");
     if (WM == 1 || wv >= 4)
-      asm volatile("global_load_lds_dword %0, %1" : : "v"(vsb + (uint32_t)kc * 256u), "s"(w_sc),
+      asm volatile(NVFP4_M0_WAIT "global_load_lds_dword %0, %1" : : "v"(vsb + (uint32_t)kc * 256u), "s"(w_sc),
                    "{m0}"(base + R::Bs + qb * 256) : "memory");
   };
 
@@ -883,17 +883,17 @@ __global__ __launch_bounds__(256) void grouped_mx_kernel(MxMoeParams p) {
 #pragma unroll
       for (int u = 0; u < AW; ++u) {
         const int i = MT >= 4 ? wv + 4 * u : wv;
-        asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(va[u] + (uint32_t)kc * 64u), "s"(p.a_q),
+        asm volatile(NVFP4_M0_WAIT "global_load_lds_dwordx4 %0, %1" : : "v"(va[u] + (uint32_t)kc * 64u), "s"(p.a_q),
                      "{m0}"(base + R::A + i * 1024) : "memory");
-        asm volatile("global_load_lds_dword %0, %1" : : "v"(vae[u] + (uint32_t)kc * 4u), "s"(p.a_e),
+        asm volatile(NVFP4_M0_WAIT "global_load_lds_dword %0, %1" : : "v"(vae[u] + (uint32_t)kc * 4u), "s"(p.a_e),
                      "{m0}"(base + R::Ae + i * 256) : "memory");
       }
     }
 #pragma unroll
     for (int t = 0; t < NTW; ++t)
-      asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(vb[t] + (uint32_t)kc * 1024u), "s"(wq),
+      asm volatile(NVFP4_M0_WAIT "global_load_lds_dwordx4 %0, %1" : : "v"(vb[t] + (uint32_t)kc * 1024u), "s"(wq),
                    "{m0}"(base + R::B + (wv * NTW + t) * 1024) : "memory");
-    asm volatile("global_load_lds_dword %0, %1" : : "v"(vbs + (uint32_t)kc * 256u), "s"(ws),
+    asm volatile(NVFP4_M0_WAIT "global_load_lds_dword %0, %1" : : "v"(vbs + (uint32_t)kc * 256u), "s"(ws),
                  "{m0}"(base + R::Bs + wv * 256) : "memory");
   };
 

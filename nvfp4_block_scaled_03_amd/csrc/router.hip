@@ -106,7 +106,7 @@ __global__ __launch_bounds__(WR * WC * KW * kWave) void gate_kernel(const uint16
     c = min(c * KW + kw, chunks - 1);                // past the end: the last chunk, not used
 #pragma unroll
     for (int q = 0; q < LPW; ++q)
-      asm volatile("global_load_lds_dwordx4 %0, off" : : "v"(src[q] + (uint64_t)c * step[q]),
+      asm volatile(NVFP4_M0_WAIT "global_load_lds_dwordx4 %0, off" : : "v"(src[q] + (uint64_t)c * step[q]),
                    "{m0}"(ring + slot * STAGE + (wg_i * LPW + q) * 1024) : "memory");
   };
 
