@@ -155,8 +155,12 @@ hipError_t launch_few_t(const Int8Args& p, hipStream_t s) {
 constexpr int kMaxParts = 4;                          // of K
 constexpr int64_t kPartBytes = int64_t(64) << 20;     // their sums, at most
 
-// s_waitcnt immediate: at most n vector memory operations outstanding.
-constexpr int wait_loads(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+// s_waitcnt immediate: at most n vector memory operations outstanding, and no LDS
+// read (the export counter left at its maximum).  The reads are not left to the
+// barrier behind: four kernels (128 x 64 and 64 x 256 tiles with K in parts) came out
+// of the compiler without its wait for them, so that a wavefront passed the barrier
+// with up to four reads of the slot that is refilled next on their way.
+constexpr int wait_loads(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
 
 template <bool GATED, bool SPLIT, int WR, int WC, int TM, int TN, int D, int OCC>
 __global__ __launch_bounds__(WR * WC * 64) __attribute__((amdgpu_waves_per_eu(WR * WC * OCC / 4, WR * WC * OCC / 4)))

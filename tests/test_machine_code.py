@@ -82,3 +82,70 @@ def test_direct_loads_wait_for_the_lds_address(kernels):
                 j -= 1
     assert loads > 0
     assert not early, f"{len(early)} of {loads} loads, e.g. {early[:3]}"
+
+
+def _blocks(code):
+    """(label or None, instructions) runs; a branch ends its run."""
+    out = [[None, []]]
+    for line in code:
+        if line.endswith(":"):
+            out.append([line[:-1], []])
+            continue
+        out[-1][1].append(line)
+        if line.startswith(("s_branch", "s_cbranch", "s_endpgm")):
+            out.append([None, []])
+    return out
+
+
+def _outstanding_at_barriers(code):
+    """Most LDS accesses that a wavefront may have outstanding at each barrier:
+    data flow over its branches, where a wait for n leaves n at most."""
+    blocks = _blocks(code)
+    at = {label: i for i, (label, _) in enumerate(blocks) if label}
+    entry = [-1] * len(blocks)
+    entry[0] = 0
+    work, found = [0], {}
+    while work:
+        i = work.pop()
+        n, following = entry[i], [i + 1] if i + 1 < len(blocks) else []
+        for k, line in enumerate(blocks[i][1]):
+            name = line.split()[0]
+            if name.startswith("ds_"):
+                n = min(n + 1, 16)
+            elif name == "s_waitcnt":
+                m = re.search(r"lgkmcnt\((\d+)\)", line)
+                n = min(n, int(m[1])) if m else n
+            elif name == "s_barrier":
+                found[(i, k)] = max(n, found.get((i, k), 0))
+            elif name == "s_branch":
+                following = [at[line.split()[1]]]
+            elif name.startswith("s_cbranch"):
+                following = following + [at[line.split()[1]]]
+            elif name == "s_endpgm":
+                following = []
+        for j in following:
+            if n > entry[j]:
+                entry[j] = n
+                work.append(j)
+    return found
+
+
+def test_no_lds_access_is_outstanding_at_a_barrier(kernels):
+    """What stands behind a barrier may write what was read in front of it."""
+    barriers, open_ = 0, {}
+    for name, code in kernels.items():
+        found = _outstanding_at_barriers(code)
+        barriers += len(found)
+        if any(found.values()):
+            open_[name] = max(found.values())
+    assert barriers > 0
+    assert not open_, open_
+
+
+def test_the_reading_of_barriers():
+    """A loop whose last read is awaited only behind the barrier of the next trip."""
+    trip = ["L0:", "s_waitcnt vmcnt(6)", "s_barrier", "s_waitcnt lgkmcnt(0)", "ds_read_b128 v[0:3], v4", "s_cbranch_scc1 L0",
+            "s_endpgm"]
+    assert list(_outstanding_at_barriers(trip).values()) == [1]
+    trip[1] = "s_waitcnt vmcnt(6) lgkmcnt(0)"
+    assert list(_outstanding_at_barriers(trip).values()) == [0]
