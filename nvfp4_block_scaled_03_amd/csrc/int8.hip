@@ -388,9 +388,9 @@ hipError_t launch_tile_t(const Int8Args& p, int nb0, int nbs, int S, hipStream_t
 // 4096 M = 32 9.3 / 10.6 / 11.4 / 15.5 / - / -, M = 512 42 / 26.5 / 18.9 / 17.7 /
 // 30.5 / 54, M = 4096 - / - / - / 102 / 76 / 65; 128 x 64 or 64 x 64 against 128 x 256
 // or 64 x 256: 34816 x 5120 M = 64 44.6 / 40.9, M = 128 59.9 / 48.2, M = 384 92.8 /
-// 87.5; K in 1 / 2 / 4 parts: 5120 x 17408 M = 16 30.2 / 22.3 / 25.8 (16 x 64), M =
-// 128 60.6 / 37.5 / 40.1 (128 x 64), and M = 384 62.6 in 256 x 128 tiles, 46.3 in 128
-// x 256 with 4 parts.
+// 87.5; K in 1 / 2 / 3 / 4 parts: 5120 x 17408 M = 16 30.2 / 22.3 / 20.6 / 25.8 (16 x
+// 64), M = 128 60.6 / 37.5 / 31.0 / 40.1 (128 x 64), and M = 384 62.6 in 256 x 128
+// tiles, 45.6 in 128 x 256 with 4 parts.
 // ---------------------------------------------------------------------------
 struct TileCost {
   int bm, bn, occ;

@@ -324,8 +324,8 @@ hipError_t launch_rows_t(const NormArgs& a, hipStream_t s) {
   }
   return hipSuccess;
 }
-// Threads and pieces a thread.  A piece a thread for the latency (H = 5120, both
-// outputs, us: 1 row 256 x 3 6.4, 512 x 2 4.7, 1024 x 1 4.2) as long as the workgroups
+// Threads and pieces a thread ("codes alone" are int8_quantize's).  A piece a thread
+// for the latency (H = 5120, both outputs, us: 1 row 256 x 3 6.4, 512 x 2 4.7, 1024 x 1 4.2) as long as the workgroups
 // take turns in loading and reducing (both outputs / codes alone: 1024 rows of 8192
 // 256 x 4 23.7 / 9.5, 1024 x 1 20.1 / 9.5; 4096 rows of 4096 256 x 2 35.6 / 13.9, 512 x
 // 1 32.2 / 14.8; 16384 rows of 2048 64 x 4 68.7 / 21.6, 256 x 1 59.4 / 27.0).  Fewer
@@ -333,7 +333,11 @@ hipError_t launch_rows_t(const NormArgs& a, hipStream_t s) {
 // and for the codes alone, whose rows have a third of the bytes (16384 rows of 1024 64
 // x 2 35.5 / 13.2, 256 x 1 39.1 / 20.8; of 5120 256 x 3 151.6 / 47.7, 1024 x 1 155.6 /
 // 77.7), and for long ones, which do not fit a piece a thread (4096 rows of 16384 512 x
-// 4 125.8 / 36.2, 1024 x 2 137.4 / 43.1).  151.6 us are 755 MB at 5.0 TB/s.
+// 4 125.8 / 36.2, 1024 x 2 137.4 / 43.1).  151.6 us are 755 MB at 5.0 TB/s.  8192 rows of
+// 4096, both outputs: 512 x 1 57, 256 x 2 60, with one set of inputs or with twelve
+// (3.6 GB, past any cache).  rms_norm takes the layout for both outputs whatever is
+// asked for; y or codes alone without a residual would gain from the other one (16384
+// rows of 4096, y / codes: 512 x 1 56.8 / 70.0, 256 x 2 47.8 / 60.7).
 template <bool NORM, bool XF32, int RES>
 hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
   const int V = a.H / 8;
